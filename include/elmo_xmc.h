@@ -213,6 +213,53 @@ int elmo_xmc_kernel_timing_read(double* ms, int64_t* launches, double* labels);
 int elmo_kahan_update(uint16_t* w, uint16_t* c, const float* g, int64_t n, float lr, void* stream);
 
 /*
+ * ---- Language-model operators -----------------------------------------------------------------
+ * The softmax side of a large head and what a model in front of it trains and serves with. Same
+ * conventions as above (device pointers, caller-owned workspaces, asynchronous, host validation);
+ * pointers here need the alignment of their elements unless an entry says more.
+ * Element types: */
+enum { ELMO_T_F32 = 0, ELMO_T_BF16 = 1, ELMO_T_F16 = 2 };
+
+/*
+ * Log probabilities of given tokens under rows of logits, with the entropy of each row and its top
+ * alternatives. All arithmetic in binary32.
+ *
+ *   Z        [N, V] logits of element type `ztype`, row n at Z + n ldz elements (ldz >= V), elements
+ *            of a row adjacent; any row alignment. -inf is a masked token.
+ *   ids      [N, M] int32, 0 <= M <= ELMO_MAX_GIVEN (NULL if M = 0). A negative id stands for no
+ *            token: its log probability is 0. An id >= V gives NaN.
+ *   k        alternatives per row, 0 <= k <= min(ELMO_MAX_TOPK, V).
+ *   logp     [N, M] FP32: (z[id] - row_max) - log_sum.
+ *   entropy  [N] FP32: -sum_v p_v log p_v.
+ *   row_max, log_sum  [N] FP32: m = max_v z_v and log sum_v e^(z_v - m), whose sum is the row's log
+ *            partition; apart they keep log_sum's digits at logits of any magnitude.
+ *   top_idx, top_logp [N, k] int32 and FP32: tokens by (logit desc, token asc), NaN logits last, and
+ *            their log probabilities (both NULL if k = 0).
+ * A row of nothing but -inf has row_max -inf, log_sum 0, entropy 0 and every log probability -inf. A
+ * NaN or +inf logit makes log_sum, entropy and every log probability of its row NaN (row_max skips
+ * NaN). Results do not depend on the launch and repeat bit for bit on one device.
+ * 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done).
+ */
+#define ELMO_MAX_GIVEN 64
+size_t elmo_logprobs_workspace_bytes(int64_t N, int64_t V, int k);
+int elmo_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M, int k,
+                  float* logp, float* entropy, float* row_max, float* log_sum, int32_t* top_idx, float* top_logp,
+                  void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * The gradient of the above with respect to the logits, from the upstream gradients dlogp [N, M]
+ * (NULL if M = 0), dentropy [N] (nullable) and dlse [N] (nullable: of row_max + log_sum):
+ *   dZ[n, v] = p_v (dlse - sum_j dlogp_j - dentropy (log p_v + H)) + sum_{j : ids_j = v} dlogp_j.
+ * row_max, log_sum and entropy are elmo_logprobs' outputs for the same Z. A token given more than
+ * once receives the sum of its gradients, a negative id none; an id >= V makes its row NaN, a row
+ * of nothing but -inf has gradient 0.
+ *   dZ       [N, V] of type `ztype`, row n at dZ + n ldd. dZ = Z with ldd = ldz is allowed (in
+ *            place); no other overlap is. No workspace.
+ */
+int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M,
+                           const float* row_max, const float* log_sum, const float* entropy, const float* dlogp,
+                           const float* dentropy, const float* dlse, void* dZ, int64_t ldd, void* stream);
+
+/*
  * Test hook: the device codec, stochastic rounding and RNG applied elementwise to n elements.
  *   op 0  BF16 RNE encode:      in0 float[n]            -> out uint16[n]
  *   op 1  E4M3 RNE-sat encode:  in0 float[n]            -> out uint8[n]

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -80,6 +81,11 @@ def lib():
         L.elmo_numerics_probe.argtypes = [i32, P, P, P, i64, u64, u64, P]
         L.elmo_numerics_probe.restype = i32
         L.elmo_kahan_update.argtypes = [P, P, P, i64, f32, P]; L.elmo_kahan_update.restype = i32
+        L.elmo_logprobs_workspace_bytes.argtypes = [i64, i64, i32]; L.elmo_logprobs_workspace_bytes.restype = sz
+        L.elmo_logprobs.argtypes = [P, i32, i64, i64, i64, P, i32, i32, P, P, P, P, P, P, P, sz, P]
+        L.elmo_logprobs.restype = i32
+        L.elmo_logprobs_backward.argtypes = [P, i32, i64, i64, i64, P, i32, P, P, P, P, P, P, P, i64, P]
+        L.elmo_logprobs_backward.restype = i32
         _lib = L
     return _lib
 
@@ -260,6 +266,103 @@ def kahan_update(w, c, g, lr):
     assert c.numel() == n and g.numel() == n
     _chk("elmo_kahan_update", lib().elmo_kahan_update(_ptr(w), _ptr(c), _ptr(g), n, float(lr), _stream()))
     return w, c
+
+
+# ---- language-model operators --------------------------------------------------------------------
+_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # ELMO_T_F32, ELMO_T_BF16, ELMO_T_F16
+
+
+def _etype(t: torch.Tensor) -> int:
+    e = _TYPES.get(t.dtype)
+    if e is None:
+        raise TypeError(f"unsupported element type {t.dtype}: float32, bfloat16 or float16")
+    return e
+
+
+def _rows(name, t: torch.Tensor):
+    """(rows, columns, row pitch) of a matrix on the current GPU whose rows have adjacent elements."""
+    if t.dim() != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a 2-D CUDA tensor")
+    n, v = t.shape
+    if v > 1 and t.stride(1) != 1:
+        raise ValueError(f"the elements of a row of {name} must be adjacent (stride 1)")
+    return n, v, (t.stride(0) if n > 1 else v)
+
+
+def _like(name, t, shape, dtype, device):
+    """t as an argument of exactly this shape and type (contiguous, on `device`), or None."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+class LogProbs(NamedTuple):
+    """What logprobs() returns; row_max + log_sum is each row's log partition."""
+    logp: torch.Tensor                   # [N, M]
+    entropy: torch.Tensor                # [N]
+    row_max: torch.Tensor                # [N]
+    log_sum: torch.Tensor                # [N]
+    top_idx: Optional[torch.Tensor]      # [N, k] int32
+    top_logp: Optional[torch.Tensor]     # [N, k]
+
+
+def logprobs(Z, ids=None, k=0, workspace=None) -> LogProbs:
+    """Log probabilities of the tokens `ids` [N, M] int32 under the logit rows Z [N, V] (float32,
+    bfloat16 or float16, any row pitch), each row's entropy, and its k best alternatives (by logit,
+    then by token) with their log probabilities. Negative ids stand for no token (log probability
+    0); -inf logits are masked tokens. See elmo_logprobs in elmo_xmc.h."""
+    e = _etype(Z)
+    N, V, ld = _rows("Z", Z)
+    dev = Z.device
+    M = 0 if ids is None else ids.shape[-1]
+    _like("ids", ids, (N, M), torch.int32, dev)
+    if not 0 <= k <= min(64, V) or M > 64 or V < 1:
+        raise ElmoError("elmo_logprobs", -2)
+    logp = torch.empty((N, M), dtype=torch.float32, device=dev)
+    stats = torch.empty((3, N), dtype=torch.float32, device=dev)
+    entropy, row_max, log_sum = stats.unbind(0)
+    idx = torch.empty((N, k), dtype=torch.int32, device=dev) if k else None
+    top = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
+    if N:
+        need = lib().elmo_logprobs_workspace_bytes(N, V, k)
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        _chk("elmo_logprobs", lib().elmo_logprobs(
+            Z.data_ptr(), e, N, V, ld, _ptr(ids) if M else None, M, k, _ptr(logp) if M else None, entropy.data_ptr(),
+            row_max.data_ptr(), log_sum.data_ptr(), _ptr(idx), _ptr(top), workspace.data_ptr(), workspace.numel(),
+            _stream()))
+    return LogProbs(logp, entropy, row_max, log_sum, idx, top)
+
+
+def logprobs_backward(Z, ids, stats: LogProbs, dlogp, dentropy=None, dlse=None, out=None):
+    """The gradient dZ [N, V] (Z's type) of logprobs(Z, ids) for the upstream gradients dlogp [N, M],
+    dentropy [N] and dlse [N] (of the log partition), from the forward's result `stats`. out = Z
+    writes the gradient over the logits. See elmo_logprobs_backward in elmo_xmc.h."""
+    e = _etype(Z)
+    N, V, ld = _rows("Z", Z)
+    dev = Z.device
+    M = 0 if ids is None else ids.shape[-1]
+    _like("ids", ids, (N, M), torch.int32, dev)
+    if M and dlogp is None:
+        raise ValueError("dlogp is missing")
+    _like("dlogp", dlogp, (N, M), torch.float32, dev)
+    _like("dentropy", dentropy, (N,), torch.float32, dev)
+    _like("dlse", dlse, (N,), torch.float32, dev)
+    for name in ("entropy", "row_max", "log_sum"):
+        _like(name, getattr(stats, name), (N,), torch.float32, dev)
+    if out is None:
+        out = torch.empty((N, V), dtype=Z.dtype, device=dev)
+    elif out.shape != Z.shape or out.dtype != Z.dtype or out.device != dev:
+        raise ValueError("out must have Z's shape, type and device")
+    ldd = _rows("out", out)[2]
+    if N:
+        _chk("elmo_logprobs_backward", lib().elmo_logprobs_backward(
+            Z.data_ptr(), e, N, V, ld, _ptr(ids) if M else None, M, stats.row_max.data_ptr(), stats.log_sum.data_ptr(),
+            stats.entropy.data_ptr(), _ptr(dlogp) if M else None, _ptr(dentropy), _ptr(dlse), out.data_ptr(), ldd,
+            _stream()))
+    return out
 
 
 def numerics_probe(op, in0=None, in1=None, n=None, seed=0, step=0, idx0=0):

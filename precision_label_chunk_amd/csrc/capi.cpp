@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 
 #include "step_kernels.hpp"
 
@@ -24,6 +25,18 @@ int check_shapes(int B, int D, int64_t L) {
   if (B < 1 || B > ELMO_MAX_B) return ELMO_ESHAPE;
   if (D < 64 || D > ELMO_MAX_D || D % 64 != 0) return ELMO_ESHAPE;
   if (L < 1 || L >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  return ELMO_OK;
+}
+
+// element type and alignment of the language-model operators' tensors
+bool known_type(int t) { return t == ELMO_T_F32 || t == ELMO_T_BF16 || t == ELMO_T_F16; }
+bool aligned_to(const void* p, size_t n) { return (uintptr_t)p % n == 0; }
+size_t type_bytes(int t) { return t == ELMO_T_F32 ? 4 : 2; }
+
+int check_rows(int ztype, int64_t N, int64_t V, int64_t ld, int M) {
+  if (!known_type(ztype)) return ELMO_EDTYPE;
+  if (N < 0 || N >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31) || ld < V) return ELMO_ESHAPE;
+  if (M < 0 || M > ELMO_MAX_GIVEN) return ELMO_ESHAPE;
   return ELMO_OK;
 }
 
@@ -194,6 +207,47 @@ int elmo_kahan_update(uint16_t* w, uint16_t* c, const float* g, int64_t n, float
   if (n == 0) return ELMO_OK;
   if (!w || !c || !g || (uintptr_t)w % 2 || (uintptr_t)c % 2 || (uintptr_t)g % 4) return ELMO_EINVAL;
   return elmo::run_kahan_update(w, c, g, n, lr, (hipStream_t)stream);
+}
+
+size_t elmo_logprobs_workspace_bytes(int64_t N, int64_t V, int k) {
+  if (check_rows(ELMO_T_F32, N, V, V, 0) != ELMO_OK || N < 1 || k < 0 || k > ELMO_MAX_TOPK || k > V) return 0;
+  return elmo::logprobs_layout(N, V, k).total;
+}
+
+int elmo_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M, int k,
+                  float* logp, float* entropy, float* row_max, float* log_sum, int32_t* top_idx, float* top_logp,
+                  void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_rows(ztype, N, V, ldz, M);
+  if (rc != ELMO_OK) return rc;
+  if (k < 0 || k > ELMO_MAX_TOPK || k > V) return ELMO_ESHAPE;
+  if (N == 0) return ELMO_OK;
+  if (!Z || !entropy || !row_max || !log_sum || (M > 0 && (!ids || !logp)) || (k > 0 && (!top_idx || !top_logp)))
+    return ELMO_EINVAL;
+  if (!aligned_to(Z, type_bytes(ztype))) return ELMO_EINVAL;
+  for (const void* p : {(const void*)ids, (const void*)logp, (const void*)entropy, (const void*)row_max,
+                        (const void*)log_sum, (const void*)top_idx, (const void*)top_logp})
+    if (!aligned_to(p, 4)) return ELMO_EINVAL;
+  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
+  const elmo::LogprobLayout s = elmo::logprobs_layout(N, V, k);
+  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  return elmo::run_logprobs(Z, ztype, N, V, ldz, ids, M, k, logp, entropy, row_max, log_sum, top_idx, top_logp, s,
+                            workspace, (hipStream_t)stream);
+}
+
+int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M,
+                           const float* row_max, const float* log_sum, const float* entropy, const float* dlogp,
+                           const float* dentropy, const float* dlse, void* dZ, int64_t ldd, void* stream) {
+  const int rc = check_rows(ztype, N, V, ldz, M);
+  if (rc != ELMO_OK) return rc;
+  if (ldd < V || (dZ == Z && ldd != ldz)) return ELMO_ESHAPE;
+  if (N == 0) return ELMO_OK;
+  if (!Z || !dZ || !row_max || !log_sum || !entropy || (M > 0 && (!ids || !dlogp))) return ELMO_EINVAL;
+  if (!aligned_to(Z, type_bytes(ztype)) || !aligned_to(dZ, type_bytes(ztype))) return ELMO_EINVAL;
+  for (const void* p : {(const void*)ids, (const void*)row_max, (const void*)log_sum, (const void*)entropy,
+                        (const void*)dlogp, (const void*)dentropy, (const void*)dlse})
+    if (!aligned_to(p, 4)) return ELMO_EINVAL;
+  return elmo::run_logprobs_grad(Z, ztype, N, V, ldz, ids, M, row_max, log_sum, entropy, dlogp, dentropy, dlse, dZ,
+                                 ldd, (hipStream_t)stream);
 }
 
 int elmo_numerics_probe(int op, const void* in0, const void* in1, void* out, int64_t n, uint64_t seed,

@@ -1,0 +1,462 @@
+// Log probabilities of given tokens under a row of logits, with the row's entropy and its top
+// alternatives, and the gradient of the three with respect to the logits.
+//
+//   m = max_v z_v,  s = sum_v e^(z_v - m),  logp_j = (z_(id_j) - m) - log s,
+//   H = -sum_v p_v log p_v = log s - (1/s) sum_v e^(z_v - m) (z_v - m).
+//
+// One pass over the logits: every lane carries the running maximum of its own elements and the two
+// sums relative to it, rescaled when the maximum rises (in base 2: y = (z - m) log2 e), so that the
+// row is read once and never stored. The maximum and log s stay apart (their sum is the row's log
+// partition): at logits of large magnitude, such as a row masked with its type's lowest value, the
+// rounded sum would lose log s.
+//
+// A block of 4 waves takes a contiguous segment of a row, each wave a contiguous quarter; short
+// batches split every row over several blocks whose (m, s, t) and candidate keys a second kernel
+// joins in a fixed order.
+#include "elem_types.hpp"
+#include "step_kernels.hpp"
+#include "wave_top.hpp"
+
+namespace elmo {
+
+constexpr int LP_WAVES = 4, LP_THREADS = 64 * LP_WAVES;
+constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
+
+// a partial softmax: m the maximum, s = sum 2^y, t = sum 2^y y with y = (z - m) log2 e
+struct SoftPart { float m, s, t; };
+
+// the reference that exponents are taken against: the maximum, or 0 while nothing is above -inf
+__device__ __forceinline__ float soft_ref(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// moves a partial sum to the reference of the larger maximum mn
+__device__ __forceinline__ void soft_move(SoftPart& a, float mn) {
+  // d is -inf for an empty part; kept finite, 2^d is 0 and d s is 0
+  const float d = __builtin_fmaxf((a.m - soft_ref(mn)) * LOG2E, -1e30f);
+  const float r = __builtin_amdgcn_exp2f(d);
+  a.t = r * __builtin_fmaf(d, a.s, a.t);
+  a.s *= r;
+  a.m = mn;
+}
+
+// one element against the reference `ref`; a logit of -inf adds nothing to either sum
+__device__ __forceinline__ void soft_add(SoftPart& a, float z, float ref) {
+  const float y = (z - ref) * LOG2E;
+  const float e = __builtin_amdgcn_exp2f(y);
+  a.s += e;
+  a.t = __builtin_fmaf(e, __builtin_fmaxf(y, -200.0f), a.t);   // 2^-200 is already 0 in binary32
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v = __builtin_fmaxf(v, __shfl_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
+  return v;
+}
+__device__ __forceinline__ void wave_join(SoftPart& a) {
+  soft_move(a, wave_max(a.m));
+  a.s = wave_sum(a.s);
+  a.t = wave_sum(a.t);
+}
+
+struct LogprobArgs {
+  const void* Z; int64_t N, V, ldz;
+  const int32_t* ids; int M, k;
+  float *logp, *entropy, *row_max, *log_sum;
+  int32_t* top_idx; float* top_logp;
+  int segs;                                     // blocks per row
+  SoftPart* part; uint64_t* keys;               // [N][segs], [N][segs][k] (segs > 1)
+};
+
+// what the finished sums say of a row: log s and the entropy, both 0 where the mask leaves nothing
+struct RowStats { float m, logs, H; bool empty; };
+__device__ __forceinline__ RowStats row_stats(const SoftPart& a) {
+  RowStats r;
+  r.m = a.m;
+  r.empty = a.m == -__builtin_inff() && a.s == 0.0f;
+  r.logs = r.empty ? 0.0f : logf(a.s);
+  r.H = r.empty ? 0.0f : __builtin_fmaf(-LN2, a.t / a.s, r.logs);
+  return r;
+}
+__device__ __forceinline__ float row_logp(const RowStats& r, float z) {
+  return r.empty ? -__builtin_inff() : (z - r.m) - r.logs;
+}
+
+// the outputs of row n, by one block, from its statistics and its k best keys in LDS
+template <typename E>
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const SoftPart& sum, const uint64_t* keys) {
+  const RowStats r = row_stats(sum);
+  const int tid = (int)threadIdx.x;
+  if (tid == 0) {
+    a.entropy[n] = r.H;
+    a.row_max[n] = r.m;
+    a.log_sum[n] = r.logs;
+  }
+  const typename E::raw* z = (const typename E::raw*)a.Z + n * a.ldz;
+  for (int j = tid; j < a.M; j += (int)blockDim.x) {
+    const int32_t id = a.ids[n * a.M + j];
+    float lp = 0.0f;                                        // a negative id stands for no token
+    if (id >= 0) lp = id < a.V ? row_logp(r, E::load(z + id)) : __builtin_nanf("");
+    a.logp[n * a.M + j] = lp;
+  }
+  if (tid < a.k) {                                          // k <= 64: the first wave ranks the keys
+    const uint64_t q = keys[tid];
+    int rank = 0;
+    for (int i = 0; i < a.k; ++i) rank += keys[i] > q;
+    const uint32_t o = (uint32_t)(q >> 32);
+    a.top_idx[n * a.k + rank] = (int32_t)~(uint32_t)q;
+    a.top_logp[n * a.k + rank] = o == 0 ? __builtin_nanf("") : row_logp(r, value_of(o));
+  }
+}
+
+// joins the waves of a block: the sums into every thread, the keys into buf[0]'s first k slots
+__device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, SoftPart* sums, int* cnts,
+                                           uint64_t (*buf)[WaveTop::CAP]) {
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  wave_join(p);
+  if (top.k) top.cut();
+  if (lane == 0) { sums[wave] = p; cnts[wave] = top.cnt; }
+  __syncthreads();
+  SoftPart q = sums[0];
+#pragma unroll
+  for (int w = 1; w < LP_WAVES; ++w) q.m = __builtin_fmaxf(q.m, sums[w].m);
+  const float m = q.m;
+  q.m = sums[0].m;
+  soft_move(q, m);
+#pragma unroll
+  for (int w = 1; w < LP_WAVES; ++w) {
+    SoftPart o = sums[w];
+    soft_move(o, m);
+    q.s += o.s;
+    q.t += o.t;
+  }
+  p = q;
+  if (top.k) {
+    if (wave == 0) {                                        // at most 64 keys of each of the four waves
+      for (int w = 1; w < LP_WAVES; ++w) {
+        const int c = cnts[w];
+        if (lane < c) top.buf[top.cnt + lane] = buf[w][lane];
+        top.cnt += c;
+      }
+      top.cut();
+      if (lane == 0) cnts[0] = top.cnt;
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E, bool TOP>
+__global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
+  constexpr int VEC = E::VEC, U = 4;                        // U vectors of 16 bytes per lane in flight
+  __shared__ uint64_t buf[TOP ? LP_WAVES : 1][WaveTop::CAP];
+  __shared__ SoftPart sums[LP_WAVES];
+  __shared__ int cnts[LP_WAVES];
+  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
+  const int64_t n = blockIdx.x / a.segs;
+  const int seg = (int)(blockIdx.x % a.segs);
+  const typename E::raw* z = (const typename E::raw*)a.Z + n * a.ldz;
+  // the row as up to VEC - 1 single elements, nv aligned vectors, up to VEC - 1 single elements
+  const int mis = (int)(((uintptr_t)z & 15u) / sizeof(typename E::raw));
+  int head = mis ? VEC - mis : 0;
+  if (head > a.V) head = (int)a.V;
+  const int nv = (int)((a.V - head) / VEC);
+  const int tail = (int)(a.V - head - (int64_t)nv * VEC);
+  const i32x4_t* zv = (const i32x4_t*)(z + head);
+  // this wave's vectors [v0, v1): whole steps of 64 vectors
+  const int parts = a.segs * LP_WAVES, me = seg * LP_WAVES + wave;
+  const int steps = (nv + 63) / 64, per = steps / parts, more = steps % parts;
+  const int s0 = me * per + (me < more ? me : more), s1 = s0 + per + (me < more ? 1 : 0);
+  const int v0 = s0 * 64, v1 = s1 * 64 < nv ? s1 * 64 : nv;
+
+  const float ninf = -__builtin_inff();
+  SoftPart p{ninf, 0.0f, 0.0f};
+  WaveTop top;
+  top.init(buf[TOP ? wave : 0], TOP ? a.k : 0);
+
+  // single elements: lane l takes element e0 + l of c
+  auto singles = [&](int64_t e0, int c) __attribute__((always_inline)) {
+    const bool in = lane < c;
+    const float v = in ? E::load(z + e0 + lane) : ninf;
+    soft_move(p, __builtin_fmaxf(p.m, v));
+    soft_add(p, v, soft_ref(p.m));
+    if constexpr (TOP) {
+      top.begin_step();
+      top.push(in && top.wants(v), key_of(v, (uint32_t)(e0 + lane)));
+    }
+  };
+  if (me == 0 && head) singles(0, head);
+
+  auto chunk = [&](int v, auto whole) __attribute__((always_inline)) {
+    i32x4_t r[U];
+    float f[U][VEC], mx[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = v + 64 * u + lane;
+      r[u] = i32x4_t{0, 0, 0, 0};
+      if (whole || i < v1) r[u] = __builtin_nontemporal_load(zv + i);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = v + 64 * u + lane;
+      E::widen(r[u], f[u]);
+      if (!whole && i >= v1) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f[u][e] = ninf;
+      }
+      mx[u] = f[u][0];
+#pragma unroll
+      for (int e = 1; e < VEC; ++e) mx[u] = __builtin_fmaxf(mx[u], f[u][e]);
+    }
+    float mn = p.m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = __builtin_fmaxf(mn, mx[u]);
+    soft_move(p, mn);
+    const float ref = soft_ref(mn);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) soft_add(p, f[u][e], ref);
+    if constexpr (TOP) {
+      static_for<0, U>([&](auto u) __attribute__((always_inline)) {                        // (register arrays: expanded at compile time)
+        const int i = v + 64 * u + lane;
+        const bool in = whole || i < v1;
+        top.begin_step();
+        if (__ballot(in && top.wants(mx[u]))) top.push_all(in, f[u], (uint32_t)(head + VEC * i));
+      });
+    }
+  };
+  int v = v0;
+  for (; v + 64 * U <= v1; v += 64 * U) chunk(v, std::true_type{});
+  if (v < v1) chunk(v, std::false_type{});
+  if (me == parts - 1 && tail) singles(a.V - tail, tail);
+
+  block_join(p, top, sums, cnts, buf);
+  if (a.segs == 1) {
+    write_row<E>(a, n, p, buf[0]);
+  } else {
+    const int64_t at = n * a.segs + seg;
+    if (threadIdx.x == 0) a.part[at] = p;
+    if (TOP && (int)threadIdx.x < a.k)
+      a.keys[at * a.k + threadIdx.x] = (int)threadIdx.x < cnts[0] ? buf[0][threadIdx.x] : 0;
+  }
+}
+
+// joins the blocks of a row: part i by thread i % 256, then as the waves of a block
+template <typename E, bool TOP>
+__global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
+  __shared__ uint64_t buf[TOP ? LP_WAVES : 1][WaveTop::CAP];
+  __shared__ SoftPart sums[LP_WAVES];
+  __shared__ int cnts[LP_WAVES];
+  const int64_t n = blockIdx.x;
+  SoftPart p{-__builtin_inff(), 0.0f, 0.0f};
+  WaveTop top;
+  top.init(buf[TOP ? threadIdx.x >> 6 : 0], TOP ? a.k : 0);
+  for (int i = (int)threadIdx.x; i < a.segs; i += LP_THREADS) {
+    SoftPart o = a.part[n * a.segs + i];
+    const float m = __builtin_fmaxf(p.m, o.m);
+    soft_move(p, m);
+    soft_move(o, m);
+    p.s += o.s;
+    p.t += o.t;
+  }
+  if constexpr (TOP) {
+    const int total = a.segs * a.k;
+    const uint64_t* keys = a.keys + n * total;
+    top.tie = true;                                         // (keys come in no order of their indices)
+    for (int i = (int)(threadIdx.x & ~63u); i < total; i += LP_THREADS) {
+      const int at = i + (int)(threadIdx.x & 63);
+      const uint64_t q = at < total ? keys[at] : 0;         // (0: a segment of fewer than k elements)
+      top.push(q != 0 && top.wants(value_of((uint32_t)(q >> 32))), q);
+    }
+  }
+  block_join(p, top, sums, cnts, buf);
+  write_row<E>(a, n, p, buf[0]);
+}
+
+// ---- gradient ------------------------------------------------------------------------------------
+// With upstream gradients g_j of logp_j, gH of H and gL of log s + m (the log partition):
+//   dz_v = p_v (gL - sum_j g_j - gH (log p_v + H)) + sum_{j: id_j = v} g_j,
+// p_v = 2^((z_v - m) log2 e - log2 s). Elementwise, bound by HBM (the logits read, the gradient
+// written). The few elements that a given token names are computed before the block's pass over its
+// segment and written after it, so that dZ may be the logits' own memory; a token given more than
+// once is summed in the order of its places, by the thread of its first.
+struct LogprobGradArgs {
+  const void* Z; int64_t N, V, ldz;
+  const int32_t* ids; int M;
+  const float *row_max, *log_sum, *entropy, *dlogp, *dentropy, *dlse;
+  void* dZ; int64_t ldd;
+  int segs;
+};
+
+template <typename E, bool HAS_H>
+__global__ __launch_bounds__(256) void k_logprobs_grad(LogprobGradArgs a) {
+  constexpr int VEC = E::VEC, U = 2;
+  typedef typename E::raw raw;
+  const int tid = (int)threadIdx.x;
+  const int64_t n = blockIdx.x / a.segs;
+  const int seg = (int)(blockIdx.x % a.segs);
+  const raw* z = (const raw*)a.Z + n * a.ldz;
+  raw* d = (raw*)a.dZ + n * a.ldd;
+  const float m = a.row_max[n], logs = a.log_sum[n], H = a.entropy[n];
+  const bool empty = m == -__builtin_inff() && logs == 0.0f;   // the mask leaves nothing: the gradient is 0
+  float c = a.dlse ? a.dlse[n] : 0.0f;
+  const float gH = HAS_H ? a.dentropy[n] : 0.0f;
+  for (int j = 0; j < a.M; ++j) {
+    const int32_t id = a.ids[n * a.M + j];
+    if (id >= 0) c -= id < a.V ? a.dlogp[n * a.M + j] : __builtin_nanf("");
+  }
+  const float ref = soft_ref(m), l2 = logs * LOG2E, cH = __builtin_fmaf(-gH, H, c), gL = -gH * LN2;
+  auto grad = [&](float zv) {
+    const float y = __builtin_fmaf(zv - ref, LOG2E, -l2);      // log2 p
+    const float p = __builtin_amdgcn_exp2f(y);
+    if (!HAS_H) return empty ? 0.0f : p * c;
+    return empty ? 0.0f : p * __builtin_fmaf(gL, __builtin_fmaxf(y, -200.0f), cH);
+  };
+
+  const int mis = (int)(((uintptr_t)z & 15u) / sizeof(raw));
+  const bool vec = (((uintptr_t)z ^ (uintptr_t)d) & 15u) == 0;
+  int head = mis ? VEC - mis : 0;
+  if (head > a.V || !vec) head = (int)a.V;                     // rows of different alignment: element by element
+  const int nv = (int)((a.V - head) / VEC);
+  const int tail = (int)(a.V - head - (int64_t)nv * VEC);
+  const int per = nv / a.segs, more = nv % a.segs;
+  const int v0 = seg * per + (seg < more ? seg : more), v1 = v0 + per + (seg < more ? 1 : 0);
+  // the elements this block writes: [e0, e1), the single ones at the row's ends by its end blocks
+  int64_t e0 = head + (int64_t)v0 * VEC, e1 = head + (int64_t)v1 * VEC, h0 = 0, h1 = 0, t0 = 0, t1 = 0;
+  if (vec) {
+    if (seg == 0) { h1 = head; e0 = 0; }
+    if (seg == a.segs - 1) { t0 = a.V - tail; t1 = a.V; e1 = a.V; }
+  } else {
+    const int64_t q = a.V / a.segs, r = a.V % a.segs;
+    h0 = e0 = seg * q + (seg < r ? seg : r);
+    h1 = e1 = e0 + q + (seg < r ? 1 : 0);
+  }
+
+  float mine = 0.0f;
+  int64_t at = -1;
+  if (tid < a.M) {
+    const int32_t id = a.ids[n * a.M + tid];
+    if (id >= e0 && id < e1) {
+      at = id;
+      for (int j = 0; j < a.M; ++j) {
+        if (a.ids[n * a.M + j] != id) continue;
+        if (j < tid) at = -1;
+        mine += a.dlogp[n * a.M + j];
+      }
+      mine = empty ? 0.0f : mine + grad(E::load(z + id));
+    }
+  }
+  __syncthreads();
+
+  const i32x4_t* zv = (const i32x4_t*)(z + head);
+  i32x4_t* dv = (i32x4_t*)(d + head);
+  auto one = [&](i32x4_t r, int i) {
+    float f[VEC];
+    E::widen(r, f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = grad(f[e]);
+    __builtin_nontemporal_store(E::narrow(f), dv + i);
+  };
+  int i = v0 + tid;
+  for (; i + 256 * (U - 1) < v1; i += 256 * U) {
+    i32x4_t r[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = __builtin_nontemporal_load(zv + i + 256 * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u) one(r[u], i + 256 * u);
+  }
+  for (; i < v1; i += 256) one(__builtin_nontemporal_load(zv + i), i);
+  for (int64_t e = h0 + tid; e < h1; e += 256) E::store(d + e, grad(E::load(z + e)));
+  for (int64_t e = t0 + tid; e < t1; e += 256) E::store(d + e, grad(E::load(z + e)));
+  if (a.M) {
+    __syncthreads();
+    if (at >= 0) E::store(d + at, mine);
+  }
+}
+
+// ---- launchers -------------------------------------------------------------------------------------
+// Blocks per row: enough that the device has several waves of blocks, none below 4096 elements.
+static int row_segments(int64_t N, int64_t V, int target) {
+  int64_t s = (target + N - 1) / N;
+  const int64_t most = V / 4096 > 0 ? V / 4096 : 1;
+  if (s > most) s = most;
+  return (int)(s < 1 ? 1 : s);
+}
+
+LogprobLayout logprobs_layout(int64_t N, int64_t V, int k) {
+  LogprobLayout s{};
+  s.segs = row_segments(N, V, 8 * device_cus());
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t o = at; at += (bytes + 255) & ~(size_t)255; return o; };
+  if (s.segs > 1) {
+    s.part = take((size_t)N * s.segs * sizeof(SoftPart));
+    s.keys = take((size_t)N * s.segs * k * 8);
+  }
+  s.total = at ? at : 256;
+  return s;
+}
+
+template <typename E>
+static int launch_logprobs(const LogprobArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.N * a.segs)), block(LP_THREADS);
+  if (a.k)
+    hipLaunchKernelGGL((k_logprobs<E, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_logprobs<E, false>), grid, block, 0, st, a);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  if (a.segs > 1) {
+    if (a.k)
+      hipLaunchKernelGGL((k_logprobs_join<E, true>), dim3((unsigned)a.N), block, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_logprobs_join<E, false>), dim3((unsigned)a.N), block, 0, st, a);
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  }
+  return ELMO_OK_;
+}
+
+int run_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M, int k,
+                 float* logp, float* entropy, float* row_max, float* log_sum, int32_t* top_idx, float* top_logp,
+                 const LogprobLayout& s, void* workspace, hipStream_t st) {
+  LogprobArgs a{};
+  a.Z = Z; a.N = N; a.V = V; a.ldz = ldz; a.ids = ids; a.M = M; a.k = k;
+  a.logp = logp; a.entropy = entropy; a.row_max = row_max; a.log_sum = log_sum;
+  a.top_idx = top_idx; a.top_logp = top_logp;
+  a.segs = s.segs;
+  a.part = (SoftPart*)((uint8_t*)workspace + s.part);
+  a.keys = (uint64_t*)((uint8_t*)workspace + s.keys);
+  switch (ztype) {
+    case T_F32_: return launch_logprobs<ElemF32>(a, st);
+    case T_BF16_: return launch_logprobs<ElemBF16>(a, st);
+    default: return launch_logprobs<ElemF16>(a, st);
+  }
+}
+
+template <typename E>
+static int launch_grad(const LogprobGradArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.N * a.segs)), block(256);
+  if (a.dentropy)
+    hipLaunchKernelGGL((k_logprobs_grad<E, true>), grid, block, 0, st, a);
+  else
+    hipLaunchKernelGGL((k_logprobs_grad<E, false>), grid, block, 0, st, a);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+int run_logprobs_grad(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M,
+                      const float* row_max, const float* log_sum, const float* entropy, const float* dlogp,
+                      const float* dentropy, const float* dlse, void* dZ, int64_t ldd, hipStream_t st) {
+  LogprobGradArgs a{};
+  a.Z = Z; a.N = N; a.V = V; a.ldz = ldz; a.ids = ids; a.M = M;
+  a.row_max = row_max; a.log_sum = log_sum; a.entropy = entropy;
+  a.dlogp = dlogp; a.dentropy = dentropy; a.dlse = dlse; a.dZ = dZ; a.ldd = ldd;
+  a.segs = row_segments(N, V, 16 * device_cus());
+  switch (ztype) {
+    case T_F32_: return launch_grad<ElemF32>(a, st);
+    case T_BF16_: return launch_grad<ElemBF16>(a, st);
+    default: return launch_grad<ElemF16>(a, st);
+  }
+}
+
+}  // namespace elmo

@@ -101,6 +101,19 @@ int run_topk(const void* W, int wdtype, int64_t L, int D, const void* X, int N, 
 // Kahan-compensated BF16 update of encoder parameters (elementwise)
 int run_kahan_update(uint16_t* w, uint16_t* c, const float* g, int64_t n, float lr, hipStream_t st);
 
+// element types of the language-model operators' tensors
+constexpr int T_F32_ = 0, T_BF16_ = 1, T_F16_ = 2;
+
+// log probabilities of given tokens with entropy and top alternatives, and their gradient
+struct LogprobLayout { int segs; size_t part, keys, total; };
+LogprobLayout logprobs_layout(int64_t N, int64_t V, int k);
+int run_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M, int k,
+                 float* logp, float* entropy, float* row_max, float* log_sum, int32_t* top_idx, float* top_logp,
+                 const LogprobLayout& s, void* workspace, hipStream_t st);
+int run_logprobs_grad(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M,
+                      const float* row_max, const float* log_sum, const float* entropy, const float* dlogp,
+                      const float* dentropy, const float* dlse, void* dZ, int64_t ldd, hipStream_t st);
+
 // this device's copy of the static scratch array of the allocation-free step (noalloc.hip): its
 // device address, looked up on the first call on the current device
 int noalloc_scratch(void** out);

@@ -138,3 +138,39 @@ def test_two_kernel_step_validates_like_the_step(L):
     assert f(null, 0, 1000, 100, null, 4, null, null, 0, 0.1, 0, 0, 128, null, null, null, 0, null) == -2
     assert f(p, 0, 1000, 768, p, 4, p, p, 1, float("nan"), 0, 0, 128, p, null, p, 1 << 30, null) == -1
     assert f(p, 0, 1000, 768, p, 32, p, p, 1, 0.1, 0, 0, 128, p, null, p, 16, null) == -4
+
+
+def test_logprobs_rejects_invalid_arguments(L):
+    p, q, w = ctypes.c_void_p(4096), ctypes.c_void_p(4097), 1 << 30
+    f = L.elmo_logprobs
+    ok = dict(Z=p, t=0, N=2, V=100, ld=100, ids=p, M=1, k=5, logp=p, H=p, m=p, s=p, ti=p, tl=p, ws=p, wb=w)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return f(a["Z"], a["t"], a["N"], a["V"], a["ld"], a["ids"], a["M"], a["k"], a["logp"], a["H"], a["m"], a["s"],
+                 a["ti"], a["tl"], a["ws"], a["wb"], None)
+    assert call(t=3) == -3
+    for bad in (dict(N=-1), dict(N=2**31), dict(V=0), dict(V=2**31), dict(ld=99), dict(M=65), dict(M=-1), dict(k=65),
+                dict(k=-1), dict(V=4, ld=4, k=5)):
+        assert call(**bad) == -2, bad
+    for bad in (dict(Z=None), dict(ids=None), dict(logp=None), dict(H=None), dict(m=None), dict(s=None), dict(ti=None),
+                dict(tl=None), dict(Z=q), dict(ids=ctypes.c_void_p(4098)), dict(tl=q)):
+        assert call(**bad) == -1, bad
+    for bad in (dict(ws=None), dict(ws=q), dict(wb=8)):
+        assert call(**bad) == -4, bad
+    assert call(N=0, Z=None) == 0
+    assert L.elmo_logprobs_workspace_bytes(2, 100, 101) == 0 and L.elmo_logprobs_workspace_bytes(0, 100, 1) == 0
+    assert L.elmo_logprobs_workspace_bytes(1, 1 << 20, 64) >= 64 * 8
+    g = L.elmo_logprobs_backward
+
+    def grad(**kw):
+        a = {**dict(Z=p, t=1, N=2, V=100, ld=100, ids=p, M=1, m=p, s=p, H=p, g=p, gH=None, gL=None,
+                    d=ctypes.c_void_p(8192), ldd=100), **kw}
+        return g(a["Z"], a["t"], a["N"], a["V"], a["ld"], a["ids"], a["M"], a["m"], a["s"], a["H"], a["g"], a["gH"],
+                 a["gL"], a["d"], a["ldd"], None)
+    assert grad(t=-1) == -3
+    assert grad(ldd=99) == -2 and grad(d=p, ldd=101) == -2 and grad(M=65) == -2
+    for bad in (dict(Z=None), dict(d=None), dict(m=None), dict(s=None), dict(H=None), dict(g=None), dict(ids=None),
+                dict(d=q), dict(gH=q), dict(gL=q)):
+        assert grad(**bad) == -1, bad
+    assert grad(N=0) == 0
