@@ -260,6 +260,31 @@ int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64
                            const float* dentropy, const float* dlse, void* dZ, int64_t ldd, void* stream);
 
 /*
+ * Products of a few feature rows with 4-bit weights with group scales, Y[n, j] = sum_k X[n, k] w[j, k]:
+ * the logits of a 4-bit head, or any layer, for the rows of a decode step. The weights are read once;
+ * features stay BF16 (elmo_xmc_logits casts them to E4M3 and reads D <= 1024), every product is exact
+ * and sums are binary32.
+ *   wdtype   ELMO_W_MXFP4: W holds L rows of 17 D / 32 bytes as described with the formats, D % 256 == 0,
+ *            8-byte aligned; group = 32, scales = zeros = NULL.
+ *            ELMO_W_INT4: W holds L rows of D/2 bytes, code c[2i] in the low nibble of byte i and
+ *            c[2i + 1] in the high one, 16-byte aligned; w = (c - z) s with, per group of `group` (32,
+ *            64 or 128, dividing D) features, s = scales[j, k / group] (BF16, [L, D / group]) and
+ *            z = zeros[j, k / group] (uint8, [L, D / group]; NULL: 8 everywhere).
+ *   X        [N, D] BF16, 1 <= N <= ELMO_MAX_MATVEC_ROWS (N = 0: nothing is done), row n at X + n ldx;
+ *            16-byte aligned rows (ldx % 8 == 0).
+ *   Y        [N, L] of element type `ytype` (rounded once from binary32), row n at Y + n ldy.
+ * 1 <= L < 2^31; D <= ELMO_MAX_MATVEC_D. An MXFP4 scale of 255 (NaN), a NaN weight scale or a NaN
+ * feature makes the results it enters NaN; so does an infinite feature (with integer codes even
+ * where the sum would be infinite). No workspace.
+ */
+enum { ELMO_W_INT4 = 3 };                 /* elmo_w4_matvec only */
+#define ELMO_MAX_MATVEC_ROWS 32
+#define ELMO_MAX_MATVEC_D 65536
+int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const uint16_t* scales,
+                   const uint8_t* zeros, const void* X, int N, int64_t ldx, void* Y, int ytype, int64_t ldy,
+                   void* stream);
+
+/*
  * Test hook: the device codec, stochastic rounding and RNG applied elementwise to n elements.
  *   op 0  BF16 RNE encode:      in0 float[n]            -> out uint16[n]
  *   op 1  E4M3 RNE-sat encode:  in0 float[n]            -> out uint8[n]

@@ -26,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libelmo_xmc.so")
 ELMO_W_BF16 = 0
 ELMO_W_E4M3 = 1
 ELMO_W_MXFP4 = 2
+ELMO_W_INT4 = 3          # w4_matvec only
 FLAG_LABEL_RANGE = 1
 FLAG_ROW_PTR = 2
 
@@ -86,6 +87,8 @@ def lib():
         L.elmo_logprobs.restype = i32
         L.elmo_logprobs_backward.argtypes = [P, i32, i64, i64, i64, P, i32, P, P, P, P, P, P, P, i64, P]
         L.elmo_logprobs_backward.restype = i32
+        L.elmo_w4_matvec.argtypes = [P, i32, i64, i32, i32, P, P, P, i32, i64, P, i32, i64, P]
+        L.elmo_w4_matvec.restype = i32
         _lib = L
     return _lib
 
@@ -362,6 +365,46 @@ def logprobs_backward(Z, ids, stats: LogProbs, dlogp, dentropy=None, dlse=None, 
             Z.data_ptr(), e, N, V, ld, _ptr(ids) if M else None, M, stats.row_max.data_ptr(), stats.log_sum.data_ptr(),
             stats.entropy.data_ptr(), _ptr(dlogp) if M else None, _ptr(dentropy), _ptr(dlse), out.data_ptr(), ldd,
             _stream()))
+    return out
+
+
+def w4_matvec(W, X, wfmt=ELMO_W_MXFP4, scales=None, zeros=None, out_dtype=torch.float32, out=None):
+    """Y [N, L] = X [N, D] W^T for up to 32 BF16 feature rows and 4-bit weights. MXFP4: W uint8 rows of
+    17 D / 32 bytes. ELMO_W_INT4: W uint8 [L, D / 2], scales bfloat16 [L, D / group] (group 32, 64 or
+    128, from the shapes), zeros uint8 of the same shape or None (8). See elmo_w4_matvec in elmo_xmc.h."""
+    if W.dtype != torch.uint8 or W.dim() != 2 or not W.is_cuda or not W.is_contiguous():
+        raise ValueError("W must be a contiguous 2-D uint8 CUDA tensor")
+    dev = W.device
+    L = W.shape[0]
+    if wfmt == ELMO_W_MXFP4:
+        if scales is not None or zeros is not None:
+            raise ValueError("MXFP4 rows hold their own scales")
+        D, group = W.shape[1] * 32 // 17, 32
+        if W.shape[1] * 32 % 17:
+            raise ValueError("MXFP4 rows are D/2 code bytes and D/32 scale bytes")
+    elif wfmt == ELMO_W_INT4:
+        D = W.shape[1] * 2
+        if scales is None or scales.dim() != 2 or scales.shape[1] < 1 or D % scales.shape[1]:
+            raise ValueError("scales must be [L, D / group]")
+        group = D // scales.shape[1]
+        _like("scales", scales, (L, D // group), torch.bfloat16, dev)
+        _like("zeros", zeros, (L, D // group), torch.uint8, dev)
+    else:
+        raise TypeError(f"{wfmt} is not a 4-bit weight format")
+    if X.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or X.device != dev:
+        raise ValueError("X must hold BF16 codes on W's device")
+    N, d, ldx = _rows("X", X)
+    if d != D:
+        raise ValueError(f"X has {d} features, W {D}")
+    if out is None:
+        out = torch.empty((N, L), dtype=out_dtype, device=dev)
+    elif tuple(out.shape) != (N, L) or out.device != dev:
+        raise ValueError("out must be [N, L] on W's device")
+    ldy = _rows("out", out)[2]
+    if N and L:
+        _chk("elmo_w4_matvec", lib().elmo_w4_matvec(
+            W.data_ptr(), wfmt, L, D, group, _ptr(scales), _ptr(zeros), X.data_ptr(), N, ldx, out.data_ptr(),
+            _etype(out), ldy, _stream()))
     return out
 
 

@@ -250,6 +250,23 @@ int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64
                                  ldd, (hipStream_t)stream);
 }
 
+int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const uint16_t* scales,
+                   const uint8_t* zeros, const void* X, int N, int64_t ldx, void* Y, int ytype, int64_t ldy,
+                   void* stream) {
+  if (wdtype != ELMO_W_MXFP4 && wdtype != ELMO_W_INT4) return ELMO_EDTYPE;
+  if (!known_type(ytype)) return ELMO_EDTYPE;
+  if (N < 0 || N > ELMO_MAX_MATVEC_ROWS || L < 1 || L >= (int64_t(1) << 31) || D < 1 || D > ELMO_MAX_MATVEC_D)
+    return ELMO_ESHAPE;
+  if (ldx < D || ldx % 8 != 0 || ldy < L) return ELMO_ESHAPE;
+  if (wdtype == ELMO_W_MXFP4 && (group != 32 || D % 256 != 0)) return ELMO_ESHAPE;
+  if (wdtype == ELMO_W_INT4 && ((group != 32 && group != 64 && group != 128) || D % group != 0)) return ELMO_ESHAPE;
+  if (N == 0) return ELMO_OK;
+  if (!W || !X || !Y || !aligned16(X) || !aligned_to(Y, type_bytes(ytype))) return ELMO_EINVAL;
+  if (wdtype == ELMO_W_MXFP4 && (scales || zeros || !aligned_to(W, 8))) return ELMO_EINVAL;
+  if (wdtype == ELMO_W_INT4 && (!scales || !aligned_to(scales, 2) || !aligned16(W))) return ELMO_EINVAL;
+  return elmo::run_w4_matvec(W, wdtype, L, D, group, scales, zeros, X, N, ldx, Y, ytype, ldy, (hipStream_t)stream);
+}
+
 int elmo_numerics_probe(int op, const void* in0, const void* in1, void* out, int64_t n, uint64_t seed,
                         uint64_t step, void* stream) {
   return elmo::run_numerics_probe(op, in0, in1, out, n, seed, step, (hipStream_t)stream);

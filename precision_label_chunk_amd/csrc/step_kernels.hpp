@@ -114,6 +114,11 @@ int run_logprobs_grad(const void* Z, int ztype, int64_t N, int64_t V, int64_t ld
                       const float* row_max, const float* log_sum, const float* entropy, const float* dlogp,
                       const float* dentropy, const float* dlse, void* dZ, int64_t ldd, hipStream_t st);
 
+// products of a few BF16 feature rows with 4-bit weights (MXFP4 rows, or integer codes with group scales)
+constexpr int W_INT4_ = 3;
+int run_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const uint16_t* scales, const uint8_t* zeros,
+                  const void* X, int N, int64_t ldx, void* Y, int ytype, int64_t ldy, hipStream_t st);
+
 // this device's copy of the static scratch array of the allocation-free step (noalloc.hip): its
 // device address, looked up on the first call on the current device
 int noalloc_scratch(void** out);

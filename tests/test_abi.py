@@ -174,3 +174,27 @@ def test_logprobs_rejects_invalid_arguments(L):
                 dict(d=q), dict(gH=q), dict(gL=q)):
         assert grad(**bad) == -1, bad
     assert grad(N=0) == 0
+
+
+def test_w4_matvec_rejects_invalid_arguments(L):
+    p, q = ctypes.c_void_p(4096), ctypes.c_void_p(4097)
+
+    def mx(**kw):
+        a = {**dict(W=p, f=2, L=10, D=256, G=32, s=None, z=None, X=p, N=2, ldx=256, Y=p, t=0, ldy=10), **kw}
+        return L.elmo_w4_matvec(a["W"], a["f"], a["L"], a["D"], a["G"], a["s"], a["z"], a["X"], a["N"], a["ldx"], a["Y"],
+                                a["t"], a["ldy"], None)
+
+    def i4(**kw):
+        return mx(**{**dict(f=3, G=64, s=p), **kw})
+    assert mx(f=1) == -3 and mx(f=4) == -3 and mx(t=3) == -3
+    for bad in (dict(N=33), dict(N=-1), dict(L=0), dict(L=2**31), dict(D=0), dict(D=128, ldx=128), dict(D=65792, ldx=65792),
+                dict(G=64), dict(ldx=248), dict(ldx=260), dict(ldy=9)):
+        assert mx(**bad) == -2, bad
+    for bad in (dict(G=16), dict(G=256), dict(D=224, ldx=256), dict(G=128, D=192)):
+        assert i4(**bad) == -2, bad
+    for bad in (dict(W=None), dict(X=None), dict(Y=None), dict(W=ctypes.c_void_p(4100)), dict(X=ctypes.c_void_p(4104)),
+                dict(Y=ctypes.c_void_p(4098)), dict(s=p), dict(z=p)):
+        assert mx(**bad) == -1, bad
+    for bad in (dict(s=None), dict(s=q), dict(W=ctypes.c_void_p(4104))):
+        assert i4(**bad) == -1, bad
+    assert mx(N=0, W=None) == 0
