@@ -285,6 +285,39 @@ int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const
                    void* stream);
 
 /*
+ * Activation checkpoints in 8 bits: what an encoder keeps between its forward and its backward pass,
+ * at 33/32 of a byte per element, and the two uses of it in the backward.
+ *
+ * Format: codes [T, D] OCP E4M3 bytes and scales [T, D / 32] E8M0 bytes (both row-major, 8-byte
+ * aligned codes); elements 32 b .. 32 b + 31 of a row share scale c = scales[t, b], X = c - 127 the
+ * smallest X >= -127 with max|x| <= 448 2^X (an all-zero block takes X = -127), and
+ * codes = E4M3-RNE(x / 2^X): nothing saturates. A NaN or infinite element takes the NaN code and
+ * leaves its block's other elements alone.
+ *
+ * D % 32 == 0, D >= 32, T >= 0 (T = 0: nothing is done). `type` is the element type of x, y, dy, dx;
+ * their rows are 16-byte aligned at pitches ld (elements, >= D).
+ */
+enum { ELMO_ACT_NONE = 0, ELMO_ACT_RELU = 1, ELMO_ACT_SILU = 2, ELMO_ACT_GELU = 3 };
+/* Saves x [T, D]; with act != NONE also y = act(x) of the unrounded x, in the same pass (y nullable
+ * only with NONE, where it must be NULL). relu(x) = max(x, 0); silu(x) = x / (1 + e^-x); gelu(x) =
+ * x Phi(x), Phi the normal distribution function (no tanh approximation). y must not overlap x. */
+int elmo_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes,
+                    uint8_t* scales, void* y, int64_t ldy, void* stream);
+/* The saved activations, x' [T, D]: exact in FP32 and BF16 (as far as the type's range goes), rounded in FP16. */
+int elmo_ckpt8_load(const uint8_t* codes, const uint8_t* scales, int64_t T, int D, void* x, int type, int64_t ldx,
+                    void* stream);
+/* dx = dy act'(x') with the saved x' (relu'(0) = 0), act != NONE; dx = dy with equal pitches is allowed. */
+int elmo_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy, int act, const uint8_t* codes,
+                        const uint8_t* scales, void* dx, int64_t lddx, void* stream);
+/* The weight gradient of a linear layer Y = X W^T from its saved input: dW [O, D] FP32 (row-major, 16-byte
+ * aligned) = dY^T x', plus dW's old values if `accumulate` is nonzero. dY [T, O] BF16, 16-byte aligned rows
+ * (O % 8 == 0, ldy % 8 == 0). Products of exact operands, binary32 sums in an order fixed by the shape.
+ * T = 0 gives 0 (or leaves dW). T < 2^31; the workspace holds the partial sums of split tokens. */
+size_t elmo_ckpt8_weight_grad_workspace_bytes(int64_t T, int O, int D);
+int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O,
+                           int D, float* dW, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Test hook: the device codec, stochastic rounding and RNG applied elementwise to n elements.
  *   op 0  BF16 RNE encode:      in0 float[n]            -> out uint16[n]
  *   op 1  E4M3 RNE-sat encode:  in0 float[n]            -> out uint8[n]

@@ -89,6 +89,14 @@ def lib():
         L.elmo_logprobs_backward.restype = i32
         L.elmo_w4_matvec.argtypes = [P, i32, i64, i32, i32, P, P, P, i32, i64, P, i32, i64, P]
         L.elmo_w4_matvec.restype = i32
+        L.elmo_ckpt8_save.argtypes = [P, i32, i64, i32, i64, i32, P, P, P, i64, P]; L.elmo_ckpt8_save.restype = i32
+        L.elmo_ckpt8_load.argtypes = [P, P, i64, i32, P, i32, i64, P]; L.elmo_ckpt8_load.restype = i32
+        L.elmo_ckpt8_act_grad.argtypes = [P, i32, i64, i32, i64, i32, P, P, P, i64, P]
+        L.elmo_ckpt8_act_grad.restype = i32
+        L.elmo_ckpt8_weight_grad_workspace_bytes.argtypes = [i64, i32, i32]
+        L.elmo_ckpt8_weight_grad_workspace_bytes.restype = sz
+        L.elmo_ckpt8_weight_grad.argtypes = [P, i64, P, P, i64, i32, i32, P, i32, P, sz, P]
+        L.elmo_ckpt8_weight_grad.restype = i32
         _lib = L
     return _lib
 
@@ -405,6 +413,91 @@ def w4_matvec(W, X, wfmt=ELMO_W_MXFP4, scales=None, zeros=None, out_dtype=torch.
         _chk("elmo_w4_matvec", lib().elmo_w4_matvec(
             W.data_ptr(), wfmt, L, D, group, _ptr(scales), _ptr(zeros), X.data_ptr(), N, ldx, out.data_ptr(),
             _etype(out), ldy, _stream()))
+    return out
+
+
+_ACTS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3}
+
+
+def _act(name) -> int:
+    if name not in _ACTS:
+        raise ValueError(f"unknown activation {name!r}: relu, silu or gelu")
+    return _ACTS[name]
+
+
+def _codes(codes, scales):
+    """(T, D) of a saved activation."""
+    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous 2-D uint8 CUDA tensor")
+    T, D = codes.shape
+    _like("scales", scales, (T, D // 32), torch.uint8, codes.device)
+    return T, D
+
+
+def ckpt8_save(x, act=None):
+    """Keeps x [T, D] (float32, bfloat16 or float16, D % 32 == 0) in 8 bits: (codes uint8 [T, D],
+    scales uint8 [T, D / 32], y), y = act(x) for act "relu", "silu" or "gelu", computed in the same
+    pass, or None without one. See elmo_ckpt8_save in elmo_xmc.h."""
+    e, a = _etype(x), _act(act)
+    T, D, ld = _rows("x", x)
+    codes = torch.empty((T, D), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((T, D // 32), dtype=torch.uint8, device=x.device)
+    y = torch.empty((T, D), dtype=x.dtype, device=x.device) if a else None
+    _chk("elmo_ckpt8_save", lib().elmo_ckpt8_save(x.data_ptr(), e, T, D, ld, a, codes.data_ptr(), scales.data_ptr(),
+                                                  _ptr(y), D, _stream()))
+    return codes, scales, y
+
+
+def ckpt8_load(codes, scales, dtype=torch.bfloat16, out=None):
+    """The activations [T, D] that ckpt8_save kept."""
+    T, D = _codes(codes, scales)
+    if out is None:
+        out = torch.empty((T, D), dtype=dtype, device=codes.device)
+    elif tuple(out.shape) != (T, D) or out.device != codes.device:
+        raise ValueError("out must be [T, D] on the codes' device")
+    _chk("elmo_ckpt8_load", lib().elmo_ckpt8_load(codes.data_ptr(), scales.data_ptr(), T, D, out.data_ptr(),
+                                                  _etype(out), _rows("out", out)[2], _stream()))
+    return out
+
+
+def ckpt8_act_grad(dy, codes, scales, act, out=None):
+    """dx = dy act'(x) [T, D] (dy's type) from the saved x; out = dy writes over the upstream gradient."""
+    e, a = _etype(dy), _act(act)
+    T, D = _codes(codes, scales)
+    if tuple(dy.shape) != (T, D) or dy.device != codes.device:
+        raise ValueError("dy must be [T, D] on the codes' device")
+    if out is None:
+        out = torch.empty((T, D), dtype=dy.dtype, device=dy.device)
+    elif out.shape != dy.shape or out.dtype != dy.dtype or out.device != dy.device:
+        raise ValueError("out must have dy's shape, type and device")
+    _chk("elmo_ckpt8_act_grad", lib().elmo_ckpt8_act_grad(
+        dy.data_ptr(), e, T, D, _rows("dy", dy)[2], a, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
+        _rows("out", out)[2], _stream()))
+    return out
+
+
+def ckpt8_weight_grad(dy, codes, scales, out=None, accumulate=False, workspace=None):
+    """dW [O, D] float32 = dy^T x from the layer's saved input x [T, D] and dy [T, O] (bfloat16,
+    O % 8 == 0); accumulate=True adds to `out`."""
+    T, D = _codes(codes, scales)
+    if dy.dtype not in (torch.bfloat16, torch.int16, torch.uint16) or dy.device != codes.device:
+        raise ValueError("dy must hold BF16 codes on the codes' device")
+    t, O, ld = _rows("dy", dy)
+    if t != T:
+        raise ValueError(f"dy has {t} tokens, the saved input {T}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((O, D), dtype=torch.float32, device=dy.device)
+    _like("out", out, (O, D), torch.float32, codes.device)
+    need = int(lib().elmo_ckpt8_weight_grad_workspace_bytes(T, O, D))
+    if need == 0:
+        raise ElmoError("elmo_ckpt8_weight_grad_workspace_bytes", -2)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+    _chk("elmo_ckpt8_weight_grad", lib().elmo_ckpt8_weight_grad(
+        dy.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), T, O, D, out.data_ptr(), int(accumulate),
+        workspace.data_ptr(), workspace.numel(), _stream()))
     return out
 
 

@@ -40,6 +40,14 @@ int check_rows(int ztype, int64_t N, int64_t V, int64_t ld, int M) {
   return ELMO_OK;
 }
 
+// a [T, D] matrix with 16-byte aligned rows, and the 8-bit form of one
+bool rows16(const void* p, int type, int64_t ld) { return aligned16(p) && ld * (int64_t)type_bytes(type) % 16 == 0; }
+int check_ckpt8(int type, int64_t T, int D) {
+  if (!known_type(type)) return ELMO_EDTYPE;
+  if (T < 0 || T >= (int64_t(1) << 31) || D < 32 || D % 32 != 0 || D > (1 << 24)) return ELMO_ESHAPE;
+  return ELMO_OK;
+}
+
 // which kernels a step runs: the faster for its shape (the single pass where it is built, B <= 32
 // and D = 256, 512 or 768), or the one the caller names
 enum { PATH_AUTO = 0, PATH_TWO_KERNEL = 1, PATH_SINGLE = 2 };
@@ -265,6 +273,59 @@ int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const
   if (wdtype == ELMO_W_MXFP4 && (scales || zeros || !aligned_to(W, 8))) return ELMO_EINVAL;
   if (wdtype == ELMO_W_INT4 && (!scales || !aligned_to(scales, 2) || !aligned16(W))) return ELMO_EINVAL;
   return elmo::run_w4_matvec(W, wdtype, L, D, group, scales, zeros, X, N, ldx, Y, ytype, ldy, (hipStream_t)stream);
+}
+
+int elmo_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes, uint8_t* scales,
+                    void* y, int64_t ldy, void* stream) {
+  const int rc = check_ckpt8(type, T, D);
+  if (rc != ELMO_OK) return rc;
+  if (act < ELMO_ACT_NONE || act > ELMO_ACT_GELU) return ELMO_EINVAL;
+  if (ldx < D || (y && ldy < D)) return ELMO_ESHAPE;
+  if (T == 0) return ELMO_OK;
+  if ((act == ELMO_ACT_NONE) != (y == nullptr)) return ELMO_EINVAL;
+  if (!x || !codes || !scales || !rows16(x, type, ldx) || (y && !rows16(y, type, ldy)) || !aligned_to(codes, 8))
+    return ELMO_EINVAL;
+  return elmo::run_ckpt8_save(x, type, T, D, ldx, act, codes, scales, y, ldy, (hipStream_t)stream);
+}
+
+int elmo_ckpt8_load(const uint8_t* codes, const uint8_t* scales, int64_t T, int D, void* x, int type, int64_t ldx,
+                    void* stream) {
+  const int rc = check_ckpt8(type, T, D);
+  if (rc != ELMO_OK) return rc;
+  if (ldx < D) return ELMO_ESHAPE;
+  if (T == 0) return ELMO_OK;
+  if (!x || !codes || !scales || !rows16(x, type, ldx) || !aligned_to(codes, 8)) return ELMO_EINVAL;
+  return elmo::run_ckpt8_load(codes, scales, T, D, x, type, ldx, (hipStream_t)stream);
+}
+
+int elmo_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy, int act, const uint8_t* codes,
+                        const uint8_t* scales, void* dx, int64_t lddx, void* stream) {
+  const int rc = check_ckpt8(type, T, D);
+  if (rc != ELMO_OK) return rc;
+  if (act < ELMO_ACT_RELU || act > ELMO_ACT_GELU) return ELMO_EINVAL;
+  if (lddy < D || lddx < D || (dx == dy && lddx != lddy)) return ELMO_ESHAPE;
+  if (T == 0) return ELMO_OK;
+  if (!dy || !dx || !codes || !scales || !rows16(dy, type, lddy) || !rows16(dx, type, lddx) || !aligned_to(codes, 8))
+    return ELMO_EINVAL;
+  return elmo::run_ckpt8_act_grad(dy, type, T, D, lddy, act, codes, scales, dx, lddx, (hipStream_t)stream);
+}
+
+size_t elmo_ckpt8_weight_grad_workspace_bytes(int64_t T, int O, int D) {
+  if (check_ckpt8(ELMO_T_BF16, T, D) != ELMO_OK || O < 8 || O % 8 != 0 || O > (1 << 24)) return 0;
+  return elmo::wgrad_layout(T, O, D).total;
+}
+
+int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O,
+                           int D, float* dW, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_ckpt8(ELMO_T_BF16, T, D);
+  if (rc != ELMO_OK) return rc;
+  if (O < 8 || O % 8 != 0 || O > (1 << 24) || ldy < O || ldy % 8 != 0) return ELMO_ESHAPE;
+  if (!dW || !aligned16(dW)) return ELMO_EINVAL;
+  if (T > 0 && (!dY || !codes || !scales || !aligned16(dY) || !aligned_to(codes, 8))) return ELMO_EINVAL;
+  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
+  const elmo::WgradLayout s = elmo::wgrad_layout(T, O, D);
+  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  return elmo::run_ckpt8_wgrad(dY, ldy, codes, scales, T, O, D, dW, accumulate, s, workspace, (hipStream_t)stream);
 }
 
 int elmo_numerics_probe(int op, const void* in0, const void* in1, void* out, int64_t n, uint64_t seed,

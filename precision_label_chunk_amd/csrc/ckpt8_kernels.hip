@@ -1,0 +1,427 @@
+// Activations kept in 8 bits between the forward and the backward pass, and the two places where the
+// backward uses them: the derivative of an elementwise activation, and the weight gradient of the
+// linear layer behind it.
+//
+// Format (the layout of the MX weight formats, with 8-bit elements): 32 consecutive features of a
+// token share one E8M0 scale 2^X, the smallest power of two with max |x| <= 448 2^X, and are stored
+// as E4M3 to nearest even. The scale is taken from the elements themselves rather than rounded down
+// as floor(log2 max |x|) - 8 would: that saturates blocks whose largest element is over 1.75 times
+// its power of two, an error of up to 12.5% in the block's largest value; this costs the smallest
+// elements of such a block one bit instead. Decoding is exact in BF16 (4 significant bits times a
+// power of two), so that the matrix products read exact operands.
+#include "elem_types.hpp"
+#include "step_kernels.hpp"
+
+namespace elmo {
+
+enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
+
+// Phi(x) and e^(-x^2/2), the normal distribution and its unscaled density. With z = |x| / sqrt 2 and
+// t = 1 / (1 + 0.3 z), erfc(z) = e^(-z^2) t P(t), P of degree 8 fitted to erfcx(z) / t over z <= 11
+// for the smallest relative error (2.0e-8); the tail keeps its relative accuracy because nothing is
+// subtracted from 1 there. In binary32 within 9e-7 of Phi relative for |x| < 5, 4e-6 beyond.
+__device__ __forceinline__ void normal_parts(float x, float& cdf, float& dens) {
+  const float z = __builtin_fabsf(x) * 0.70710678118654752f;
+  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, z, 1.0f));
+  float p = -0.12955603003501892f;
+  p = __builtin_fmaf(p, t, 0.4857371747493744f);
+  p = __builtin_fmaf(p, t, -0.5126697421073914f);
+  p = __builtin_fmaf(p, t, 0.548213005065918f);
+  p = __builtin_fmaf(p, t, -0.09502958506345749f);
+  p = __builtin_fmaf(p, t, 0.2151077836751938f);
+  p = __builtin_fmaf(p, t, 0.1482861191034317f);
+  p = __builtin_fmaf(p, t, 0.1707238256931305f);
+  p = __builtin_fmaf(p, t, 0.16918741166591644f);
+  dens = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f);        // -log2(e) / 2
+  const float half = 0.5f * t * p * dens;
+  cdf = x < 0.0f ? half : 1.0f - half;
+}
+// sigma(x) = a (a r) and 1 - sigma(x) = q, without cancellation: with e = e^(-|x|) and r = 1 / (1 + e),
+// sigma is r or e r and its complement the other. Below 0, e is split into two factors a = e^(-|x|/2),
+// so that x sigma(x) keeps its value down to the smallest results (x = -100) where e leaves the
+// normal range.
+struct Sigmoid { float a, ar, q; };
+__device__ __forceinline__ Sigmoid sigmoid_parts(float x) {
+  const float h = __builtin_amdgcn_exp2f(__builtin_fabsf(x) * -0.72134752044448170f);
+  const float e = h * h, r = __builtin_amdgcn_rcpf(1.0f + e);
+  const bool neg = x < 0.0f;
+  const float a = neg ? h : 1.0f;
+  return Sigmoid{a, a * r, neg ? r : e * r};
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float x) {
+  if constexpr (ACT == ACT_RELU) return x < 0.0f ? 0.0f : x;           // (NaN stays)
+  if constexpr (ACT == ACT_SILU) {
+    const Sigmoid s = sigmoid_parts(x);
+    return (x * s.a) * s.ar;
+  }
+  if constexpr (ACT == ACT_GELU) {
+    float cdf, dens;
+    normal_parts(x, cdf, dens);
+    return x * cdf;
+  }
+  return x;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float x) {
+  if constexpr (ACT == ACT_RELU) return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
+  if constexpr (ACT == ACT_SILU) {
+    const Sigmoid s = sigmoid_parts(x);
+    return s.a * (s.ar * __builtin_fmaf(x, s.q, 1.0f));
+  }
+  if constexpr (ACT == ACT_GELU) {
+    float cdf, dens;
+    normal_parts(x, cdf, dens);
+    return __builtin_fmaf(x * 0.39894228040143268f, dens, cdf);        // 1 / sqrt(2 pi)
+  }
+  return 1.0f;
+}
+
+// 8 consecutive elements at p, 16-byte aligned
+template <typename E>
+__device__ __forceinline__ void load8(const typename E::raw* p, float (&f)[8]) {
+  E::widen(__builtin_nontemporal_load((const i32x4_t*)p), f);
+  if constexpr (E::VEC == 4) E::widen(__builtin_nontemporal_load((const i32x4_t*)p + 1), f + 4);
+}
+template <typename E>
+__device__ __forceinline__ void store8(typename E::raw* p, const float (&f)[8]) {
+  __builtin_nontemporal_store(E::narrow(f), (i32x4_t*)p);
+  if constexpr (E::VEC == 4) __builtin_nontemporal_store(E::narrow(f + 4), (i32x4_t*)p + 1);
+}
+// the 8 elements that 8 codes at p stand for
+__device__ __forceinline__ void decode8(i32x2_t c, float scale, float (&f)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int w = c[h];
+    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    f[4 * h] = a[0] * scale; f[4 * h + 1] = a[1] * scale;
+    f[4 * h + 2] = b[0] * scale; f[4 * h + 3] = b[1] * scale;
+  }
+}
+
+// the largest magnitude of a block's bits to its scale code X + 127: floor(log2 a) - 8 + 127, one
+// more where the fraction is over 1.75; at least 0 (2^-127, also for a block of zeros)
+__device__ __forceinline__ uint32_t block_scale_code(uint32_t a) {
+  const int c = (int)(a >> 23) - 8 + ((a & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return c < 0 ? 0u : (uint32_t)c;
+}
+
+struct Ckpt8Args {
+  const void* in; int64_t ldin;                 // x, or dy
+  void* out; int64_t ldout;                     // y, dx or the restored activations (nullable in save)
+  uint8_t* codes; uint8_t* scales;
+  int64_t n8; int D;                            // vectors of 8 features
+};
+
+// start of vector i in a matrix of row pitch ld
+__device__ __forceinline__ int64_t vec_at(int64_t i, int D, int64_t ld) {
+  if (ld == D) return 8 * i;
+  const int64_t row = i / (D / 8);
+  return row * ld + 8 * (i - row * (D / 8));
+}
+
+// Elementwise, bound by HBM: each thread takes 8 features, the four threads of a block of 32 share
+// their largest magnitude.
+template <typename E, int ACT, bool OUT>
+__global__ __launch_bounds__(256) void k_ckpt8_save(Ckpt8Args a) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
+    float f[8];
+    load8<E>((const typename E::raw*)a.in + vec_at(i, a.D, a.ldin), f);
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t m = f2u(f[e]) & 0x7fffffffu;
+      top = m < 0x7f800000u && m > top ? m : top;               // (NaN and infinity set no scale)
+    }
+    const uint32_t t1 = (uint32_t)__shfl_xor((int)top, 1);
+    top = t1 > top ? t1 : top;
+    const uint32_t t2 = (uint32_t)__shfl_xor((int)top, 2);
+    top = t2 > top ? t2 : top;
+    const uint32_t code = block_scale_code(top);
+    const float inv = u2f((254u - code) << 23);                 // 2^-X: code <= 247, always normal
+    i32x2_t c;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float g[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        g[e] = f[4 * h + e] * inv;                              // exact; at most 448
+        if (!(__builtin_fabsf(g[e]) <= 448.0f)) g[e] = __builtin_nanf("");
+      }
+      int w = 0;
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], w, false);
+      w = __builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
+      c[h] = w;
+    }
+    __builtin_nontemporal_store(c, (i32x2_t*)a.codes + i);
+    if ((i & 3) == 0) a.scales[i >> 2] = (uint8_t)code;
+    if constexpr (OUT) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = act_value<ACT>(f[e]);
+      store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), f);
+    }
+  }
+}
+
+template <typename E>
+__global__ __launch_bounds__(256) void k_ckpt8_load(Ckpt8Args a) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
+    float f[8];
+    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), e8m0_to_f32(a.scales[i >> 2]), f);
+    store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), f);
+  }
+}
+
+// dx = dy act'(x) with x from its 8 bits; dx may be dy's own memory
+template <typename E, int ACT>
+__global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
+    float f[8], d[8];
+    load8<E>((const typename E::raw*)a.in + vec_at(i, a.D, a.ldin), d);
+    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), e8m0_to_f32(a.scales[i >> 2]), f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] *= act_slope<ACT>(f[e]);
+    store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), d);
+  }
+}
+
+// ---- weight gradient -------------------------------------------------------------------------------
+// dW [O][D] = dY^T X over T tokens, dY BF16 [T][O], X the 8-bit form [T][D]; FP32 sums.
+//
+// Both operands have the contraction (tokens) as their rows, so both come out of LDS through the
+// transposing reads (ds_read_b64_tr_b16). A block of 4 waves (2 x 2) owns a tile of 64 MF x 64 NF
+// of dW, each wave MF x NF products of 32 x 32; a stage holds BK tokens of both operands as BF16,
+// the codes decoded on their way into LDS (half an operation per code, shared by the whole tile).
+// Two LDS buffers and the next stage's loads in registers: one barrier per stage. Rows are padded
+// by 64 bytes, so that the four token rows of a transposing read cover all 64 banks.
+// Few tiles split the tokens over `segs` blocks, whose partial tiles k_wgrad_join adds in order.
+constexpr int WG_BK = 32;
+
+struct WgradArgs {
+  const uint16_t* dY; int64_t ldy;
+  const uint8_t *codes, *scales;
+  int64_t T; int O, D;
+  float* dW; int accumulate;
+  int segs; int64_t per;                        // tokens per segment, a multiple of WG_BK
+  float* part;                                  // [segs][O][D]
+  int tiles_d;
+};
+
+template <int MF, int NF>
+__global__ __launch_bounds__(256) void k_ckpt8_wgrad(WgradArgs a) {
+  constexpr int BM = 64 * MF, BN = 64 * NF;
+  constexpr int PA = BM + 32, PB = BN + 32;               // LDS row pitch (elements)
+  constexpr int NA = WG_BK * BM / 8 / 256;                // 16-byte vectors of dY per thread and stage
+  constexpr int NB = WG_BK * BN / 8 / 256;                // 8-code vectors per thread and stage
+  __shared__ __attribute__((aligned(16))) uint16_t la[2][WG_BK * PA];
+  __shared__ __attribute__((aligned(16))) uint16_t lb[2][WG_BK * PB];
+  const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int seg = (int)(blockIdx.x % a.segs), tile = (int)(blockIdx.x / a.segs);
+  const int o0 = tile / a.tiles_d * BM, d0 = tile % a.tiles_d * BN;
+  const int64_t t0 = seg * a.per;
+  const int64_t t1 = t0 + a.per < a.T ? t0 + a.per : a.T;
+  const int stages = t1 > t0 ? (int)((t1 - t0 + WG_BK - 1) / WG_BK) : 0;
+
+  i32x4_t ra[NA];
+  i32x2_t rb[NB];
+  uint32_t rs[NB];
+  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < NA; ++v) {
+      const int k = (tid + 256 * v) / (BM / 8), c = (tid + 256 * v) % (BM / 8) * 8;
+      ra[v] = i32x4_t{0, 0, 0, 0};
+      if (t + k < t1 && o0 + c < a.O) ra[v] = *(const i32x4_t*)(a.dY + (t + k) * a.ldy + o0 + c);
+    }
+#pragma unroll
+    for (int v = 0; v < NB; ++v) {
+      const int k = (tid + 256 * v) / (BN / 8), c = (tid + 256 * v) % (BN / 8) * 8;
+      rb[v] = i32x2_t{0, 0};
+      rs[v] = 0;
+      if (t + k < t1 && d0 + c < a.D) {
+        rb[v] = *(const i32x2_t*)(a.codes + (t + k) * a.D + d0 + c);
+        rs[v] = a.scales[(t + k) * (a.D / 32) + (d0 + c) / 32];
+      }
+    }
+  };
+  auto put = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int v = 0; v < NA; ++v) {
+      const int k = (tid + 256 * v) / (BM / 8), c = (tid + 256 * v) % (BM / 8) * 8;
+      *(i32x4_t*)&la[b][k * PA + c] = ra[v];
+    }
+#pragma unroll
+    for (int v = 0; v < NB; ++v) {
+      const int k = (tid + 256 * v) / (BN / 8), c = (tid + 256 * v) % (BN / 8) * 8;
+      const float s = e8m0_to_f32(rs[v]);
+      i32x4_t w;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int q = rb[v][h];
+        w[2 * h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, false));
+        w[2 * h + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, true));
+      }
+      *(i32x4_t*)&lb[b][k * PB + c] = w;
+    }
+  };
+
+  f32x16_t acc[MF][NF];
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  // lane's place in a transposing read: group g of 16 lanes takes columns 16 (g & 1) .. + 16 and rows
+  // 8 (g >> 1) .. + 4 (then + 4 .. + 8); lane j of it supplies row j / 4, columns 4 (j % 4) .. + 4
+  const int g = lane >> 4, j16 = lane & 15;
+  const int mo = (wave >> 1) * 32 * MF + 16 * (g & 1) + 4 * (j16 & 3);
+  const int no = (wave & 1) * 32 * NF + 16 * (g & 1) + 4 * (j16 & 3);
+  const int ko = 8 * (g >> 1) + (j16 >> 2);
+
+  if (stages) {
+    fetch(t0);
+    put(0);
+  }
+  __syncthreads();
+  for (int s = 0; s < stages; ++s) {
+    const int b = s & 1;
+    if (s + 1 < stages) fetch(t0 + (int64_t)(s + 1) * WG_BK);
+#pragma unroll
+    for (int kk = 0; kk < WG_BK; kk += 16) {
+      s16x8_t fa[MF], fb[NF];
+#pragma unroll
+      for (int i = 0; i < MF; ++i) {
+        const uint16_t* p = &la[b][(kk + ko) * PA + mo + 32 * i];
+        fa[i] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PA));
+      }
+#pragma unroll
+      for (int j = 0; j < NF; ++j) {
+        const uint16_t* p = &lb[b][(kk + ko) * PB + no + 32 * j];
+        fb[j] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PB));
+      }
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(fa[i], fb[j], acc[i][j]);
+    }
+    if (s + 1 < stages) put(b ^ 1);
+    __syncthreads();
+  }
+
+  float* out = a.segs > 1 ? a.part + (int64_t)seg * a.O * a.D : a.dW;
+  const bool add = a.segs == 1 && a.accumulate;
+#pragma unroll
+  for (int i = 0; i < MF; ++i)
+#pragma unroll
+    for (int j = 0; j < NF; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int o = o0 + ((wave >> 1) * MF + i) * 32 + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+        const int d = d0 + ((wave & 1) * NF + j) * 32 + (lane & 31);
+        if (o < a.O && d < a.D) {
+          float* q = out + (int64_t)o * a.D + d;
+          *q = add ? *q + acc[i][j][r] : acc[i][j][r];
+        }
+      }
+}
+
+// dW = (accumulate ? dW : 0) + the segments' partials, in their order
+__global__ __launch_bounds__(256) void k_wgrad_join(const float* part, float* dW, int64_t n4, int segs, int accumulate) {
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    f32x4_t s = accumulate ? ((const f32x4_t*)dW)[i] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int g = 0; g < segs; ++g) {
+      const f32x4_t p = ((const f32x4_t*)part)[g * n4 + i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += p[e];
+    }
+    ((f32x4_t*)dW)[i] = s;
+  }
+}
+
+// ---- launchers -------------------------------------------------------------------------------------
+static unsigned grid_of(int64_t n) {
+  const int64_t want = (n + 255) / 256, cap = 256 * (int64_t)device_cus();
+  return (unsigned)(want < cap ? want : cap);
+}
+#define ELMO_LAUNCH(kernel, n, st, ...)                                        \
+  hipLaunchKernelGGL((kernel), dim3(grid_of(n)), dim3(256), 0, st, __VA_ARGS__)
+
+template <typename E>
+static void save_as(const Ckpt8Args& a, int act, hipStream_t st) {
+  if (!a.out) ELMO_LAUNCH((k_ckpt8_save<E, ACT_NONE, false>), a.n8, st, a);
+  else if (act == ACT_RELU) ELMO_LAUNCH((k_ckpt8_save<E, ACT_RELU, true>), a.n8, st, a);
+  else if (act == ACT_SILU) ELMO_LAUNCH((k_ckpt8_save<E, ACT_SILU, true>), a.n8, st, a);
+  else ELMO_LAUNCH((k_ckpt8_save<E, ACT_GELU, true>), a.n8, st, a);
+}
+template <typename E>
+static void grad_as(const Ckpt8Args& a, int act, hipStream_t st) {
+  if (act == ACT_RELU) ELMO_LAUNCH((k_ckpt8_act_grad<E, ACT_RELU>), a.n8, st, a);
+  else if (act == ACT_SILU) ELMO_LAUNCH((k_ckpt8_act_grad<E, ACT_SILU>), a.n8, st, a);
+  else ELMO_LAUNCH((k_ckpt8_act_grad<E, ACT_GELU>), a.n8, st, a);
+}
+
+int run_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes, uint8_t* scales,
+                   void* y, int64_t ldy, hipStream_t st) {
+  Ckpt8Args a{};
+  a.in = x; a.ldin = ldx; a.out = y; a.ldout = ldy; a.codes = codes; a.scales = scales; a.n8 = T * (D / 8); a.D = D;
+  if (type == T_F32_) save_as<ElemF32>(a, act, st);
+  else if (type == T_BF16_) save_as<ElemBF16>(a, act, st);
+  else save_as<ElemF16>(a, act, st);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+int run_ckpt8_load(const uint8_t* codes, const uint8_t* scales, int64_t T, int D, void* x, int type, int64_t ldx,
+                   hipStream_t st) {
+  Ckpt8Args a{};
+  a.out = x; a.ldout = ldx; a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales);
+  a.n8 = T * (D / 8); a.D = D;
+  if (type == T_F32_) ELMO_LAUNCH(k_ckpt8_load<ElemF32>, a.n8, st, a);
+  else if (type == T_BF16_) ELMO_LAUNCH(k_ckpt8_load<ElemBF16>, a.n8, st, a);
+  else ELMO_LAUNCH(k_ckpt8_load<ElemF16>, a.n8, st, a);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+int run_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy, int act, const uint8_t* codes,
+                       const uint8_t* scales, void* dx, int64_t lddx, hipStream_t st) {
+  Ckpt8Args a{};
+  a.in = dy; a.ldin = lddy; a.out = dx; a.ldout = lddx;
+  a.codes = const_cast<uint8_t*>(codes); a.scales = const_cast<uint8_t*>(scales); a.n8 = T * (D / 8); a.D = D;
+  if (type == T_F32_) grad_as<ElemF32>(a, act, st);
+  else if (type == T_BF16_) grad_as<ElemBF16>(a, act, st);
+  else grad_as<ElemF16>(a, act, st);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+// Tiles of 128 x 128; the tokens split so that every CU has a few blocks, none below 512 tokens.
+WgradLayout wgrad_layout(int64_t T, int O, int D) {
+  WgradLayout s{};
+  s.tiles_o = (O + 127) / 128;
+  s.tiles_d = (D + 127) / 128;
+  const int64_t tiles = (int64_t)s.tiles_o * s.tiles_d;
+  int64_t segs = (2 * device_cus() + tiles - 1) / tiles;
+  const int64_t most = T / 512 > 0 ? T / 512 : 1;
+  if (segs > most) segs = most;
+  s.per = ((T + segs - 1) / segs + WG_BK - 1) / WG_BK * WG_BK;
+  if (s.per < WG_BK) s.per = WG_BK;
+  s.segs = T > 0 ? (int)((T + s.per - 1) / s.per) : 1;
+  s.total = s.segs > 1 ? (size_t)s.segs * O * D * 4 : 256;
+  return s;
+}
+
+int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O, int D,
+                    float* dW, int accumulate, const WgradLayout& s, void* workspace, hipStream_t st) {
+  WgradArgs a{};
+  a.dY = (const uint16_t*)dY; a.ldy = ldy; a.codes = codes; a.scales = scales; a.T = T; a.O = O; a.D = D;
+  a.dW = dW; a.accumulate = accumulate; a.segs = s.segs; a.per = s.per; a.part = (float*)workspace; a.tiles_d = s.tiles_d;
+  hipLaunchKernelGGL((k_ckpt8_wgrad<2, 2>), dim3((unsigned)(s.tiles_o * s.tiles_d * s.segs)), dim3(256), 0, st, a);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  if (s.segs > 1) {
+    const int64_t n4 = (int64_t)O * D / 4;
+    ELMO_LAUNCH(k_wgrad_join, n4, st, (const float*)workspace, dW, n4, s.segs, accumulate);
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  }
+  return ELMO_OK_;
+}
+
+}  // namespace elmo

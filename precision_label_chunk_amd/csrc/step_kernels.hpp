@@ -119,6 +119,18 @@ constexpr int W_INT4_ = 3;
 int run_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const uint16_t* scales, const uint8_t* zeros,
                   const void* X, int N, int64_t ldx, void* Y, int ytype, int64_t ldy, hipStream_t st);
 
+// activations kept in 8 bits (E4M3 with an E8M0 scale per 32 features) and their use in the backward
+struct WgradLayout { int tiles_o, tiles_d, segs; int64_t per; size_t total; };
+int run_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes, uint8_t* scales,
+                   void* y, int64_t ldy, hipStream_t st);
+int run_ckpt8_load(const uint8_t* codes, const uint8_t* scales, int64_t T, int D, void* x, int type, int64_t ldx,
+                   hipStream_t st);
+int run_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy, int act, const uint8_t* codes,
+                       const uint8_t* scales, void* dx, int64_t lddx, hipStream_t st);
+WgradLayout wgrad_layout(int64_t T, int O, int D);
+int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O, int D,
+                    float* dW, int accumulate, const WgradLayout& s, void* workspace, hipStream_t st);
+
 // this device's copy of the static scratch array of the allocation-free step (noalloc.hip): its
 // device address, looked up on the first call on the current device
 int noalloc_scratch(void** out);

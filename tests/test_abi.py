@@ -198,3 +198,40 @@ def test_w4_matvec_rejects_invalid_arguments(L):
     for bad in (dict(s=None), dict(s=q), dict(W=ctypes.c_void_p(4104))):
         assert i4(**bad) == -1, bad
     assert mx(N=0, W=None) == 0
+
+
+def test_ckpt8_rejects_invalid_arguments(L):
+    p, q, o = ctypes.c_void_p(4096), ctypes.c_void_p(4100), ctypes.c_void_p(65536)
+
+    def save(**kw):
+        a = {**dict(x=p, t=1, T=2, D=64, ld=64, act=3, c=p, s=p, y=o, ldy=64), **kw}
+        return L.elmo_ckpt8_save(a["x"], a["t"], a["T"], a["D"], a["ld"], a["act"], a["c"], a["s"], a["y"], a["ldy"], None)
+    assert save(t=3) == -3
+    for bad in (dict(T=-1), dict(D=0), dict(D=48, ld=48), dict(ld=63), dict(ldy=32), dict(T=2**31)):
+        assert save(**bad) == -2, bad
+    for bad in (dict(x=None), dict(c=None), dict(s=None), dict(act=4), dict(act=-1), dict(act=0), dict(y=None), dict(x=q),
+                dict(c=q), dict(ld=68), dict(y=q), dict(ldy=68)):
+        assert save(**bad) == -1, bad
+    assert save(T=0, x=None) == 0
+    assert L.elmo_ckpt8_load(p, p, 2, 48, p, 1, 48, None) == -2 and L.elmo_ckpt8_load(None, p, 2, 64, p, 1, 64, None) == -1
+    assert L.elmo_ckpt8_load(p, p, 2, 64, p, 1, 68, None) == -1 and L.elmo_ckpt8_load(p, p, 2, 64, p, 7, 64, None) == -3
+
+    def grad(**kw):
+        a = {**dict(dy=p, t=1, T=2, D=64, ld=64, act=1, c=p, s=p, dx=o, ldx=64), **kw}
+        return L.elmo_ckpt8_act_grad(a["dy"], a["t"], a["T"], a["D"], a["ld"], a["act"], a["c"], a["s"], a["dx"], a["ldx"], None)
+    assert grad(t=9) == -3 and grad(D=33) == -2 and grad(ldx=63) == -2 and grad(dx=p, ldx=72) == -2
+    for bad in (dict(act=0), dict(act=4), dict(dy=None), dict(dx=None), dict(c=None), dict(s=None), dict(dx=q), dict(ld=68)):
+        assert grad(**bad) == -1, bad
+
+    def wgrad(**kw):
+        a = {**dict(dy=p, ldy=16, c=p, s=p, T=4, O=16, D=64, dW=o, acc=0, ws=p, wb=1 << 30), **kw}
+        return L.elmo_ckpt8_weight_grad(a["dy"], a["ldy"], a["c"], a["s"], a["T"], a["O"], a["D"], a["dW"], a["acc"],
+                                        a["ws"], a["wb"], None)
+    for bad in (dict(O=0), dict(O=12), dict(D=40), dict(T=-1), dict(ldy=8), dict(ldy=20)):
+        assert wgrad(**bad) == -2, bad
+    for bad in (dict(dy=None), dict(c=None), dict(s=None), dict(dW=None), dict(dW=q), dict(dy=q), dict(c=q)):
+        assert wgrad(**bad) == -1, bad
+    for bad in (dict(ws=None), dict(ws=q), dict(wb=1)):
+        assert wgrad(**bad) == -4, bad
+    assert L.elmo_ckpt8_weight_grad_workspace_bytes(4, 12, 64) == 0
+    assert L.elmo_ckpt8_weight_grad_workspace_bytes(1 << 20, 768, 768) >= 768 * 768 * 4
