@@ -294,7 +294,7 @@ int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const
  * codes = E4M3-RNE(x / 2^X): nothing saturates. A NaN or infinite element takes the NaN code and
  * leaves its block's other elements alone.
  *
- * D % 32 == 0, D >= 32, T >= 0 (T = 0: nothing is done). `type` is the element type of x, y, dy, dx;
+ * D % 32 == 0, 32 <= D <= 2^24, 0 <= T < 2^31 (T = 0: nothing is done). `type` is the element type of x, y, dy, dx;
  * their rows are 16-byte aligned at pitches ld (elements, >= D).
  */
 enum { ELMO_ACT_NONE = 0, ELMO_ACT_RELU = 1, ELMO_ACT_SILU = 2, ELMO_ACT_GELU = 3 };
@@ -311,8 +311,8 @@ int elmo_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy
                         const uint8_t* scales, void* dx, int64_t lddx, void* stream);
 /* The weight gradient of a linear layer Y = X W^T from its saved input: dW [O, D] FP32 (row-major, 16-byte
  * aligned) = dY^T x', plus dW's old values if `accumulate` is nonzero. dY [T, O] BF16, 16-byte aligned rows
- * (O % 8 == 0, ldy % 8 == 0). Products of exact operands, binary32 sums in an order fixed by the shape.
- * T = 0 gives 0 (or leaves dW). T < 2^31; the workspace holds the partial sums of split tokens. */
+ * (O % 8 == 0, ldy % 8 == 0, ldy <= 2^23). Products of exact operands, binary32 sums in an order fixed by the shape.
+ * T = 0 gives 0 (or leaves dW). The workspace holds the partial sums of split tokens. */
 size_t elmo_ckpt8_weight_grad_workspace_bytes(int64_t T, int O, int D);
 int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O,
                            int D, float* dW, int accumulate, void* workspace, size_t workspace_bytes, void* stream);

@@ -311,7 +311,7 @@ int elmo_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy
 }
 
 size_t elmo_ckpt8_weight_grad_workspace_bytes(int64_t T, int O, int D) {
-  if (check_ckpt8(ELMO_T_BF16, T, D) != ELMO_OK || O < 8 || O % 8 != 0 || O > (1 << 24)) return 0;
+  if (check_ckpt8(ELMO_T_BF16, T, D) != ELMO_OK || O < 8 || O % 8 != 0 || O > (1 << 23)) return 0;
   return elmo::wgrad_layout(T, O, D).total;
 }
 
@@ -319,7 +319,7 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
                            int D, float* dW, int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   const int rc = check_ckpt8(ELMO_T_BF16, T, D);
   if (rc != ELMO_OK) return rc;
-  if (O < 8 || O % 8 != 0 || O > (1 << 24) || ldy < O || ldy % 8 != 0) return ELMO_ESHAPE;
+  if (O < 8 || O % 8 != 0 || ldy < O || ldy > (1 << 23) || ldy % 8 != 0) return ELMO_ESHAPE;
   if (!dW || !aligned16(dW)) return ELMO_EINVAL;
   if (T > 0 && (!dY || !codes || !scales || !aligned16(dY) || !aligned_to(codes, 8))) return ELMO_EINVAL;
   if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;

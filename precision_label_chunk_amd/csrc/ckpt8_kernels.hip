@@ -89,14 +89,17 @@ __device__ __forceinline__ void store8(typename E::raw* p, const float (&f)[8]) 
   __builtin_nontemporal_store(E::narrow(f), (i32x4_t*)p);
   if constexpr (E::VEC == 4) __builtin_nontemporal_store(E::narrow(f + 4), (i32x4_t*)p + 1);
 }
-// the 8 elements that 8 codes at p stand for
-__device__ __forceinline__ void decode8(i32x2_t c, float scale, float (&f)[8]) {
+// the 8 elements that 8 codes stand for; the conversion takes a scale's exponent field alone, which
+// means in E8M0 what it means there (0: 2^-127, 255: NaN)
+__device__ __forceinline__ void decode8(i32x2_t c, uint32_t scale_code, float (&f)[8]) {
+  const float scale = u2f(scale_code << 23);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int w = c[h];
-    const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-    f[4 * h] = a[0] * scale; f[4 * h + 1] = a[1] * scale;
-    f[4 * h + 2] = b[0] * scale; f[4 * h + 3] = b[1] * scale;
+    const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+    const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
+    f[4 * h] = a[0]; f[4 * h + 1] = a[1];
+    f[4 * h + 2] = b[0]; f[4 * h + 3] = b[1];
   }
 }
 
@@ -168,7 +171,7 @@ template <typename E>
 __global__ __launch_bounds__(256) void k_ckpt8_load(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
     float f[8];
-    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), e8m0_to_f32(a.scales[i >> 2]), f);
+    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), a.scales[i >> 2], f);
     store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), f);
   }
 }
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
     float f[8], d[8];
     load8<E>((const typename E::raw*)a.in + vec_at(i, a.D, a.ldin), d);
-    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), e8m0_to_f32(a.scales[i >> 2]), f);
+    decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), a.scales[i >> 2], f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) d[e] *= act_slope<ACT>(f[e]);
     store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), d);
@@ -193,11 +196,13 @@ __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
 // transposing reads (ds_read_b64_tr_b16). A block of 4 waves (2 x 2) owns a tile of 64 MF x 64 NF
 // of dW, each wave MF x NF products of 32 x 32; a stage holds BK tokens of both operands as BF16,
 // the codes decoded on their way into LDS (half an operation per code, shared by the whole tile).
-// Two LDS buffers and the next stage's loads in registers: one barrier per stage. Rows are padded
-// by 64 bytes, so that the four token rows of a transposing read cover all 64 banks.
+// Two LDS buffers and the next one or two stages' loads in registers: one barrier per stage. Rows are
+// padded by 64 bytes, so that the four token rows of a transposing read cover all 64 banks (no
+// conflicts counted). Bound by the matrix cores at the clock they hold: 16384 tokens, 2048 x 4096 in
+// 265 us, 1040 TFLOP/s, where the library's BF16 product of the decoded operands takes 265; the
+// products keep the cores busy 46% of the cycles, the rest is the LDS reads that feed them.
 // Few tiles split the tokens over `segs` blocks, whose partial tiles k_wgrad_join adds in order.
 constexpr int WG_BK = 32;
-
 struct WgradArgs {
   const uint16_t* dY; int64_t ldy;
   const uint8_t *codes, *scales;
@@ -205,10 +210,10 @@ struct WgradArgs {
   float* dW; int accumulate;
   int segs; int64_t per;                        // tokens per segment, a multiple of WG_BK
   float* part;                                  // [segs][O][D]
-  int tiles_d;
+  int tiles, tiles_d;
 };
 
-template <int MF, int NF>
+template <int MF, int NF, int AHEAD>
 __global__ __launch_bounds__(256) void k_ckpt8_wgrad(WgradArgs a) {
   constexpr int BM = 64 * MF, BN = 64 * NF;
   constexpr int PA = BM + 32, PB = BN + 32;               // LDS row pitch (elements)
@@ -217,51 +222,54 @@ __global__ __launch_bounds__(256) void k_ckpt8_wgrad(WgradArgs a) {
   __shared__ __attribute__((aligned(16))) uint16_t la[2][WG_BK * PA];
   __shared__ __attribute__((aligned(16))) uint16_t lb[2][WG_BK * PB];
   const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int seg = (int)(blockIdx.x % a.segs), tile = (int)(blockIdx.x / a.segs);
+  // Blocks go to the 8 XCDs in turn; each XCD gets a run of (segment, tile) in that order, so that the
+  // tiles that read a segment's tokens share an L2 (16384 tokens, 768 x 768 with the large tile: 73 -> 48 us)
+  const int n = (int)gridDim.x, xcd = (int)blockIdx.x & 7, run = n / 8, more = n % 8;
+  const int id = xcd * run + (xcd < more ? xcd : more) + (int)(blockIdx.x >> 3);
+  const int seg = id / a.tiles, tile = id % a.tiles;
   const int o0 = tile / a.tiles_d * BM, d0 = tile % a.tiles_d * BN;
   const int64_t t0 = seg * a.per;
   const int64_t t1 = t0 + a.per < a.T ? t0 + a.per : a.T;
-  const int stages = t1 > t0 ? (int)((t1 - t0 + WG_BK - 1) / WG_BK) : 0;
 
-  i32x4_t ra[NA];
-  i32x2_t rb[NB];
-  uint32_t rs[NB];
-  auto fetch = [&](int64_t t) __attribute__((always_inline)) {
+  // A thread's vectors of a stage lie a fixed number of token rows apart: one offset per operand is
+  // held, the others are formed at each fetch. The buffers end with the segment's last token, so that rows past it read zeros;
+  // columns past O or D read other elements of the matrix and reach only results that are not stored.
+  constexpr int KA = 256 / (BM / 8), KB = 256 / (BN / 8);  // token rows between a thread's vectors
+  const int ka = tid / (BM / 8), ca = tid % (BM / 8) * 8, kb = tid / (BN / 8), cb = tid % (BN / 8) * 8;
+  const int sd = a.D / 32, lda = (int)a.ldy * 2;
+  const int offa = ka * lda + 2 * ca, offb = kb * a.D + cb, offs = kb * sd + cb / 32;
+  i32x4_t ra[AHEAD][NA];
+  i32x2_t rb[AHEAD][NB];
+  uint32_t rs[AHEAD][NB];
+  auto fetch = [&](int64_t t, int r) __attribute__((always_inline)) {
+    const int rows = t1 - t > 0 ? (int)(t1 - t < 2 * WG_BK ? t1 - t : 2 * WG_BK) : 0;   // (a stage reads WG_BK)
+    const auto bufa = buffer_rsrc(a.dY + t * a.ldy + o0, rows ? (rows - 1) * lda + 2 * (a.O - o0) : 0);
+    const auto bufb = buffer_rsrc(a.codes + t * a.D + d0, rows ? rows * a.D - d0 : 0);
+    const auto bufs = buffer_rsrc(a.scales + t * sd + d0 / 32, rows ? rows * sd - d0 / 32 : 0);
+    int oa = offa, ob = offb, os = offs;
+    asm volatile("" : "+v"(oa), "+v"(ob), "+v"(os));        // (not hoisted: a register each across the loop)
 #pragma unroll
-    for (int v = 0; v < NA; ++v) {
-      const int k = (tid + 256 * v) / (BM / 8), c = (tid + 256 * v) % (BM / 8) * 8;
-      ra[v] = i32x4_t{0, 0, 0, 0};
-      if (t + k < t1 && o0 + c < a.O) ra[v] = *(const i32x4_t*)(a.dY + (t + k) * a.ldy + o0 + c);
-    }
+    for (int v = 0; v < NA; ++v) ra[r][v] = buffer_load16(bufa, oa + v * KA * lda);
 #pragma unroll
     for (int v = 0; v < NB; ++v) {
-      const int k = (tid + 256 * v) / (BN / 8), c = (tid + 256 * v) % (BN / 8) * 8;
-      rb[v] = i32x2_t{0, 0};
-      rs[v] = 0;
-      if (t + k < t1 && d0 + c < a.D) {
-        rb[v] = *(const i32x2_t*)(a.codes + (t + k) * a.D + d0 + c);
-        rs[v] = a.scales[(t + k) * (a.D / 32) + (d0 + c) / 32];
-      }
+      rb[r][v] = __builtin_amdgcn_raw_buffer_load_b64(bufb, ob + v * KB * a.D, 0, 0);
+      rs[r][v] = __builtin_amdgcn_raw_buffer_load_b8(bufs, os + v * KB * sd, 0, 0);
     }
   };
-  auto put = [&](int b) __attribute__((always_inline)) {
+  auto put = [&](int b, int r) __attribute__((always_inline)) {
 #pragma unroll
-    for (int v = 0; v < NA; ++v) {
-      const int k = (tid + 256 * v) / (BM / 8), c = (tid + 256 * v) % (BM / 8) * 8;
-      *(i32x4_t*)&la[b][k * PA + c] = ra[v];
-    }
+    for (int v = 0; v < NA; ++v) *(i32x4_t*)&la[b][(ka + v * KA) * PA + ca] = ra[r][v];
 #pragma unroll
     for (int v = 0; v < NB; ++v) {
-      const int k = (tid + 256 * v) / (BN / 8), c = (tid + 256 * v) % (BN / 8) * 8;
-      const float s = e8m0_to_f32(rs[v]);
+      const float s = u2f(rs[r][v] << 23);                  // (the conversion takes the exponent field alone)
       i32x4_t w;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int q = rb[v][h];
+        const int q = rb[r][v][h];
         w[2 * h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, false));
         w[2 * h + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(q, s, true));
       }
-      *(i32x4_t*)&lb[b][k * PB + c] = w;
+      *(i32x4_t*)&lb[b][(kb + v * KB) * PB + cb] = w;
     }
   };
 
@@ -279,34 +287,68 @@ __global__ __launch_bounds__(256) void k_ckpt8_wgrad(WgradArgs a) {
   const int no = (wave & 1) * 32 * NF + 16 * (g & 1) + 4 * (j16 & 3);
   const int ko = 8 * (g >> 1) + (j16 >> 2);
 
-  if (stages) {
-    fetch(t0);
-    put(0);
-  }
-  __syncthreads();
-  for (int s = 0; s < stages; ++s) {
-    const int b = s & 1;
-    if (s + 1 < stages) fetch(t0 + (int64_t)(s + 1) * WG_BK);
+  s16x8_t fa[2][MF], fb[2][NF];
+  auto frags = [&](int b, int kk, int f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int kk = 0; kk < WG_BK; kk += 16) {
-      s16x8_t fa[MF], fb[NF];
-#pragma unroll
-      for (int i = 0; i < MF; ++i) {
-        const uint16_t* p = &la[b][(kk + ko) * PA + mo + 32 * i];
-        fa[i] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PA));
-      }
-#pragma unroll
-      for (int j = 0; j < NF; ++j) {
-        const uint16_t* p = &lb[b][(kk + ko) * PB + no + 32 * j];
-        fb[j] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PB));
-      }
-#pragma unroll
-      for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(fa[i], fb[j], acc[i][j]);
+    for (int i = 0; i < MF; ++i) {
+      const uint16_t* p = &la[b][(kk + ko) * PA + mo + 32 * i];
+      fa[f][i] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PA));
     }
-    if (s + 1 < stages) put(b ^ 1);
+#pragma unroll
+    for (int j = 0; j < NF; ++j) {
+      const uint16_t* p = &lb[b][(kk + ko) * PB + no + 32 * j];
+      fb[f][j] = join(lds_read_tr16(p), lds_read_tr16(p + 4 * PB));
+    }
+  };
+  auto products = [&](int f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int j = 0; j < NF; ++j) acc[i][j] = mfma_bf16(fa[f][i], fb[f][j], acc[i][j]);
+  };
+
+  // Stage s: the second half's fragments are read under the first half's products, the next stage goes
+  // to LDS and the one AHEAD stages later is fetched into its registers; behind the barrier the next
+  // stage's first fragments are read under the second half's products. (fetch and put past the last
+  // stage move zeros.)
+  auto stage = [&](int64_t t, auto b) __attribute__((always_inline)) {
+    const int B = b, RS = AHEAD == 2 ? B ^ 1 : 0;
+    frags(B, 16, 1);
+    products(0);
+    put(B ^ 1, RS);
+    fetch(t + (AHEAD + 1) * WG_BK, RS);
+    // one product, then a share of the rest: an LDS read, conversions, an LDS write, a load
+#pragma unroll
+    for (int i = 0; i < MF * NF; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2 * (MF + NF) / (MF * NF) > 0 ? 2 * (MF + NF) / (MF * NF) : 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
     __syncthreads();
+    frags(B ^ 1, 0, 0);
+    products(1);
+#pragma unroll
+    for (int i = 0; i < MF * NF; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    }
+  };
+  fetch(t0, 0);
+  put(0, 0);
+  fetch(t0 + WG_BK, AHEAD - 1);                             // (AHEAD = 2: stage s in registers s & 1)
+  if constexpr (AHEAD == 2) fetch(t0 + 2 * WG_BK, 0);
+  __syncthreads();
+  frags(0, 0, 0);
+  if constexpr (AHEAD == 2) {                               // (the register sets named at compile time)
+    for (int64_t t = t0; t < t1; t += 2 * WG_BK) {
+      stage(t, std::integral_constant<int, 0>{});
+      if (t + WG_BK < t1) stage(t + WG_BK, std::integral_constant<int, 1>{});
+    }
+  } else {
+    int b = 0;
+    for (int64_t t = t0; t < t1; t += WG_BK, b ^= 1) stage(t, b);
   }
 
   float* out = a.segs > 1 ? a.part + (int64_t)seg * a.O * a.D : a.dW;
@@ -326,16 +368,28 @@ __global__ __launch_bounds__(256) void k_ckpt8_wgrad(WgradArgs a) {
       }
 }
 
-// dW = (accumulate ? dW : 0) + the segments' partials, in their order
+// dW = (accumulate ? dW : 0) + the segments' partials. Thread (x, y) of a block of 64 x 4 sums the
+// partials y, y + 4, .. of vector x; the four sums are added in the order of y.
 __global__ __launch_bounds__(256) void k_wgrad_join(const float* part, float* dW, int64_t n4, int segs, int accumulate) {
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    f32x4_t s = accumulate ? ((const f32x4_t*)dW)[i] : f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int g = 0; g < segs; ++g) {
-      const f32x4_t p = ((const f32x4_t*)part)[g * n4 + i];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += p[e];
+  __shared__ f32x4_t sums[4][64];
+  const int x = (int)threadIdx.x & 63, y = (int)threadIdx.x >> 6;
+  for (int64_t i0 = blockIdx.x * (int64_t)64; i0 < n4; i0 += (int64_t)gridDim.x * 64) {
+    const int64_t i = i0 + x;
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < n4) {
+#pragma unroll 4
+      for (int g = y; g < segs; g += 4) s += ((const f32x4_t*)part)[g * n4 + i];
     }
-    ((f32x4_t*)dW)[i] = s;
+    sums[y][x] = s;
+    __syncthreads();
+    if (y == 0 && i < n4) {
+      s += sums[1][x];
+      s += sums[2][x];
+      s += sums[3][x];
+      if (accumulate) s += ((const f32x4_t*)dW)[i];
+      ((f32x4_t*)dW)[i] = s;
+    }
+    __syncthreads();
   }
 }
 
@@ -393,20 +447,37 @@ int run_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy,
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
 
-// Tiles of 128 x 128; the tokens split so that every CU has a few blocks, none below 512 tokens.
+// Tile (128 x 128 or 256 x 256) and number of token segments by the time they are expected to take, in
+// nanoseconds: a block's fixed part, its stages at the rate that one or several blocks per CU reach,
+// and the join's launch and traffic (coefficients fitted to timings between 64 x 64 and 4096 x 4096).
+// The large tile reads LDS half as often per product, the small one fills the device with less
+// splitting: 16384 tokens take 265 us with 256 x 256 and 324 with 128 x 128 at 2048 x 4096, and 44
+// against 37 at 768 x 768.
 WgradLayout wgrad_layout(int64_t T, int O, int D) {
-  WgradLayout s{};
-  s.tiles_o = (O + 127) / 128;
-  s.tiles_d = (D + 127) / 128;
-  const int64_t tiles = (int64_t)s.tiles_o * s.tiles_d;
-  int64_t segs = (2 * device_cus() + tiles - 1) / tiles;
-  const int64_t most = T / 512 > 0 ? T / 512 : 1;
-  if (segs > most) segs = most;
-  s.per = ((T + segs - 1) / segs + WG_BK - 1) / WG_BK * WG_BK;
-  if (s.per < WG_BK) s.per = WG_BK;
-  s.segs = T > 0 ? (int)((T + s.per - 1) / s.per) : 1;
-  s.total = s.segs > 1 ? (size_t)s.segs * O * D * 4 : 256;
-  return s;
+  const int cus = device_cus();
+  WgradLayout best{};
+  double least = 0.0;
+  for (int big = 0; big < 2; ++big) {
+    const int tile = big ? 256 : 128;
+    const int64_t to = (O + tile - 1) / tile, td = (D + tile - 1) / tile, tiles = to * td;
+    const int64_t stages = (T + WG_BK - 1) / WG_BK;
+    for (int64_t segs = 1; segs <= 256 && (segs == 1 || (segs <= stages && tiles * segs <= 4 * cus)); ++segs) {
+      const int64_t per = (stages + segs - 1) / segs, used = per ? (stages + per - 1) / per : 1;
+      if (used != segs && segs > 1) continue;
+      const int64_t blocks = tiles * segs, most = (blocks + cus - 1) / cus;   // blocks on the fullest CU
+      double ns;
+      if (big) ns = 9000.0 + (double)most * per * 1000.0;
+      else ns = 5000.0 + (double)(most / 2) * per * 640.0 + (double)(most % 2) * per * 530.0;
+      if (segs > 1) ns += 3000.0 + (double)segs * O * D * (8.0 / 6000.0);
+      if (least == 0.0 || ns < least) {
+        least = ns;
+        best.big = big; best.tiles_o = (int)to; best.tiles_d = (int)td; best.segs = (int)segs; best.per = per * WG_BK;
+      }
+    }
+  }
+  if (best.per < WG_BK) best.per = WG_BK;
+  best.total = best.segs > 1 ? (size_t)best.segs * O * D * 4 : 256;
+  return best;
 }
 
 int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O, int D,
@@ -414,11 +485,16 @@ int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uin
   WgradArgs a{};
   a.dY = (const uint16_t*)dY; a.ldy = ldy; a.codes = codes; a.scales = scales; a.T = T; a.O = O; a.D = D;
   a.dW = dW; a.accumulate = accumulate; a.segs = s.segs; a.per = s.per; a.part = (float*)workspace; a.tiles_d = s.tiles_d;
-  hipLaunchKernelGGL((k_ckpt8_wgrad<2, 2>), dim3((unsigned)(s.tiles_o * s.tiles_d * s.segs)), dim3(256), 0, st, a);
+  a.tiles = s.tiles_o * s.tiles_d;
+  const dim3 grid((unsigned)((int64_t)s.tiles_o * s.tiles_d * s.segs));
+  if (s.big)
+    hipLaunchKernelGGL((k_ckpt8_wgrad<4, 4, 1>), grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((k_ckpt8_wgrad<2, 2, 2>), grid, dim3(256), 0, st, a);
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   if (s.segs > 1) {
     const int64_t n4 = (int64_t)O * D / 4;
-    ELMO_LAUNCH(k_wgrad_join, n4, st, (const float*)workspace, dW, n4, s.segs, accumulate);
+    ELMO_LAUNCH(k_wgrad_join, 4 * n4, st, (const float*)workspace, dW, n4, s.segs, accumulate);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   }
   return ELMO_OK_;

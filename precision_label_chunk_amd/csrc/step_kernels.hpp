@@ -120,7 +120,7 @@ int run_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const 
                   const void* X, int N, int64_t ldx, void* Y, int ytype, int64_t ldy, hipStream_t st);
 
 // activations kept in 8 bits (E4M3 with an E8M0 scale per 32 features) and their use in the backward
-struct WgradLayout { int tiles_o, tiles_d, segs; int64_t per; size_t total; };
+struct WgradLayout { int big, tiles_o, tiles_d, segs; int64_t per; size_t total; };
 int run_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes, uint8_t* scales,
                    void* y, int64_t ldy, hipStream_t st);
 int run_ckpt8_load(const uint8_t* codes, const uint8_t* scales, int64_t T, int D, void* x, int type, int64_t ldx,
