@@ -280,7 +280,19 @@ def kahan_update(w, c, g, lr):
 
 
 # ---- language-model operators --------------------------------------------------------------------
+# A call on small operands is a few microseconds of device time, so these bindings keep the host's
+# part short: the raw stream handle, whole numbers for pointers, one check per property.
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # ELMO_T_F32, ELMO_T_BF16, ELMO_T_F16
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(device) -> int:
+    """The handle of the current stream of a tensor's device, which must be the current device."""
+    if device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _etype(t: torch.Tensor) -> int:
@@ -291,7 +303,7 @@ def _etype(t: torch.Tensor) -> int:
 
 
 def _rows(name, t: torch.Tensor):
-    """(rows, columns, row pitch) of a matrix on the current GPU whose rows have adjacent elements."""
+    """(rows, columns, row pitch) of a CUDA matrix whose rows have adjacent elements."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     n, v = t.shape
@@ -304,9 +316,13 @@ def _like(name, t, shape, dtype, device):
     """t as an argument of exactly this shape and type (contiguous, on `device`), or None."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
     return t
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 class LogProbs(NamedTuple):
@@ -332,8 +348,7 @@ def logprobs(Z, ids=None, k=0, workspace=None) -> LogProbs:
     if not 0 <= k <= min(64, V) or M > 64 or V < 1:
         raise ElmoError("elmo_logprobs", -2)
     logp = torch.empty((N, M), dtype=torch.float32, device=dev)
-    stats = torch.empty((3, N), dtype=torch.float32, device=dev)
-    entropy, row_max, log_sum = stats.unbind(0)
+    entropy, row_max, log_sum = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
     idx = torch.empty((N, k), dtype=torch.int32, device=dev) if k else None
     top = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
     if N:
@@ -341,9 +356,9 @@ def logprobs(Z, ids=None, k=0, workspace=None) -> LogProbs:
         if workspace is None or workspace.numel() < need:
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         _chk("elmo_logprobs", lib().elmo_logprobs(
-            Z.data_ptr(), e, N, V, ld, _ptr(ids) if M else None, M, k, _ptr(logp) if M else None, entropy.data_ptr(),
-            row_max.data_ptr(), log_sum.data_ptr(), _ptr(idx), _ptr(top), workspace.data_ptr(), workspace.numel(),
-            _stream()))
+            Z.data_ptr(), e, N, V, ld, _at(ids) if M else None, M, k, _at(logp) if M else None, entropy.data_ptr(),
+            row_max.data_ptr(), log_sum.data_ptr(), _at(idx), _at(top), workspace.data_ptr(), workspace.numel(),
+            _stream_of(dev)))
     return LogProbs(logp, entropy, row_max, log_sum, idx, top)
 
 
@@ -370,9 +385,9 @@ def logprobs_backward(Z, ids, stats: LogProbs, dlogp, dentropy=None, dlse=None, 
     ldd = _rows("out", out)[2]
     if N:
         _chk("elmo_logprobs_backward", lib().elmo_logprobs_backward(
-            Z.data_ptr(), e, N, V, ld, _ptr(ids) if M else None, M, stats.row_max.data_ptr(), stats.log_sum.data_ptr(),
-            stats.entropy.data_ptr(), _ptr(dlogp) if M else None, _ptr(dentropy), _ptr(dlse), out.data_ptr(), ldd,
-            _stream()))
+            Z.data_ptr(), e, N, V, ld, _at(ids) if M else None, M, stats.row_max.data_ptr(), stats.log_sum.data_ptr(),
+            stats.entropy.data_ptr(), _at(dlogp) if M else None, _at(dentropy), _at(dlse), out.data_ptr(), ldd,
+            _stream_of(dev)))
     return out
 
 
@@ -411,8 +426,8 @@ def w4_matvec(W, X, wfmt=ELMO_W_MXFP4, scales=None, zeros=None, out_dtype=torch.
     ldy = _rows("out", out)[2]
     if N and L:
         _chk("elmo_w4_matvec", lib().elmo_w4_matvec(
-            W.data_ptr(), wfmt, L, D, group, _ptr(scales), _ptr(zeros), X.data_ptr(), N, ldx, out.data_ptr(),
-            _etype(out), ldy, _stream()))
+            W.data_ptr(), wfmt, L, D, group, _at(scales), _at(zeros), X.data_ptr(), N, ldx, out.data_ptr(),
+            _etype(out), ldy, _stream_of(dev)))
     return out
 
 
@@ -444,7 +459,7 @@ def ckpt8_save(x, act=None):
     scales = torch.empty((T, D // 32), dtype=torch.uint8, device=x.device)
     y = torch.empty((T, D), dtype=x.dtype, device=x.device) if a else None
     _chk("elmo_ckpt8_save", lib().elmo_ckpt8_save(x.data_ptr(), e, T, D, ld, a, codes.data_ptr(), scales.data_ptr(),
-                                                  _ptr(y), D, _stream()))
+                                                  _at(y), D, _stream_of(x.device)))
     return codes, scales, y
 
 
@@ -456,7 +471,8 @@ def ckpt8_load(codes, scales, dtype=torch.bfloat16, out=None):
     elif tuple(out.shape) != (T, D) or out.device != codes.device:
         raise ValueError("out must be [T, D] on the codes' device")
     _chk("elmo_ckpt8_load", lib().elmo_ckpt8_load(codes.data_ptr(), scales.data_ptr(), T, D, out.data_ptr(),
-                                                  _etype(out), _rows("out", out)[2], _stream()))
+                                                  _etype(out), _rows("out", out)[2],
+                                                  _stream_of(codes.device)))
     return out
 
 
@@ -472,7 +488,7 @@ def ckpt8_act_grad(dy, codes, scales, act, out=None):
         raise ValueError("out must have dy's shape, type and device")
     _chk("elmo_ckpt8_act_grad", lib().elmo_ckpt8_act_grad(
         dy.data_ptr(), e, T, D, _rows("dy", dy)[2], a, codes.data_ptr(), scales.data_ptr(), out.data_ptr(),
-        _rows("out", out)[2], _stream()))
+        _rows("out", out)[2], _stream_of(codes.device)))
     return out
 
 
@@ -497,7 +513,7 @@ def ckpt8_weight_grad(dy, codes, scales, out=None, accumulate=False, workspace=N
         workspace = torch.empty((need,), dtype=torch.uint8, device=dy.device)
     _chk("elmo_ckpt8_weight_grad", lib().elmo_ckpt8_weight_grad(
         dy.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), T, O, D, out.data_ptr(), int(accumulate),
-        workspace.data_ptr(), workspace.numel(), _stream()))
+        workspace.data_ptr(), workspace.numel(), _stream_of(codes.device)))
     return out
 
 

@@ -13,6 +13,10 @@
 // A block of 4 waves takes a contiguous segment of a row, each wave a contiguous quarter; short
 // batches split every row over several blocks whose (m, s, t) and candidate keys a second kernel
 // joins in a fixed order.
+//
+// Bound by HBM: 4096 rows of 131072 BF16 logits in 180 us (5.95 TB/s), 256 rows of 670000 FP32 logits
+// in 112 us (6.1 TB/s). With alternatives the comparisons come close to the arithmetic that the read
+// hides: top 5 of the FP32 rows 118 us, top 20 of the BF16 rows 202 us, top 64 253 us.
 #include "elem_types.hpp"
 #include "step_kernels.hpp"
 #include "wave_top.hpp"
@@ -102,48 +106,64 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t n, const
     if (id >= 0) lp = id < a.V ? row_logp(r, E::load(z + id)) : __builtin_nanf("");
     a.logp[n * a.M + j] = lp;
   }
-  if (tid < a.k) {                                          // k <= 64: the first wave ranks the keys
-    const uint64_t q = keys[tid];
-    int rank = 0;
-    for (int i = 0; i < a.k; ++i) rank += keys[i] > q;
+  if (tid < a.k) {
+    const uint64_t q = keys[tid];                           // (best first)
     const uint32_t o = (uint32_t)(q >> 32);
-    a.top_idx[n * a.k + rank] = (int32_t)~(uint32_t)q;
-    a.top_logp[n * a.k + rank] = o == 0 ? __builtin_nanf("") : row_logp(r, value_of(o));
+    a.top_idx[n * a.k + tid] = (int32_t)~(uint32_t)q;
+    a.top_logp[n * a.k + tid] = o == 0 ? __builtin_nanf("") : row_logp(r, value_of(o));
   }
 }
 
-// joins the waves of a block: the sums into every thread, the keys into buf[0]'s first k slots
-__device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, SoftPart* sums, int* cnts,
-                                           uint64_t (*buf)[WaveTop::CAP]) {
+// LDS of a block
+template <bool TOP>
+struct LogprobShared {
+  uint64_t buf[TOP ? LP_WAVES : 1][TOP ? WaveTop::CAP : 1];
+  uint64_t best[64];
+  SoftPart sums[LP_WAVES];
+  int cnts[LP_WAVES];
+  uint32_t floors[LP_WAVES];                                // each wave's (k / 4)-th largest lane maximum
+};
+
+// joins the waves of a block: the sums into every thread, the k best keys, best first, into s.best
+// (slots without a key: 0). The keys rank by counting the larger ones, two per thread.
+template <bool TOP>
+__device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, LogprobShared<TOP>& s) {
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
   wave_join(p);
-  if (top.k) top.cut();
-  if (lane == 0) { sums[wave] = p; cnts[wave] = top.cnt; }
+  if constexpr (TOP)
+    if (top.cnt > WaveTop::MOST) top.cut();
+  if (lane == 0) { s.sums[wave] = p; s.cnts[wave] = top.cnt; }
   __syncthreads();
-  SoftPart q = sums[0];
+  SoftPart q = s.sums[0];
 #pragma unroll
-  for (int w = 1; w < LP_WAVES; ++w) q.m = __builtin_fmaxf(q.m, sums[w].m);
+  for (int w = 1; w < LP_WAVES; ++w) q.m = __builtin_fmaxf(q.m, s.sums[w].m);
   const float m = q.m;
-  q.m = sums[0].m;
+  q.m = s.sums[0].m;
   soft_move(q, m);
 #pragma unroll
   for (int w = 1; w < LP_WAVES; ++w) {
-    SoftPart o = sums[w];
+    SoftPart o = s.sums[w];
     soft_move(o, m);
     q.s += o.s;
     q.t += o.t;
   }
   p = q;
-  if (top.k) {
-    if (wave == 0) {                                        // at most 64 keys of each of the four waves
-      for (int w = 1; w < LP_WAVES; ++w) {
-        const int c = cnts[w];
-        if (lane < c) top.buf[top.cnt + lane] = buf[w][lane];
-        top.cnt += c;
+  if constexpr (TOP) {
+    const uint64_t a = lane < top.cnt ? s.buf[wave][lane] : 0, b = 64 + lane < top.cnt ? s.buf[wave][64 + lane] : 0;
+    int ra = 0, rb = 0, total = 0;
+    for (int w = 0; w < LP_WAVES; ++w) {
+      const int c = s.cnts[w];
+      total += c;
+#pragma unroll 4
+      for (int i = 0; i < c; ++i) {
+        const uint64_t o = s.buf[w][i];
+        ra += o > a;
+        rb += o > b;
       }
-      top.cut();
-      if (lane == 0) cnts[0] = top.cnt;
     }
+    if (a && ra < top.k) s.best[ra] = a;
+    if (b && rb < top.k) s.best[rb] = b;
+    if ((int)threadIdx.x >= total && (int)threadIdx.x < top.k) s.best[threadIdx.x] = 0;
     __syncthreads();
   }
 }
@@ -151,9 +171,7 @@ __device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, SoftPart* 
 template <typename E, bool TOP>
 __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
   constexpr int VEC = E::VEC, U = 4;                        // U vectors of 16 bytes per lane in flight
-  __shared__ uint64_t buf[TOP ? LP_WAVES : 1][WaveTop::CAP];
-  __shared__ SoftPart sums[LP_WAVES];
-  __shared__ int cnts[LP_WAVES];
+  __shared__ LogprobShared<TOP> s;
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
   const int64_t n = blockIdx.x / a.segs;
   const int seg = (int)(blockIdx.x % a.segs);
@@ -174,7 +192,11 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
   const float ninf = -__builtin_inff();
   SoftPart p{ninf, 0.0f, 0.0f};
   WaveTop top;
-  top.init(buf[TOP ? wave : 0], TOP ? a.k : 0);
+  top.init(s.buf[TOP ? wave : 0], TOP ? a.k : 0);
+  if constexpr (TOP) {
+    if (threadIdx.x < LP_WAVES) s.floors[threadIdx.x] = 0;
+    __syncthreads();
+  }
 
   // single elements: lane l takes element e0 + l of c
   auto singles = [&](int64_t e0, int c) __attribute__((always_inline)) {
@@ -183,12 +205,13 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
     soft_move(p, __builtin_fmaxf(p.m, v));
     soft_add(p, v, soft_ref(p.m));
     if constexpr (TOP) {
-      top.begin_step();
-      top.push(in && top.wants(v), key_of(v, (uint32_t)(e0 + lane)));
+      top.threshold(top.bound);
+      top.push(in && top.wants(v), key_of(v, (uint32_t)(e0 + lane)));   // (at most 7: there is room)
     }
   };
   if (me == 0 && head) singles(0, head);
 
+  uint32_t chunks = 1;
   auto chunk = [&](int v, auto whole) __attribute__((always_inline)) {
     i32x4_t r[U];
     float f[U][VEC], mx[U];
@@ -200,9 +223,8 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int i = v + 64 * u + lane;
       E::widen(r[u], f[u]);
-      if (!whole && i >= v1) {
+      if (!whole && v + 64 * u + lane >= v1) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f[u][e] = ninf;
       }
@@ -220,12 +242,40 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) soft_add(p, f[u][e], ref);
     if constexpr (TOP) {
-      static_for<0, U>([&](auto u) __attribute__((always_inline)) {                        // (register arrays: expanded at compile time)
+      // (a maximum is one of the values; -inf says nothing: it may stand for none)
+      auto order = [&](float x) __attribute__((always_inline)) { return x == ninf ? 0u : order_of(x); };
+      uint32_t first = 0;
+      if ((chunks & (chunks - 1)) == 0) {                   // after 1, 2, 4, .. chunks
+        const uint32_t o[1] = {order(p.m)};
+        if (chunks == 1) {                                  // (many alternatives: of the vectors' maxima)
+          if (a.k <= 16) first = kth_of_lanes(o, a.k);
+          else {
+            uint32_t ou[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) ou[u] = order(mx[u]);
+            first = kth_of_lanes(ou, a.k);
+          }
+        }
+        const uint32_t least = kth_of_lanes(o, (a.k + LP_WAVES - 1) / LP_WAVES);
+        if (lane == 0) __hip_atomic_store(&s.floors[wave], least, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      }
+      ++chunks;
+      uint32_t least = ~0u;
+#pragma unroll
+      for (int w = 0; w < LP_WAVES; ++w) {
+        const uint32_t fw = __hip_atomic_load(&s.floors[w], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        least = fw < least ? fw : least;
+      }
+      // values of this chunk count if they reach the first bound or the waves' common one (which other
+      // waves' values of larger indices may have set), and have to pass the wave's own
+      const uint32_t reach = order_below(first > least ? first : least);
+      top.threshold(reach > top.bound ? reach : top.bound);
+      static_for<0, U>([&](auto u) __attribute__((always_inline)) {   // (register arrays: expanded at compile time)
         const int i = v + 64 * u + lane;
         const bool in = whole || i < v1;
-        top.begin_step();
         if (__ballot(in && top.wants(mx[u]))) top.push_all(in, f[u], (uint32_t)(head + VEC * i));
       });
+      top.bound = first > top.bound ? first : top.bound;
     }
   };
   int v = v0;
@@ -233,27 +283,24 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
   if (v < v1) chunk(v, std::false_type{});
   if (me == parts - 1 && tail) singles(a.V - tail, tail);
 
-  block_join(p, top, sums, cnts, buf);
+  block_join<TOP>(p, top, s);
   if (a.segs == 1) {
-    write_row<E>(a, n, p, buf[0]);
+    write_row<E>(a, n, p, s.best);
   } else {
     const int64_t at = n * a.segs + seg;
     if (threadIdx.x == 0) a.part[at] = p;
-    if (TOP && (int)threadIdx.x < a.k)
-      a.keys[at * a.k + threadIdx.x] = (int)threadIdx.x < cnts[0] ? buf[0][threadIdx.x] : 0;
+    if (TOP && (int)threadIdx.x < a.k) a.keys[at * a.k + threadIdx.x] = s.best[threadIdx.x];   // (0: no key)
   }
 }
 
 // joins the blocks of a row: part i by thread i % 256, then as the waves of a block
 template <typename E, bool TOP>
 __global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
-  __shared__ uint64_t buf[TOP ? LP_WAVES : 1][WaveTop::CAP];
-  __shared__ SoftPart sums[LP_WAVES];
-  __shared__ int cnts[LP_WAVES];
+  __shared__ LogprobShared<TOP> s;
   const int64_t n = blockIdx.x;
   SoftPart p{-__builtin_inff(), 0.0f, 0.0f};
   WaveTop top;
-  top.init(buf[TOP ? threadIdx.x >> 6 : 0], TOP ? a.k : 0);
+  top.init(s.buf[TOP ? threadIdx.x >> 6 : 0], TOP ? a.k : 0);
   for (int i = (int)threadIdx.x; i < a.segs; i += LP_THREADS) {
     SoftPart o = a.part[n * a.segs + i];
     const float m = __builtin_fmaxf(p.m, o.m);
@@ -265,22 +312,35 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
   if constexpr (TOP) {
     const int total = a.segs * a.k;
     const uint64_t* keys = a.keys + n * total;
-    top.tie = true;                                         // (keys come in no order of their indices)
-    for (int i = (int)(threadIdx.x & ~63u); i < total; i += LP_THREADS) {
-      const int at = i + (int)(threadIdx.x & 63);
-      const uint64_t q = at < total ? keys[at] : 0;         // (0: a segment of fewer than k elements)
+    const int lane = (int)(threadIdx.x & 63), i0 = (int)(threadIdx.x & ~63u);
+    // a common bound first, as in the blocks: the least over the waves of the (k / 4)-th largest lane
+    // maximum
+    uint32_t largest = 0, least = ~0u;
+    for (int i = (int)threadIdx.x; i < total; i += LP_THREADS) {
+      const uint32_t o = (uint32_t)(keys[i] >> 32);
+      largest = o > largest ? o : largest;
+    }
+    const uint32_t o[1] = {largest}, f = kth_of_lanes(o, (a.k + LP_WAVES - 1) / LP_WAVES);
+    if (lane == 0) s.floors[threadIdx.x >> 6] = f;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < LP_WAVES; ++w) least = s.floors[w] < least ? s.floors[w] : least;
+    top.threshold(order_below(least));
+    for (int i = i0; i < total; i += LP_THREADS) {          // (in no order of their indices: a cut lets ties in)
+      const uint64_t q = i + lane < total ? keys[i + lane] : 0;   // (0: a segment of fewer than k elements)
       top.push(q != 0 && top.wants(value_of((uint32_t)(q >> 32))), q);
+      if (top.cnt > WaveTop::CAP - 64) top.cut();
     }
   }
-  block_join(p, top, sums, cnts, buf);
-  write_row<E>(a, n, p, buf[0]);
+  block_join<TOP>(p, top, s);
+  write_row<E>(a, n, p, s.best);
 }
 
 // ---- gradient ------------------------------------------------------------------------------------
 // With upstream gradients g_j of logp_j, gH of H and gL of log s + m (the log partition):
 //   dz_v = p_v (gL - sum_j g_j - gH (log p_v + H)) + sum_{j: id_j = v} g_j,
 // p_v = 2^((z_v - m) log2 e - log2 s). Elementwise, bound by HBM (the logits read, the gradient
-// written). The few elements that a given token names are computed before the block's pass over its
+// written: 4096 x 131072 BF16 in 401 us, 5.35 TB/s). The few elements that a given token names are computed before the block's pass over its
 // segment and written after it, so that dZ may be the logits' own memory; a token given more than
 // once is summed in the order of its places, by the thread of its first.
 struct LogprobGradArgs {
@@ -293,7 +353,7 @@ struct LogprobGradArgs {
 
 template <typename E, bool HAS_H>
 __global__ __launch_bounds__(256) void k_logprobs_grad(LogprobGradArgs a) {
-  constexpr int VEC = E::VEC, U = 2;
+  constexpr int VEC = E::VEC, U = 4;
   typedef typename E::raw raw;
   const int tid = (int)threadIdx.x;
   const int64_t n = blockIdx.x / a.segs;
@@ -378,11 +438,14 @@ __global__ __launch_bounds__(256) void k_logprobs_grad(LogprobGradArgs a) {
 }
 
 // ---- launchers -------------------------------------------------------------------------------------
-// Blocks per row: enough that the device has several waves of blocks, none below 4096 elements.
+// Blocks per row: enough to fill the device several times over, but at least 4096 elements each, and
+// at most 512 (one 8600000-token row with the top 5: 24 us with 512 blocks, 39 with 2048, whose join
+// is one block's work; 26 with 256).
 static int row_segments(int64_t N, int64_t V, int target) {
   int64_t s = (target + N - 1) / N;
   const int64_t most = V / 4096 > 0 ? V / 4096 : 1;
   if (s > most) s = most;
+  if (s > 512) s = 512;
   return (int)(s < 1 ? 1 : s);
 }
 

@@ -2,11 +2,17 @@
 // their indices: value descending, then index ascending, NaN last.
 //
 // Candidates are 64-bit keys in a wave-private LDS buffer: the value as an order-preserving whole
-// number in the upper half (NaN lowest), the complement of the index in the lower, so that keys are
-// distinct and their order is the wanted one. A value is appended only if it can still belong to
-// the k best: the buffer's k-th key so far bounds it from below. When the buffer is nearly full it
-// is cut to its k best, which raises the bound; on values in no particular order n elements are cut
-// about log(n) / log(CAP / k) times, so that nearly every vector is passed over by one comparison.
+// number in the upper half (NaN 0), the complement of the index in the lower, so that keys are
+// distinct and their order is the wanted one. A value is appended only if it can still belong to the
+// k best, that is if it is over a threshold:
+//   * the k-th best key of the buffer when it was last cut to its k best;
+//   * the k-th largest of the lanes' own maxima (k lanes reach it, so k values do), for the first
+//     values;
+//   * the smallest over the block's waves of the (k / 4)-th largest of its lanes' maxima: together the
+//     waves hold k values that reach it. It follows the whole block's values and is published again
+//     whenever a wave has seen twice as many.
+// With it a 131072-value row has about one candidate for every three vectors of 512 values, and the
+// rest are passed over by one comparison each.
 #pragma once
 #include "numerics.hpp"
 
@@ -16,9 +22,10 @@ __device__ __forceinline__ uint32_t order_of(float v) {
   const uint32_t u = f2u(v + 0.0f);                        // -0 counts as +0
   return v != v ? 0u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint32_t o) {    // (o > 0)
-  return u2f((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
-}
+// the value of an order; NaN for orders below that of -inf
+__device__ __forceinline__ float value_of(uint32_t o) { return u2f((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o); }
+// the next smaller order a value can have (that of -0 is never used)
+__device__ __forceinline__ uint32_t order_below(uint32_t o) { return o == 0u ? 0u : o == 0x80000000u ? 0x7ffffffeu : o - 1u; }
 __device__ __forceinline__ uint64_t key_of(float v, uint32_t idx) { return ((uint64_t)order_of(v) << 32) | (uint32_t)~idx; }
 
 __device__ __forceinline__ int lanes_below(uint64_t mask) {
@@ -31,100 +38,108 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// A P that k of the lanes' orders (W per lane; 0: none) reach: the largest with zeros in its low half,
+// or one that exactly k reach; 0 if fewer than k are not 0. (The upper half tells values apart to one
+// part in 256: enough for a bound, at half the steps.)
+template <int W>
+__device__ __forceinline__ uint32_t kth_of_lanes(const uint32_t (&o)[W], int k) {
+  uint32_t P = 0;
+#pragma unroll 1
+  for (uint32_t b = 0x80000000u; b >= 0x10000u; b >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) n += __popcll(__ballot(o[w] >= (P | b)));
+    if (n >= k) P |= b;
+    if (n == k) break;
+  }
+  return P;
+}
+
 struct WaveTop {
-  static constexpr int CAP = 256;                          // keys per wave (4 per lane at a cut)
+  static constexpr int CAP = 384, PER = CAP / 64;          // keys per wave, and per lane at a cut
+  static constexpr int GROUP = 4;                          // values per lane between checks of the room
+  static constexpr int MOST = CAP - 64 * GROUP;            // keys that may stay: 2 per lane
   uint64_t* buf;                                           // LDS, CAP keys
   int k, cnt;
-  bool open;                                               // no bound yet: everything is a candidate
-  bool tie;                                                // a cut since begin_step: equal values may precede
-  float bound;
+  uint32_t bound;                                          // values of later indices matter if above this order
+  float over;                                              // the threshold in force: NaN lets everything pass
 
   __device__ __forceinline__ void init(uint64_t* lds, int k_) {
-    buf = lds; k = k_; cnt = 0; open = true; tie = false; bound = 0.0f;
+    buf = lds; k = k_; cnt = 0; bound = 0; over = __builtin_nanf("");
   }
-  // Values of one step arrive in no order of their indices, so equality with a bound set inside
-  // the step does not exclude; values of later steps have larger indices than all kept ones.
-  __device__ __forceinline__ void begin_step() { tie = false; }
-  __device__ __forceinline__ bool wants(float v) const { return open || v > bound || (tie && v == bound); }
+  __device__ __forceinline__ void threshold(uint32_t o) { over = value_of(o); }
+  // (a NaN value passes any threshold; vectors are only looked at if a number in them does)
+  __device__ __forceinline__ bool wants(float v) const { return !(v <= over); }
 
-  // the wanted ones of the W values f of each lane (indices i0, i0 + 1, ..), one per lane and turn
-  template <int W>
-  __device__ __forceinline__ void push_all(bool in, const float (&f)[W], uint32_t i0) {
-    uint32_t left = 0;
-#pragma unroll
-    for (int e = 0; e < W; ++e) left |= in && wants(f[e]) ? 1u << e : 0u;
-    while (__ballot(left != 0)) {
-      const uint32_t e = left ? (uint32_t)__builtin_ctz(left) : 0u;
-      float v = f[0];
-#pragma unroll
-      for (int j = 1; j < W; ++j) {
-        const float fj = f[j];                             // (read in both arms: the array stays in registers)
-        v = e == (uint32_t)j ? fj : v;
-      }
-      push(left && wants(v), key_of(v, i0 + e));           // (a cut may have raised the bound)
-      left &= left - 1;
-    }
-  }
-  // one candidate per lane (where `want`); all lanes of the wave call it
+  // one candidate per lane (where `want`); the caller sees to the room
   __device__ __forceinline__ void push(bool want, uint64_t key) {
     const uint64_t mask = __ballot(want);
     if (mask == 0) return;
     if (want) buf[cnt + lanes_below(mask)] = key;
     cnt += __popcll(mask);
-    if (cnt > CAP - 64) cut();
+  }
+  // the wanted ones of the W values f of each lane (indices i0, i0 + 1, ..)
+  template <int W>
+  __device__ __forceinline__ void push_all(bool in, const float (&f)[W], uint32_t i0) {
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      push(in && wants(f[e]), key_of(f[e], i0 + e));
+      if (e % GROUP == GROUP - 1 && cnt > MOST) cut();
+    }
   }
 
-  // keep the k best of the cnt <= CAP keys
+  // Keep the k best of the cnt <= CAP keys. The new bound holds for values behind the present vector;
+  // its own values that equal it (their indices may be smaller) are still let in.
   __device__ __forceinline__ void cut() {
     wave_lds_fence();
     if (cnt > k) {
       const int lane = (int)(threadIdx.x & 63);
-      uint32_t hi[4], lo[4];
+      uint32_t hi[PER], lo[PER];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < PER; ++j) {
         const uint64_t q = 64 * j + lane < cnt ? buf[64 * j + lane] : 0;   // (0 is no key: ~index >= 2^31)
         hi[j] = (uint32_t)(q >> 32); lo[j] = (uint32_t)q;
       }
-      // the k-th largest upper half, from its top bit down: the largest P that k keys reach
+      // the k-th largest upper half, from its top bit down: the largest P that k keys reach (or, as soon
+      // as there is one, a P that exactly k reach)
       uint32_t P = 0;
+      int c = 0;
 #pragma unroll 1
-      for (uint32_t b = 0x80000000u; b; b >>= 1) {
-        int c = 0;
+      for (uint32_t b = 0x80000000u; b && c != k; b >>= 1) {
+        int n = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) c += __popcll(__ballot(hi[j] >= (P | b)));
-        if (c >= k) P |= b;
+        for (int j = 0; j < PER; ++j) n += __popcll(__ballot(hi[j] >= (P | b)));
+        if (n >= k) { P |= b; c = n; }
       }
-      int over = 0, equal = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        over += __popcll(__ballot(hi[j] > P));
-        equal += __popcll(__ballot(hi[j] == P && lo[j] != 0));
-      }
-      // of the keys with that upper half, the k - over with the largest lower half (smallest index)
+      // of the keys with that upper half, those with the largest lower halves (smallest indices)
       uint32_t Q = 1;
-      if (over + equal > k) {
-        Q = 0;
-#pragma unroll 1
-        for (uint32_t b = 0x80000000u; b; b >>= 1) {
-          int c = 0;
+      if (c != k) {
+        int above = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) c += __popcll(__ballot(hi[j] == P && lo[j] >= (Q | b)));
-          if (c >= k - over) Q |= b;
+        for (int j = 0; j < PER; ++j) above += __popcll(__ballot(hi[j] > P));
+        Q = 0;
+        c = 0;
+#pragma unroll 1
+        for (uint32_t b = 0x80000000u; b && c != k - above; b >>= 1) {
+          int n = 0;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) n += __popcll(__ballot(hi[j] == P && lo[j] >= (Q | b)));
+          if (n >= k - above) { Q |= b; c = n; }
         }
       }
       wave_lds_fence();
       int at = 0;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const bool keep = hi[j] > P || (hi[j] == P && lo[j] >= Q);
+      for (int j = 0; j < PER; ++j) {
+        const bool keep = lo[j] != 0 && (hi[j] > P || (hi[j] == P && lo[j] >= Q));
         const uint64_t mask = __ballot(keep);
         if (keep) buf[at + lanes_below(mask)] = ((uint64_t)hi[j] << 32) | lo[j];
         at += __popcll(mask);
       }
       cnt = at;
-      open = P == 0;
-      bound = value_of(P);
-      tie = true;
+      bound = P > bound ? P : bound;
+      const float now = value_of(order_below(P));
+      if (!(now <= over)) over = now;                      // (an open threshold is NaN, and so is `now` below -inf)
     }
     wave_lds_fence();
   }
