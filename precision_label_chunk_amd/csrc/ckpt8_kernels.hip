@@ -17,23 +17,38 @@ namespace elmo {
 enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 
 // Phi(x) and e^(-x^2/2), the normal distribution and its unscaled density. With z = |x| / sqrt 2 and
-// t = 1 / (1 + 0.3 z), erfc(z) = e^(-z^2) t P(t), P of degree 8 fitted to erfcx(z) / t over z <= 11
-// for the smallest relative error (2.0e-8); the tail keeps its relative accuracy because nothing is
-// subtracted from 1 there. In binary32 within 9e-7 of Phi relative for |x| < 5, 4e-6 beyond.
+// t = 1 / (1 + c z), erfc(z) / 2 = e^(-z^2) t P(t), P fitted to erfcx(z) / (2 t) over z <= 11 for the
+// smallest relative error; the tail keeps its relative accuracy because nothing is subtracted from 1
+// there. For FP32 outputs c = 0.3 and degree 8 (2.0e-8; in binary32 within 9e-7 of Phi relative for
+// |x| < 5, 4e-6 beyond), for 16-bit ones c = 0.5 and degree 6 (1.7e-6, a two-hundredth of FP16's
+// rounding): the activation is as long as the memory traffic that hides it, and two operations less.
+template <bool FINE>
 __device__ __forceinline__ void normal_parts(float x, float& cdf, float& dens) {
-  const float z = __builtin_fabsf(x) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, z, 1.0f));
-  float p = -0.12955603003501892f;
-  p = __builtin_fmaf(p, t, 0.4857371747493744f);
-  p = __builtin_fmaf(p, t, -0.5126697421073914f);
-  p = __builtin_fmaf(p, t, 0.548213005065918f);
-  p = __builtin_fmaf(p, t, -0.09502958506345749f);
-  p = __builtin_fmaf(p, t, 0.2151077836751938f);
-  p = __builtin_fmaf(p, t, 0.1482861191034317f);
-  p = __builtin_fmaf(p, t, 0.1707238256931305f);
-  p = __builtin_fmaf(p, t, 0.16918741166591644f);
-  dens = __builtin_amdgcn_exp2f(x * x * -0.72134752044448170f);        // -log2(e) / 2
-  const float half = 0.5f * t * p * dens;
+  float t, p;
+  if constexpr (FINE) {
+    t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(x), 0.2121320366859436f, 1.0f));
+    p = -0.06477801501750946f;
+    p = __builtin_fmaf(p, t, 0.2428685873746872f);
+    p = __builtin_fmaf(p, t, -0.2563348710536957f);
+    p = __builtin_fmaf(p, t, 0.274106502532959f);
+    p = __builtin_fmaf(p, t, -0.047514792531728745f);
+    p = __builtin_fmaf(p, t, 0.1075538918375969f);
+    p = __builtin_fmaf(p, t, 0.07414305955171585f);
+    p = __builtin_fmaf(p, t, 0.08536191284656525f);
+    p = __builtin_fmaf(p, t, 0.08459370583295822f);
+  } else {
+    t = __builtin_amdgcn_rcpf(__builtin_fmaf(__builtin_fabsf(x), 0.3535533845424652f, 1.0f));
+    p = 0.04323947802186012f;
+    p = __builtin_fmaf(p, t, -0.17534863948822021f);
+    p = __builtin_fmaf(p, t, 0.19041365385055542f);
+    p = __builtin_fmaf(p, t, 0.021891044452786446f);
+    p = __builtin_fmaf(p, t, 0.13965976238250732f);
+    p = __builtin_fmaf(p, t, 0.13899248838424683f);
+    p = __builtin_fmaf(p, t, 0.14115135371685028f);
+  }
+  const float u = x * 0.84932180028801904f;                // sqrt(log2(e) / 2)
+  dens = __builtin_amdgcn_exp2f(-(u * u));
+  const float half = t * p * dens;
   cdf = x < 0.0f ? half : 1.0f - half;
 }
 // sigma(x) = a (a r) and 1 - sigma(x) = q, without cancellation: with e = e^(-|x|) and r = 1 / (1 + e),
@@ -49,7 +64,7 @@ __device__ __forceinline__ Sigmoid sigmoid_parts(float x) {
   return Sigmoid{a, a * r, neg ? r : e * r};
 }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ float act_value(float x) {
   if constexpr (ACT == ACT_RELU) return x < 0.0f ? 0.0f : x;           // (NaN stays)
   if constexpr (ACT == ACT_SILU) {
@@ -58,12 +73,12 @@ __device__ __forceinline__ float act_value(float x) {
   }
   if constexpr (ACT == ACT_GELU) {
     float cdf, dens;
-    normal_parts(x, cdf, dens);
+    normal_parts<FINE>(x, cdf, dens);
     return x * cdf;
   }
   return x;
 }
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ float act_slope(float x) {
   if constexpr (ACT == ACT_RELU) return x > 0.0f ? 1.0f : x <= 0.0f ? 0.0f : x;
   if constexpr (ACT == ACT_SILU) {
@@ -72,11 +87,13 @@ __device__ __forceinline__ float act_slope(float x) {
   }
   if constexpr (ACT == ACT_GELU) {
     float cdf, dens;
-    normal_parts(x, cdf, dens);
+    normal_parts<FINE>(x, cdf, dens);
     return __builtin_fmaf(x * 0.39894228040143268f, dens, cdf);        // 1 / sqrt(2 pi)
   }
   return 1.0f;
 }
+
+typedef __attribute__((ext_vector_type(2))) short s16x2_t;
 
 // 8 consecutive elements at p, 16-byte aligned
 template <typename E>
@@ -84,10 +101,16 @@ __device__ __forceinline__ void load8(const typename E::raw* p, float (&f)[8]) {
   E::widen(__builtin_nontemporal_load((const i32x4_t*)p), f);
   if constexpr (E::VEC == 4) E::widen(__builtin_nontemporal_load((const i32x4_t*)p + 1), f + 4);
 }
+// Non-temporal stores only where each covers whole lines: FP32 rows take two stores per thread, 32 bytes
+// apart (16384 x 4096 restored in 56 us with plain stores, 97 with non-temporal ones)
 template <typename E>
 __device__ __forceinline__ void store8(typename E::raw* p, const float (&f)[8]) {
-  __builtin_nontemporal_store(E::narrow(f), (i32x4_t*)p);
-  if constexpr (E::VEC == 4) __builtin_nontemporal_store(E::narrow(f + 4), (i32x4_t*)p + 1);
+  if constexpr (E::VEC == 4) {
+    *(i32x4_t*)p = E::narrow(f);
+    *((i32x4_t*)p + 1) = E::narrow(f + 4);
+  } else {
+    __builtin_nontemporal_store(E::narrow(f), (i32x4_t*)p);
+  }
 }
 // the 8 elements that 8 codes stand for; the conversion takes a scale's exponent field alone, which
 // means in E8M0 what it means there (0: 2^-127, 255: NaN)
@@ -131,37 +154,41 @@ __global__ __launch_bounds__(256) void k_ckpt8_save(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
     float f[8];
     load8<E>((const typename E::raw*)a.in + vec_at(i, a.D, a.ldin), f);
-    uint32_t top = 0;
+    uint32_t top = 0;                                       // as whole numbers: signalling NaNs upset v_max_f32
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint32_t m = f2u(f[e]) & 0x7fffffffu;
-      top = m < 0x7f800000u && m > top ? m : top;               // (NaN and infinity set no scale)
+      top = m > top ? m : top;
+    }
+    if (__builtin_expect(top >= 0x7f800000u, 0)) {          // infinity and NaN set no scale
+      top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = f2u(f[e]) & 0x7fffffffu;
+        top = m > top && m < 0x7f800000u ? m : top;
+      }
     }
     const uint32_t t1 = (uint32_t)__shfl_xor((int)top, 1);
     top = t1 > top ? t1 : top;
     const uint32_t t2 = (uint32_t)__shfl_xor((int)top, 2);
     top = t2 > top ? t2 : top;
     const uint32_t code = block_scale_code(top);
-    const float inv = u2f((254u - code) << 23);                 // 2^-X: code <= 247, always normal
+    // the conversion divides by the scale (its exponent field: 0 for 2^-127), exactly, and rounds to nearest
+    // even; no finite element is over 448, and infinity and NaN both give the NaN code
+    const float scale = u2f(code << 23);
     i32x2_t c;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float g[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        g[e] = f[4 * h + e] * inv;                              // exact; at most 448
-        if (!(__builtin_fabsf(g[e]) <= 448.0f)) g[e] = __builtin_nanf("");
-      }
-      int w = 0;
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(g[0], g[1], w, false);
-      w = __builtin_amdgcn_cvt_pk_fp8_f32(g[2], g[3], w, true);
-      c[h] = w;
+      s16x2_t w = {0, 0};
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[4 * h], f[4 * h + 1], scale, false);
+      w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, f[4 * h + 2], f[4 * h + 3], scale, true);
+      c[h] = __builtin_bit_cast(int, w);
     }
-    __builtin_nontemporal_store(c, (i32x2_t*)a.codes + i);
+    ((i32x2_t*)a.codes)[i] = c;
     if ((i & 3) == 0) a.scales[i >> 2] = (uint8_t)code;
     if constexpr (OUT) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = act_value<ACT>(f[e]);
+      for (int e = 0; e < 8; ++e) f[e] = act_value<ACT, E::VEC == 4>(f[e]);
       store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), f);
     }
   }
@@ -184,7 +211,7 @@ __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
     load8<E>((const typename E::raw*)a.in + vec_at(i, a.D, a.ldin), d);
     decode8(__builtin_nontemporal_load((const i32x2_t*)a.codes + i), a.scales[i >> 2], f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) d[e] *= act_slope<ACT>(f[e]);
+    for (int e = 0; e < 8; ++e) d[e] *= act_slope<ACT, E::VEC == 4>(f[e]);
     store8<E>((typename E::raw*)a.out + vec_at(i, a.D, a.ldout), d);
   }
 }

@@ -256,8 +256,10 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
             first = kth_of_lanes(ou, a.k);
           }
         }
-        const uint32_t least = kth_of_lanes(o, (a.k + LP_WAVES - 1) / LP_WAVES);
-        if (lane == 0) __hip_atomic_store(&s.floors[wave], least, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        if (v + 64 * U < v1) {                              // (the last chunk's would bound nothing)
+          const uint32_t mine = kth_of_lanes(o, (a.k + LP_WAVES - 1) / LP_WAVES);
+          if (lane == 0) __hip_atomic_store(&s.floors[wave], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        }
       }
       ++chunks;
       uint32_t least = ~0u;
