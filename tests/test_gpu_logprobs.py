@@ -338,3 +338,26 @@ def test_empty_batch_and_refusals(elmo):
         elmo.logprobs_backward(Z, ids, r, None)
     with pytest.raises(ValueError):
         elmo.logprobs_backward(Z, ids, r, r.logp, out=torch.zeros((2, 49), device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,bits,view", [(torch.float32, 0x7F800001, torch.int32), (torch.bfloat16, 0x7F81, torch.int16),
+                                             (torch.float16, 0x7C01, torch.int16)])
+@pytest.mark.parametrize("k", [4, 40])
+def test_signalling_nan_logits_hide_no_alternative(elmo, dtype, bits, view, k):
+    """Signalling NaNs beside the largest logits: the alternatives are those of the other tokens."""
+    for V in (3000, 40000):
+        g = torch.Generator().manual_seed(V)
+        Z = (torch.randn(2, V, generator=g) * 3).to(dtype)
+        bad = torch.zeros(2, V, dtype=torch.bool)
+        best = Z.float().topk(k, dim=1).indices
+        for n in range(2):
+            for i in best[n].tolist():
+                for j in (i - 1, i + 1, i ^ 4):
+                    if 0 <= j < V and j not in best[n]:
+                        bad[n, j] = True
+        want = torch.sort(torch.where(bad, torch.full_like(Z, -math.inf), Z).float(), dim=1, descending=True, stable=True).indices[:, :k]
+        raw = Z.view(view).clone()
+        raw[bad] = bits
+        r = elmo.logprobs(raw.view(dtype).cuda(), k=k)
+        assert torch.equal(r.top_idx.cpu().long(), want)
+        assert bool(r.entropy.isnan().all())
