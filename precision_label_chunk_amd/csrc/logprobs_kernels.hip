@@ -125,14 +125,18 @@ struct LogprobShared {
 };
 
 // joins the waves of a block: the sums into every thread, the k best keys, best first, into s.best
-// (slots without a key: 0). The keys rank by counting the larger ones, two per thread.
+// (slots without a key: 0). `largest`: the order of the largest value among a lane's (0: none), for a
+// last common bound, which few more than k keys reach; those rank by counting the larger ones.
 template <bool TOP>
-__device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, LogprobShared<TOP>& s) {
+__device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, uint32_t largest, LogprobShared<TOP>& s) {
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
   wave_join(p);
-  if constexpr (TOP)
+  if (lane == 0) s.sums[wave] = p;
+  if constexpr (TOP) {
     if (top.cnt > WaveTop::MOST) top.cut();
-  if (lane == 0) { s.sums[wave] = p; s.cnts[wave] = top.cnt; }
+    const uint32_t o[1] = {largest}, f = kth_of_lanes(o, (top.k + LP_WAVES - 1) / LP_WAVES);
+    if (lane == 0) s.floors[wave] = f;
+  }
   __syncthreads();
   SoftPart q = s.sums[0];
 #pragma unroll
@@ -149,17 +153,21 @@ __device__ __forceinline__ void block_join(SoftPart& p, WaveTop& top, LogprobSha
   }
   p = q;
   if constexpr (TOP) {
+    uint32_t least = ~0u;
+#pragma unroll
+    for (int w = 0; w < LP_WAVES; ++w) least = s.floors[w] < least ? s.floors[w] : least;
+    top.keep_from(least);
+    if (lane == 0) s.cnts[wave] = top.cnt;
+    __syncthreads();
     const uint64_t a = lane < top.cnt ? s.buf[wave][lane] : 0, b = 64 + lane < top.cnt ? s.buf[wave][64 + lane] : 0;
     int ra = 0, rb = 0, total = 0;
     for (int w = 0; w < LP_WAVES; ++w) {
       const int c = s.cnts[w];
       total += c;
 #pragma unroll 4
-      for (int i = 0; i < c; ++i) {
-        const uint64_t o = s.buf[w][i];
-        ra += o > a;
-        rb += o > b;
-      }
+      for (int i = 0; i < c; ++i) ra += s.buf[w][i] > a;
+      if (top.cnt > 64)                                     // (of this wave: uniform)
+        for (int i = 0; i < c; ++i) rb += s.buf[w][i] > b;
     }
     if (a && ra < top.k) s.best[ra] = a;
     if (b && rb < top.k) s.best[rb] = b;
@@ -285,7 +293,7 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
   if (v < v1) chunk(v, std::false_type{});
   if (me == parts - 1 && tail) singles(a.V - tail, tail);
 
-  block_join<TOP>(p, top, s);
+  block_join<TOP>(p, top, p.m == ninf ? 0u : order_of(p.m), s);
   if (a.segs == 1) {
     write_row<E>(a, n, p, s.best);
   } else {
@@ -311,30 +319,24 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
     p.s += o.s;
     p.t += o.t;
   }
+  uint32_t largest = 0;
   if constexpr (TOP) {
     const int total = a.segs * a.k;
     const uint64_t* keys = a.keys + n * total;
     const int lane = (int)(threadIdx.x & 63), i0 = (int)(threadIdx.x & ~63u);
-    // a common bound first, as in the blocks: the least over the waves of the (k / 4)-th largest lane
-    // maximum
-    uint32_t largest = 0, least = ~0u;
     for (int i = (int)threadIdx.x; i < total; i += LP_THREADS) {
       const uint32_t o = (uint32_t)(keys[i] >> 32);
       largest = o > largest ? o : largest;
     }
-    const uint32_t o[1] = {largest}, f = kth_of_lanes(o, (a.k + LP_WAVES - 1) / LP_WAVES);
-    if (lane == 0) s.floors[threadIdx.x >> 6] = f;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < LP_WAVES; ++w) least = s.floors[w] < least ? s.floors[w] : least;
-    top.threshold(order_below(least));
+    const uint32_t o[1] = {largest};
+    if (total > 64 * LP_WAVES) top.threshold(order_below(kth_of_lanes(o, a.k)));
     for (int i = i0; i < total; i += LP_THREADS) {          // (in no order of their indices: a cut lets ties in)
       const uint64_t q = i + lane < total ? keys[i + lane] : 0;   // (0: a segment of fewer than k elements)
       top.push(q != 0 && top.wants(value_of((uint32_t)(q >> 32))), q);
       if (top.cnt > WaveTop::CAP - 64) top.cut();
     }
   }
-  block_join<TOP>(p, top, s);
+  block_join<TOP>(p, top, largest, s);
   write_row<E>(a, n, p, s.best);
 }
 

@@ -88,6 +88,20 @@ struct WaveTop {
     }
   }
 
+  // keep the keys of at least this order; cnt <= MOST
+  __device__ __forceinline__ void keep_from(uint32_t least) {
+    wave_lds_fence();
+    const int lane = (int)(threadIdx.x & 63);
+    const uint64_t a = lane < cnt ? buf[lane] : 0, b = 64 + lane < cnt ? buf[64 + lane] : 0;
+    const bool ka = a != 0 && (uint32_t)(a >> 32) >= least, kb = b != 0 && (uint32_t)(b >> 32) >= least;
+    const uint64_t ma = __ballot(ka), mb = __ballot(kb);
+    wave_lds_fence();
+    if (ka) buf[lanes_below(ma)] = a;
+    if (kb) buf[__popcll(ma) + lanes_below(mb)] = b;
+    cnt = __popcll(ma) + __popcll(mb);
+    wave_lds_fence();
+  }
+
   // Keep the k best of the cnt <= CAP keys. The new bound holds for values behind the present vector;
   // its own values that equal it (their indices may be smaller) are still let in.
   __device__ __forceinline__ void cut() {
