@@ -283,16 +283,16 @@ def kahan_update(w, c, g, lr):
 # A call on small operands is a few microseconds of device time, so these bindings keep the host's
 # part short: the raw stream handle, whole numbers for pointers, one check per property.
 _TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}     # ELMO_T_F32, ELMO_T_BF16, ELMO_T_F16
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(device) -> int:
     """The handle of the current stream of a tensor's device, which must be the current device."""
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+    now = _current_device()
+    if device.index != now:
+        raise ValueError(f"tensors are on {device}, the current device is cuda:{now}")
+    return _raw_stream(now)
 
 
 def _etype(t: torch.Tensor) -> int:
@@ -304,12 +304,13 @@ def _etype(t: torch.Tensor) -> int:
 
 def _rows(name, t: torch.Tensor):
     """(rows, columns, row pitch) of a CUDA matrix whose rows have adjacent elements."""
-    if t.dim() != 2 or not t.is_cuda:
+    if not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D CUDA tensor")
     n, v = t.shape
-    if v > 1 and t.stride(1) != 1:
+    pitch, step = t.stride()
+    if step != 1 and v > 1:
         raise ValueError(f"the elements of a row of {name} must be adjacent (stride 1)")
-    return n, v, (t.stride(0) if n > 1 else v)
+    return n, v, (pitch if n > 1 else v)
 
 
 def _like(name, t, shape, dtype, device):
@@ -347,14 +348,14 @@ def logprobs(Z, ids=None, k=0, workspace=None) -> LogProbs:
     _like("ids", ids, (N, M), torch.int32, dev)
     if not 0 <= k <= min(64, V) or M > 64 or V < 1:
         raise ElmoError("elmo_logprobs", -2)
-    logp = torch.empty((N, M), dtype=torch.float32, device=dev)
-    entropy, row_max, log_sum = torch.empty((3, N), dtype=torch.float32, device=dev).unbind(0)
-    idx = torch.empty((N, k), dtype=torch.int32, device=dev) if k else None
-    top = torch.empty((N, k), dtype=torch.float32, device=dev) if k else None
+    logp = Z.new_empty((N, M), dtype=torch.float32)
+    entropy, row_max, log_sum = Z.new_empty((3, N), dtype=torch.float32).unbind(0)
+    idx = Z.new_empty((N, k), dtype=torch.int32) if k else None
+    top = Z.new_empty((N, k), dtype=torch.float32) if k else None
     if N:
         need = lib().elmo_logprobs_workspace_bytes(N, V, k)
         if workspace is None or workspace.numel() < need:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = Z.new_empty((need,), dtype=torch.uint8)
         _chk("elmo_logprobs", lib().elmo_logprobs(
             Z.data_ptr(), e, N, V, ld, _at(ids) if M else None, M, k, _at(logp) if M else None, entropy.data_ptr(),
             row_max.data_ptr(), log_sum.data_ptr(), _at(idx), _at(top), workspace.data_ptr(), workspace.numel(),
@@ -379,7 +380,7 @@ def logprobs_backward(Z, ids, stats: LogProbs, dlogp, dentropy=None, dlse=None, 
     for name in ("entropy", "row_max", "log_sum"):
         _like(name, getattr(stats, name), (N,), torch.float32, dev)
     if out is None:
-        out = torch.empty((N, V), dtype=Z.dtype, device=dev)
+        out = Z.new_empty((N, V), dtype=Z.dtype)
     elif out.shape != Z.shape or out.dtype != Z.dtype or out.device != dev:
         raise ValueError("out must have Z's shape, type and device")
     ldd = _rows("out", out)[2]
@@ -420,7 +421,7 @@ def w4_matvec(W, X, wfmt=ELMO_W_MXFP4, scales=None, zeros=None, out_dtype=torch.
     if d != D:
         raise ValueError(f"X has {d} features, W {D}")
     if out is None:
-        out = torch.empty((N, L), dtype=out_dtype, device=dev)
+        out = W.new_empty((N, L), dtype=out_dtype)
     elif tuple(out.shape) != (N, L) or out.device != dev:
         raise ValueError("out must be [N, L] on W's device")
     ldy = _rows("out", out)[2]
@@ -442,7 +443,7 @@ def _act(name) -> int:
 
 def _codes(codes, scales):
     """(T, D) of a saved activation."""
-    if codes.dtype != torch.uint8 or codes.dim() != 2 or not codes.is_cuda or not codes.is_contiguous():
+    if not codes.is_cuda or codes.dim() != 2 or codes.dtype != torch.uint8 or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous 2-D uint8 CUDA tensor")
     T, D = codes.shape
     _like("scales", scales, (T, D // 32), torch.uint8, codes.device)
@@ -455,9 +456,9 @@ def ckpt8_save(x, act=None):
     pass, or None without one. See elmo_ckpt8_save in elmo_xmc.h."""
     e, a = _etype(x), _act(act)
     T, D, ld = _rows("x", x)
-    codes = torch.empty((T, D), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((T, D // 32), dtype=torch.uint8, device=x.device)
-    y = torch.empty((T, D), dtype=x.dtype, device=x.device) if a else None
+    codes = x.new_empty((T, D), dtype=torch.uint8)
+    scales = x.new_empty((T, D // 32), dtype=torch.uint8)
+    y = x.new_empty((T, D), dtype=x.dtype) if a else None
     _chk("elmo_ckpt8_save", lib().elmo_ckpt8_save(x.data_ptr(), e, T, D, ld, a, codes.data_ptr(), scales.data_ptr(),
                                                   _at(y), D, _stream_of(x.device)))
     return codes, scales, y
@@ -467,7 +468,7 @@ def ckpt8_load(codes, scales, dtype=torch.bfloat16, out=None):
     """The activations [T, D] that ckpt8_save kept."""
     T, D = _codes(codes, scales)
     if out is None:
-        out = torch.empty((T, D), dtype=dtype, device=codes.device)
+        out = codes.new_empty((T, D), dtype=dtype)
     elif tuple(out.shape) != (T, D) or out.device != codes.device:
         raise ValueError("out must be [T, D] on the codes' device")
     _chk("elmo_ckpt8_load", lib().elmo_ckpt8_load(codes.data_ptr(), scales.data_ptr(), T, D, out.data_ptr(),
@@ -483,7 +484,7 @@ def ckpt8_act_grad(dy, codes, scales, act, out=None):
     if tuple(dy.shape) != (T, D) or dy.device != codes.device:
         raise ValueError("dy must be [T, D] on the codes' device")
     if out is None:
-        out = torch.empty((T, D), dtype=dy.dtype, device=dy.device)
+        out = dy.new_empty((T, D), dtype=dy.dtype)
     elif out.shape != dy.shape or out.dtype != dy.dtype or out.device != dy.device:
         raise ValueError("out must have dy's shape, type and device")
     _chk("elmo_ckpt8_act_grad", lib().elmo_ckpt8_act_grad(
@@ -504,13 +505,13 @@ def ckpt8_weight_grad(dy, codes, scales, out=None, accumulate=False, workspace=N
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((O, D), dtype=torch.float32, device=dy.device)
+        out = dy.new_empty((O, D), dtype=torch.float32)
     _like("out", out, (O, D), torch.float32, codes.device)
     need = int(lib().elmo_ckpt8_weight_grad_workspace_bytes(T, O, D))
     if need == 0:
         raise ElmoError("elmo_ckpt8_weight_grad_workspace_bytes", -2)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dy.device)
+        workspace = dy.new_empty((need,), dtype=torch.uint8)
     _chk("elmo_ckpt8_weight_grad", lib().elmo_ckpt8_weight_grad(
         dy.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), T, O, D, out.data_ptr(), int(accumulate),
         workspace.data_ptr(), workspace.numel(), _stream_of(codes.device)))

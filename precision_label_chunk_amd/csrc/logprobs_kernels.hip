@@ -16,7 +16,7 @@
 //
 // Bound by HBM: 4096 rows of 131072 BF16 logits in 180 us (5.95 TB/s), 256 rows of 670000 FP32 logits
 // in 112 us (6.1 TB/s). With alternatives the comparisons come close to the arithmetic that the read
-// hides: top 5 of the FP32 rows 118 us, top 20 of the BF16 rows 202 us, top 64 253 us.
+// hides: top 5 of the FP32 rows 117 us, top 20 of the BF16 rows 188 us, top 64 222 us.
 #include "elem_types.hpp"
 #include "step_kernels.hpp"
 #include "wave_top.hpp"
@@ -455,7 +455,8 @@ static int row_segments(int64_t N, int64_t V, int target) {
 
 LogprobLayout logprobs_layout(int64_t N, int64_t V, int k) {
   LogprobLayout s{};
-  s.segs = row_segments(N, V, 8 * device_cus());
+  // (4 blocks per CU: 64 rows of 262144 FP32 with the top 20 in 27.5 us, 32 with 8 blocks and 36 with 1)
+  s.segs = row_segments(N, V, 4 * device_cus());
   size_t at = 0;
   auto take = [&](size_t bytes) { const size_t o = at; at += (bytes + 255) & ~(size_t)255; return o; };
   if (s.segs > 1) {
