@@ -45,10 +45,13 @@ struct W4Args {
   const uint16_t* X; int N; int64_t ldx;
   void* Y; int ytype; int64_t ldy;
   int64_t tiles;                      // ceil(L / 16)
+  // the panel of D that a launch takes, in the kernel's units of features: rows of larger products do
+  // not fit LDS at once, and their FP32 results are summed panel by panel
+  int unit0, units, add;
 };
 
 __device__ __forceinline__ void store_result(const W4Args& a, int64_t at, float v) {
-  if (a.ytype == T_F32_) ElemF32::store((float*)a.Y + at, v);
+  if (a.ytype == T_F32_) ElemF32::store((float*)a.Y + at, a.add ? ((const float*)a.Y)[at] + v : v);
   else if (a.ytype == T_BF16_) ElemBF16::store((uint16_t*)a.Y + at, v);
   else ElemF16::store((uint16_t*)a.Y + at, v);
 }
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_mx_lds(W4Args a) {
   extern __shared__ __attribute__((aligned(16))) i32x4_t xs[];      // [D / 8][N], then the joins
   const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, q = lane >> 4;
   const int ks = wave % KS, grp = wave / KS;
-  const int units = a.D / 256;
+  const int units = a.units, chunks = 32 * units;
   const int64_t step = (int64_t)gridDim.x * GR, tile00 = (int64_t)blockIdx.x * GR;
   int64_t tile = tile00 + grp;
 
@@ -176,20 +179,20 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_mx_lds(W4Args a) {
   int64_t lt = tile;
   int lu = ks;
   auto load_next = [&](MxUnit& d) __attribute__((always_inline)) {
-    load_unit(a, mx_row(a, lt < a.tiles ? lt : a.tiles - 1, col), lu, q, d);   // (past the end: read, not used)
+    load_unit(a, mx_row(a, lt < a.tiles ? lt : a.tiles - 1, col), a.unit0 + lu, q, d);   // (past the end: read, not used)
     lu += KS;
     if (lu >= units) { lu = ks; lt += step; }
   };
   load_next(m[0]);
-  for (int i = tid; i < a.D / 8 * a.N; i += 64 * WAVES) {
-    const int n = i / (a.D / 8), c = i % (a.D / 8);        // (consecutive threads read a row)
-    xs[c * a.N + n] = *(const i32x4_t*)(a.X + n * a.ldx + 8 * c);
+  for (int i = tid; i < chunks * a.N; i += 64 * WAVES) {
+    const int n = i / chunks, c = i % chunks;              // (consecutive threads read a row)
+    xs[c * a.N + n] = *(const i32x4_t*)(a.X + n * a.ldx + 256 * a.unit0 + 8 * c);
   }
   __syncthreads();
   const i32x4_t* x0[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) x0[j] = xs + 4 * q * a.N + (16 * j + col < a.N ? 16 * j + col : a.N - 1);
-  float* part = (float*)(xs + a.D / 8 * a.N);
+  float* part = (float*)(xs + chunks * a.N);
   // every wave of a block makes the same number of turns: the joins are barriers
   const int64_t turns = (a.tiles - tile00 + step - 1) / step;
   const int mine = (units - ks + KS - 1) / KS;             // units of this wave per tile (KS <= units)
@@ -233,8 +236,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_mx_lds(W4Args a) {
   }
 }
 
-// Any D: the KS waves of a block share LT tiles, each taking every KS-th unit; the feature rows come
-// from the caches, once per LT tiles. Sums joined through LDS.
+// Feature rows that do not fit LDS, where panels do not serve: KS waves share LT tiles, each taking every KS-th
+// unit; the rows come from the caches, once per LT tiles. Sums joined through LDS.
 template <int NT, int LT, int KS>
 __global__ __launch_bounds__(64 * KS) void k_w4_mx_deep(W4Args a) {
   constexpr int V = LT * NT * 4;
@@ -405,7 +408,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
   extern __shared__ __attribute__((aligned(16))) i32x4_t xs[];
   const int tid = (int)threadIdx.x, wave = tid >> 6, lane = tid & 63, col = lane & 15, q = lane >> 4;
   const int ks = wave % KS, grp = wave / KS, N = a.N;
-  const int units = (a.D + 127) / 128;
+  const int units = a.units;
   const int64_t step = (int64_t)gridDim.x * GR, tile00 = (int64_t)blockIdx.x * GR;
   int64_t tile = tile00 + grp;
   float* sums = (float*)(xs + (units + 1) * 16 * N);
@@ -417,7 +420,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
   auto load_next = [&](IntUnit& d) __attribute__((always_inline)) {
     int64_t label = (lt < a.tiles ? lt : a.tiles - 1) * 16 + col;    // (past the end: read, not used)
     if (label >= a.L) label = a.L - 1;
-    load_int<G>(a, label, lu, q, d);
+    load_int<G>(a, label, a.unit0 + lu, q, d);
     lu += KS;
     if (lu >= units) { lu = ks; lt += step; }
   };
@@ -428,7 +431,7 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
     float sum = 0.0f;
     for (int c = ug * (16 / SB); c < (ug + 1) * (16 / SB); ++c) {
       i32x4_t v = {0, 0, 0, 0};
-      if (8 * c < a.D) v = *(const i32x4_t*)(a.X + n * a.ldx + 8 * c);
+      if (u < units && 128 * a.unit0 + 8 * c < a.D) v = *(const i32x4_t*)(a.X + n * a.ldx + 128 * a.unit0 + 8 * c);
       float f[8];
       ElemBF16::widen(v, f);
 #pragma unroll
@@ -480,7 +483,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
   }
 }
 
-// Any D: the feature rows from the caches, their sums as products against ones.
+// Feature rows that do not fit LDS, where panels do not serve: the rows from the caches, their sums as
+// products against ones.
 template <int G, int NT, bool FEW, int KS>
 __global__ __launch_bounds__(64 * KS) void k_w4_int_deep(W4Args a) {
   constexpr int V = FEW ? 1 : 4 * NT, GU = 128 / G;
@@ -532,13 +536,13 @@ static int go_regs(const W4Args& a, hipStream_t st) {
   hipLaunchKernelGGL(k_w4_mx_regs<UNITS>, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
-static size_t mx_lds_bytes(const W4Args& a, int NT, int KS, int WAVES) {
-  return (size_t)a.D * 2 * a.N + (KS > 1 ? (size_t)2 * WAVES * NT * 1024 : 0);
+static size_t mx_lds_bytes(const W4Args& a, int units, int NT, int KS, int WAVES) {
+  return (size_t)units * 512 * a.N + (KS > 1 ? (size_t)2 * WAVES * NT * 1024 : 0);
 }
 template <int NT, int KS, int WAVES>
 static int go_lds(const W4Args& a, hipStream_t st) {
   constexpr int GR = WAVES / KS;
-  const size_t lds = mx_lds_bytes(a, NT, KS, WAVES);
+  const size_t lds = mx_lds_bytes(a, a.units, NT, KS, WAVES);
   int per_cu = (int)(W4_LDS / lds);
   if (per_cu > 16 / WAVES) per_cu = 16 / WAVES;            // 4 waves per SIMD
   if (per_cu < 1) per_cu = 1;
@@ -554,28 +558,56 @@ static int go_deep(const W4Args& a, hipStream_t st) {
   hipLaunchKernelGGL((k_w4_mx_deep<NT, LT, KS>), dim3((unsigned)((a.tiles + LT - 1) / LT)), dim3(64 * KS), 0, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
+// Runs `go` on panels of `units` units that fit LDS with 8 waves each (lds(n): bytes for n units), as
+// equal as they come, adding the results of all but the first. False, and nothing run, where that takes
+// several panels and either their sums would have to round (16-bit results) or there are too few tiles
+// to be worth staging the rows of each: 24 rows of 4864 features against 113635 integer labels take 142
+// us in panels and 300 with the rows from the caches, 12 rows of 8192 against 4096 labels 25 and 17.
+template <typename B, typename G>
+static bool in_panels(const W4Args& a, int units, B&& lds, G&& go, int& rc) {
+  int most = units;
+  while (most > 1 && lds(most) > W4_LDS) --most;
+  const int panels = (units + most - 1) / most, per = (units + panels - 1) / panels;
+  if (panels > 1 && (a.ytype != T_F32_ || a.tiles <= 4 * device_cus())) return false;
+  rc = ELMO_OK_;
+  for (int u = 0; u < units && rc == ELMO_OK_; u += per) {
+    W4Args p = a;
+    p.unit0 = u;
+    p.units = units - u < per ? units - u : per;
+    p.add = u > 0;
+    rc = go(p);
+  }
+  return true;
+}
+
 template <int NT>
 static int pick_mx(const W4Args& a, hipStream_t st) {
-  const int units = a.D / 256;
-  if (units < 8 && mx_lds_bytes(a, NT, 1, 4) <= W4_LDS) return go_lds<NT, 1, 4>(a, st);
-  // where only one block fits a CU, 16 waves of it hide more latency than 8, unless there are too few
-  // tiles to give both groups a share
-  if (units >= 8 && 2 * mx_lds_bytes(a, NT, 8, 8) > W4_LDS && a.tiles >= 4 * device_cus() &&
-      mx_lds_bytes(a, NT, 8, 16) <= W4_LDS)
-    return go_lds<NT, 8, 16>(a, st);
-  if (units >= 8 && mx_lds_bytes(a, NT, 8, 8) <= W4_LDS) return go_lds<NT, 8, 8>(a, st);
-  return go_deep<NT, 2, 8>(a, st);
+  int rc;
+  const bool done = in_panels(
+      a, a.D / 256, [&](int n) { return mx_lds_bytes(a, n, NT, n < 8 ? 1 : 8, 8); },
+      [&](const W4Args& p) {
+        if (p.units < 8)
+          return 2 * mx_lds_bytes(p, p.units, NT, 1, 4) > W4_LDS ? go_lds<NT, 1, 16>(p, st) : go_lds<NT, 1, 4>(p, st);
+        // where only one block fits a CU, 16 waves of it hide more latency than 8, unless there are too
+        // few tiles to give both groups a share
+        if (2 * mx_lds_bytes(p, p.units, NT, 8, 8) > W4_LDS && p.tiles >= 4 * device_cus() &&
+            mx_lds_bytes(p, p.units, NT, 8, 16) <= W4_LDS)
+          return go_lds<NT, 8, 16>(p, st);
+        return go_lds<NT, 8, 8>(p, st);
+      },
+      rc);
+  return done ? rc : go_deep<NT, 2, 8>(a, st);
 }
 
 template <int G, int NT, bool FEW, int KS, int WAVES>
-static size_t int_lds_bytes(const W4Args& a) {
-  const size_t units = (a.D + 127) / 128, sums = FEW ? 64 : (128 / G) * NT * 64;
-  return (units + 1) * (256 * a.N + sums) + (KS > 1 ? (size_t)(WAVES == 16 ? 1 : 2) * WAVES * (FEW ? 1 : 4 * NT) * 256 : 0);
+static size_t int_lds_bytes(const W4Args& a, int units) {
+  const size_t sums = FEW ? 64 : (128 / G) * NT * 64;
+  return ((size_t)units + 1) * (256 * a.N + sums) + (KS > 1 ? (size_t)(WAVES == 16 ? 1 : 2) * WAVES * (FEW ? 1 : 4 * NT) * 256 : 0);
 }
 template <int G, int NT, bool FEW, int KS, int WAVES>
 static int go_int(const W4Args& a, hipStream_t st) {
   constexpr int GR = WAVES / KS;
-  const size_t lds = int_lds_bytes<G, NT, FEW, KS, WAVES>(a);
+  const size_t lds = int_lds_bytes<G, NT, FEW, KS, WAVES>(a, a.units);
   int per_cu = (int)(W4_LDS / lds);
   if (per_cu > 24 / WAVES) per_cu = 24 / WAVES;            // 6 waves per SIMD (65536 x 4096, one row: 36.5 us; at 4: 41.7)
   if (per_cu < 1) per_cu = 1;
@@ -588,12 +620,19 @@ static int go_int(const W4Args& a, hipStream_t st) {
 }
 template <int G, int NT, bool FEW>
 static int pick_int(const W4Args& a, hipStream_t st) {
-  const int units = (a.D + 127) / 128;
-  if (units < 8 && int_lds_bytes<G, NT, FEW, 1, 4>(a) <= W4_LDS) return go_int<G, NT, FEW, 1, 4>(a, st);
-  if (units >= 8 && 2 * int_lds_bytes<G, NT, FEW, 8, 8>(a) > W4_LDS && a.tiles >= 4 * device_cus() &&
-      int_lds_bytes<G, NT, FEW, 8, 16>(a) <= W4_LDS)
-    return go_int<G, NT, FEW, 8, 16>(a, st);
-  if (units >= 8 && int_lds_bytes<G, NT, FEW, 8, 8>(a) <= W4_LDS) return go_int<G, NT, FEW, 8, 8>(a, st);
+  int rc;
+  const bool done = in_panels(
+      a, (a.D + 127) / 128,
+      [&](int n) { return n < 8 ? int_lds_bytes<G, NT, FEW, 1, 4>(a, n) : int_lds_bytes<G, NT, FEW, 8, 8>(a, n); },
+      [&](const W4Args& p) {
+        if (p.units < 8) return go_int<G, NT, FEW, 1, 4>(p, st);
+        if (2 * int_lds_bytes<G, NT, FEW, 8, 8>(p, p.units) > W4_LDS && p.tiles >= 4 * device_cus() &&
+            int_lds_bytes<G, NT, FEW, 8, 16>(p, p.units) <= W4_LDS)
+          return go_int<G, NT, FEW, 8, 16>(p, st);
+        return go_int<G, NT, FEW, 8, 8>(p, st);
+      },
+      rc);
+  if (done) return rc;
   hipLaunchKernelGGL((k_w4_int_deep<G, NT, FEW, 8>), dim3((unsigned)a.tiles), dim3(512), 0, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }

@@ -200,3 +200,35 @@ def test_refusals(elmo):
         elmo.w4_matvec(W, X, wfmt=elmo.ELMO_W_E4M3)
     with pytest.raises(TypeError):
         elmo.w4_matvec(W, X, out_dtype=torch.float64)
+
+
+@pytest.mark.parametrize("fmt,N,L,D,G", [("mx", 29, 17000, 3840, 32), ("mx", 32, 16500, 4096, 32), ("mx", 16, 16401, 6144, 32),
+                                         ("mx", 18, 20000, 2560, 32), ("int4", 21, 16500, 7296, 128), ("int4", 24, 17003, 4832, 32),
+                                         ("int4", 9, 16400, 8192, 64), ("int4", 32, 20001, 2080, 32)])
+def test_feature_rows_beyond_lds(elmo, fmt, N, L, D, G):
+    """Many labels and more features than fit LDS at once (FP32 results summed over panels of D,
+    16-bit ones in one go), and just as many as fit; float64 products on the GPU in slices."""
+    print(f"  {fmt} N={N} L={L} D={D} G={G}", flush=True)
+    X = _x(N, D, N)
+    x = X.double()
+    if fmt == "mx":
+        W, kw, eps = _mx(L, D, L), {}, (D / 32 + 56) * U
+    else:
+        W, s, z = _int4(L, D, G, L, True)
+        kw, eps = dict(wfmt=elmo.ELMO_W_INT4, scales=s, zeros=z), (24 + D / 128) * U      # (panels: a few sums more)
+    y, h = elmo.w4_matvec(W, X, **kw), elmo.w4_matvec(W, X, out_dtype=torch.bfloat16, **kw)
+    table = E2M1.cuda()
+    for a in range(0, L, 4096):
+        r = W[a:a + 4096]
+        c = torch.stack([r[:, :D // 2] & 15, r[:, :D // 2] >> 4], 2).flatten(1).int()
+        if fmt == "mx":
+            w = table[c] * torch.exp2(r[:, D // 2:].double() - 127).repeat_interleave(32, 1)
+            size = w.abs()
+        else:
+            sc, zp = (t[a:a + 4096].double().repeat_interleave(G, 1) for t in (s, z))
+            w, size = (c.double() - zp) * sc, (c.double() + zp) * sc.abs()
+        ref, tol = x @ w.t().contiguous(), eps * (x.abs() @ size.t().contiguous())
+        off = (y[:, a:a + 4096].double() - ref).abs()
+        assert bool((off <= tol).all()), f"off by {off.max():.3e}, {(off / tol).max():.3g} of the tolerance"
+        off = (h[:, a:a + 4096].double() - ref).abs()
+        assert bool((off <= tol + 2.0**-8 * ref.abs()).all())
