@@ -31,8 +31,8 @@ VARIANTS = {
 
 
 def sources():
-    csrc = os.path.join(HERE, "csrc")
-    return sorted(glob.glob(os.path.join(csrc, "*.hip"))) + sorted(glob.glob(os.path.join(csrc, "*.cpp")))
+    dirs = [os.path.join(HERE, d) for d in ("csrc", "csrc_lm")]
+    return [f for ext in ("*.hip", "*.cpp") for d in dirs for f in sorted(glob.glob(os.path.join(d, ext)))]
 
 
 def units():

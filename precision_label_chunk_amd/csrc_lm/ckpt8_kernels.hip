@@ -10,7 +10,7 @@
 // elements of such a block one bit instead. Decoding is exact in BF16 (4 significant bits times a
 // power of two), so that the matrix products read exact operands.
 #include "elem_types.hpp"
-#include "step_kernels.hpp"
+#include "lm_kernels.hpp"
 
 namespace elmo {
 

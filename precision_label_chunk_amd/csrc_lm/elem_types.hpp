@@ -4,8 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "mfma.hpp"
-#include "numerics.hpp"
+#include "../csrc/mfma.hpp"
+#include "../csrc/numerics.hpp"
 
 namespace elmo {
 

@@ -18,7 +18,7 @@
 // in 112 us (6.1 TB/s). With alternatives the comparisons come close to the arithmetic that the read
 // hides: top 5 of the FP32 rows 117 us, top 20 of the BF16 rows 188 us, top 64 222 us.
 #include "elem_types.hpp"
-#include "step_kernels.hpp"
+#include "lm_kernels.hpp"
 #include "wave_top.hpp"
 
 namespace elmo {

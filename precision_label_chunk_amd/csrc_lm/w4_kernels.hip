@@ -27,7 +27,7 @@
 // A code byte c in 0..15 read as E4M3 is c 2^-9 (subnormals and the first binade have the same
 // spacing), so the FP8 -> BF16 conversion with scale 2^9 decodes it.
 #include "elem_types.hpp"
-#include "step_kernels.hpp"
+#include "lm_kernels.hpp"
 
 namespace elmo {
 

@@ -14,7 +14,7 @@
 // With it a 131072-value row has about one candidate for every three vectors of 512 values, and the
 // rest are passed over by one comparison each.
 #pragma once
-#include "numerics.hpp"
+#include "../csrc/numerics.hpp"
 
 namespace elmo {
 
