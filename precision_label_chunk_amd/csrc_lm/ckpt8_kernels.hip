@@ -147,8 +147,9 @@ __device__ __forceinline__ int64_t vec_at(int64_t i, int D, int64_t ld) {
   return row * ld + 8 * (i - row * (D / 8));
 }
 
-// Elementwise, bound by HBM: each thread takes 8 features, the four threads of a block of 32 share
-// their largest magnitude.
+// Elementwise, bound by HBM: each thread takes 8 features (one 16-byte load of a 16-bit type), the
+// four threads of a block of 32 share their largest magnitude. 16384 x 4096 BF16 with gelu in 53 us
+// (6.4 TB/s), relu 52, kept alone 36 (5.6 TB/s).
 template <typename E, int ACT, bool OUT>
 __global__ __launch_bounds__(256) void k_ckpt8_save(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
@@ -203,7 +204,8 @@ __global__ __launch_bounds__(256) void k_ckpt8_load(Ckpt8Args a) {
   }
 }
 
-// dx = dy act'(x) with x from its 8 bits; dx may be dy's own memory
+// dx = dy act'(x) with x from its 8 bits; dx may be dy's own memory. Bound by HBM: 16384 x 4096 BF16 in
+// 53 us with relu (6.3 TB/s), 57 with silu and 59 with gelu (5.7), whose arithmetic is not all hidden.
 template <typename E, int ACT>
 __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
@@ -225,9 +227,11 @@ __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
 // the codes decoded on their way into LDS (half an operation per code, shared by the whole tile).
 // Two LDS buffers and the next one or two stages' loads in registers: one barrier per stage. Rows are
 // padded by 64 bytes, so that the four token rows of a transposing read cover all 64 banks (no
-// conflicts counted). Bound by the matrix cores at the clock they hold: 16384 tokens, 2048 x 4096 in
-// 265 us, 1040 TFLOP/s, where the library's BF16 product of the decoded operands takes 265; the
-// products keep the cores busy 46% of the cycles, the rest is the LDS reads that feed them.
+// conflicts counted). Bound by latency: one wave per SIMD has nothing to run while it waits. 16384
+// tokens, 2048 x 4096, the join included: 269 us on inputs used again and 294 (936 TFLOP/s) on inputs
+// that change from call to call, where the library's BF16 product of the decoded operands, timed in
+// turn with it, takes 245 and 255. On changing inputs the matrix cores are busy 41% of the cycles, LDS
+// 21%, and the waves spend 39% of theirs waiting for data or at the barrier.
 // Few tiles split the tokens over `segs` blocks, whose partial tiles k_wgrad_join adds in order.
 constexpr int WG_BK = 32;
 struct WgradArgs {
@@ -478,8 +482,8 @@ int run_ckpt8_act_grad(const void* dy, int type, int64_t T, int D, int64_t lddy,
 // nanoseconds: a block's fixed part, its stages at the rate that one or several blocks per CU reach,
 // and the join's launch and traffic (coefficients fitted to timings between 64 x 64 and 4096 x 4096).
 // The large tile reads LDS half as often per product, the small one fills the device with less
-// splitting: 16384 tokens take 265 us with 256 x 256 and 324 with 128 x 128 at 2048 x 4096, and 44
-// against 37 at 768 x 768.
+// splitting: 16384 tokens (the same for every call) take 265 us with 256 x 256 and 324 with 128 x 128
+// at 2048 x 4096, and 44 against 37 at 768 x 768.
 WgradLayout wgrad_layout(int64_t T, int O, int D) {
   const int cus = device_cus();
   WgradLayout best{};
