@@ -326,6 +326,16 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _scratch(workspace, need, like):
+    """The caller's workspace (bytes on the operands' device), or a new one if it is missing or too small."""
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != like.device
+                                  or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {like.device}")
+    if workspace is None or workspace.numel() < need:
+        return like.new_empty((need,), dtype=torch.uint8)
+    return workspace
+
+
 class LogProbs(NamedTuple):
     """What logprobs() returns; row_max + log_sum is each row's log partition."""
     logp: torch.Tensor                   # [N, M]
@@ -353,9 +363,7 @@ def logprobs(Z, ids=None, k=0, workspace=None) -> LogProbs:
     idx = Z.new_empty((N, k), dtype=torch.int32) if k else None
     top = Z.new_empty((N, k), dtype=torch.float32) if k else None
     if N:
-        need = lib().elmo_logprobs_workspace_bytes(N, V, k)
-        if workspace is None or workspace.numel() < need:
-            workspace = Z.new_empty((need,), dtype=torch.uint8)
+        workspace = _scratch(workspace, lib().elmo_logprobs_workspace_bytes(N, V, k), Z)
         _chk("elmo_logprobs", lib().elmo_logprobs(
             Z.data_ptr(), e, N, V, ld, _at(ids) if M else None, M, k, _at(logp) if M else None, entropy.data_ptr(),
             row_max.data_ptr(), log_sum.data_ptr(), _at(idx), _at(top), workspace.data_ptr(), workspace.numel(),
@@ -510,8 +518,7 @@ def ckpt8_weight_grad(dy, codes, scales, out=None, accumulate=False, workspace=N
     need = int(lib().elmo_ckpt8_weight_grad_workspace_bytes(T, O, D))
     if need == 0:
         raise ElmoError("elmo_ckpt8_weight_grad_workspace_bytes", -2)
-    if workspace is None or workspace.numel() < need:
-        workspace = dy.new_empty((need,), dtype=torch.uint8)
+    workspace = _scratch(workspace, need, dy)
     _chk("elmo_ckpt8_weight_grad", lib().elmo_ckpt8_weight_grad(
         dy.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), T, O, D, out.data_ptr(), int(accumulate),
         workspace.data_ptr(), workspace.numel(), _stream_of(codes.device)))

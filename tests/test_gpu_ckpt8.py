@@ -296,3 +296,17 @@ def test_refusals(elmo):
         elmo.ckpt8_weight_grad(_x(4, 12, torch.bfloat16, 1), codes, scales)
     with pytest.raises(ValueError):
         elmo.ckpt8_weight_grad(x, codes, scales, accumulate=True)
+
+
+def test_weight_grad_workspace_is_device_bytes(elmo):
+    """A workspace on the host, of another type or strided is refused before its address is used."""
+    codes, scales, _ = elmo.ckpt8_save(_x(600, 64, torch.bfloat16, 1))
+    dy = _x(600, 64, torch.bfloat16, 2)
+    want = elmo.ckpt8_weight_grad(dy, codes, scales)
+    need = 1 << 21
+    for bad in (torch.zeros(need, dtype=torch.uint8), torch.zeros(need, dtype=torch.float32, device="cuda"),
+                torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            elmo.ckpt8_weight_grad(dy, codes, scales, workspace=bad)
+    fine = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    assert torch.equal(elmo.ckpt8_weight_grad(dy, codes, scales, workspace=fine), want)

@@ -361,3 +361,17 @@ def test_signalling_nan_logits_hide_no_alternative(elmo, dtype, bits, view, k):
         r = elmo.logprobs(raw.view(dtype).cuda(), k=k)
         assert torch.equal(r.top_idx.cpu().long(), want)
         assert bool(r.entropy.isnan().all())
+
+
+def test_workspace_is_device_bytes(elmo):
+    """A workspace on the host, of another type or strided is refused before its address is used."""
+    Z = torch.randn(2, 70000, device="cuda")
+    want = elmo.logprobs(Z, k=3)
+    need = 1 << 20
+    for bad in (torch.zeros(need, dtype=torch.uint8), torch.zeros(need, dtype=torch.float32, device="cuda"),
+                torch.zeros(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError):
+            elmo.logprobs(Z, k=3, workspace=bad)
+    for fine in (torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.zeros(8, dtype=torch.uint8, device="cuda")):
+        r = elmo.logprobs(Z, k=3, workspace=fine)
+        assert torch.equal(r.entropy, want.entropy) and torch.equal(r.top_idx, want.top_idx)
