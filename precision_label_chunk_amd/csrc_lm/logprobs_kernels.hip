@@ -34,8 +34,9 @@ __device__ __forceinline__ float soft_ref(float m) { return m == -__builtin_inff
 
 // moves a partial sum to the reference of the larger maximum mn
 __device__ __forceinline__ void soft_move(SoftPart& a, float mn) {
-  // d is -inf for an empty part; kept finite, 2^d is 0 and d s is 0
-  const float d = __builtin_fmaxf((a.m - soft_ref(mn)) * LOG2E, -1e30f);
+  // d is -inf for an empty part or one that lies far below; 2^-1e4 is 0 as well, and d s stays finite
+  // for every sum s of up to 2^31 elements, so that 0 times it is 0
+  const float d = __builtin_fmaxf((a.m - soft_ref(mn)) * LOG2E, -1e4f);
   const float r = __builtin_amdgcn_exp2f(d);
   a.t = r * __builtin_fmaf(d, a.s, a.t);
   a.s *= r;

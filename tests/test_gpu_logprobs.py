@@ -375,3 +375,18 @@ def test_workspace_is_device_bytes(elmo):
     for fine in (torch.zeros(need, dtype=torch.uint8, device="cuda"), torch.zeros(8, dtype=torch.uint8, device="cuda")):
         r = elmo.logprobs(Z, k=3, workspace=fine)
         assert torch.equal(r.entropy, want.entropy) and torch.equal(r.top_idx, want.top_idx)
+
+
+@pytest.mark.parametrize("k", [0, 2])
+def test_one_token_over_many_at_the_lowest_value(elmo, k):
+    """1.5e9 tokens masked with the type's lowest value and one that is not: sums of more than 3.4e8
+    equal terms meet a distance that binary32 does not hold. The token has all the probability."""
+    V = 1_500_000_001
+    Z = torch.full((1, V), torch.finfo(torch.bfloat16).min, dtype=torch.bfloat16, device="cuda")
+    Z[0, V - 2] = 1.0
+    ids = torch.tensor([[V - 2]], dtype=torch.int32, device="cuda")
+    r = elmo.logprobs(Z, ids, k=k)
+    assert r.row_max.item() == 1.0 and r.log_sum.item() == 0.0
+    assert r.logp.item() == 0.0 and r.entropy.item() == 0.0
+    if k:
+        assert r.top_idx.cpu().tolist() == [[V - 2, 0]] and r.top_logp[0, 0].item() == 0.0
