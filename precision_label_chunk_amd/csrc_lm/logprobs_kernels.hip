@@ -69,6 +69,7 @@ __device__ __forceinline__ void wave_join(SoftPart& a) {
 
 struct LogprobArgs {
   const void* Z; int64_t N, V, ldz;
+  int64_t row0;                                 // the launch's first row
   const int32_t* ids; int M, k;
   float *logp, *entropy, *row_max, *log_sum;
   int32_t* top_idx; float* top_logp;
@@ -182,7 +183,7 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs(LogprobArgs a) {
   constexpr int VEC = E::VEC, U = 4;                        // U vectors of 16 bytes per lane in flight
   __shared__ LogprobShared<TOP> s;
   const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
-  const int64_t n = blockIdx.x / a.segs;
+  const int64_t n = a.row0 + blockIdx.x / a.segs;
   const int seg = (int)(blockIdx.x % a.segs);
   const typename E::raw* z = (const typename E::raw*)a.Z + n * a.ldz;
   // the row as up to VEC - 1 single elements, nv aligned vectors, up to VEC - 1 single elements
@@ -350,6 +351,7 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
 // once is summed in the order of its places, by the thread of its first.
 struct LogprobGradArgs {
   const void* Z; int64_t N, V, ldz;
+  int64_t row0;                                 // the launch's first row
   const int32_t* ids; int M;
   const float *row_max, *log_sum, *entropy, *dlogp, *dentropy, *dlse;
   void* dZ; int64_t ldd;
@@ -361,7 +363,7 @@ __global__ __launch_bounds__(256) void k_logprobs_grad(LogprobGradArgs a) {
   constexpr int VEC = E::VEC, U = 4;
   typedef typename E::raw raw;
   const int tid = (int)threadIdx.x;
-  const int64_t n = blockIdx.x / a.segs;
+  const int64_t n = a.row0 + blockIdx.x / a.segs;
   const int seg = (int)(blockIdx.x % a.segs);
   const raw* z = (const raw*)a.Z + n * a.ldz;
   raw* d = (raw*)a.dZ + n * a.ldd;
@@ -468,14 +470,29 @@ LogprobLayout logprobs_layout(int64_t N, int64_t V, int k) {
   return s;
 }
 
+// A launch holds fewer than 2^32 threads: rows go in runs of at most 2^23 (several runs only where a row
+// is one block, as split rows are few).
+template <typename F>
+static int row_runs(int64_t N, int segs, F&& launch) {
+  constexpr int64_t MOST = int64_t(1) << 23;
+  for (int64_t row0 = 0; row0 < N; row0 += MOST) {
+    launch(row0, dim3((unsigned)((N - row0 < MOST ? N - row0 : MOST) * segs)));
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  }
+  return ELMO_OK_;
+}
+
 template <typename E>
-static int launch_logprobs(const LogprobArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.N * a.segs)), block(LP_THREADS);
-  if (a.k)
-    hipLaunchKernelGGL((k_logprobs<E, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_logprobs<E, false>), grid, block, 0, st, a);
-  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+static int launch_logprobs(LogprobArgs a, hipStream_t st) {
+  const dim3 block(LP_THREADS);
+  const int rc = row_runs(a.N, a.segs, [&](int64_t row0, dim3 grid) {
+    a.row0 = row0;
+    if (a.k)
+      hipLaunchKernelGGL((k_logprobs<E, true>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_logprobs<E, false>), grid, block, 0, st, a);
+  });
+  if (rc != ELMO_OK_) return rc;
   if (a.segs > 1) {
     if (a.k)
       hipLaunchKernelGGL((k_logprobs_join<E, true>), dim3((unsigned)a.N), block, 0, st, a);
@@ -504,13 +521,15 @@ int run_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, co
 }
 
 template <typename E>
-static int launch_grad(const LogprobGradArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.N * a.segs)), block(256);
-  if (a.dentropy)
-    hipLaunchKernelGGL((k_logprobs_grad<E, true>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((k_logprobs_grad<E, false>), grid, block, 0, st, a);
-  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+static int launch_grad(LogprobGradArgs a, hipStream_t st) {
+  const dim3 block(256);
+  return row_runs(a.N, a.segs, [&](int64_t row0, dim3 grid) {
+    a.row0 = row0;
+    if (a.dentropy)
+      hipLaunchKernelGGL((k_logprobs_grad<E, true>), grid, block, 0, st, a);
+    else
+      hipLaunchKernelGGL((k_logprobs_grad<E, false>), grid, block, 0, st, a);
+  });
 }
 
 int run_logprobs_grad(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, const int32_t* ids, int M,

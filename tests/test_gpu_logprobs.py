@@ -390,3 +390,23 @@ def test_one_token_over_many_at_the_lowest_value(elmo, k):
     assert r.logp.item() == 0.0 and r.entropy.item() == 0.0
     if k:
         assert r.top_idx.cpu().tolist() == [[V - 2, 0]] and r.top_logp[0, 0].item() == 0.0
+
+
+def test_more_rows_than_one_launch_holds(elmo):
+    """2^24 + 5 rows: 256 threads each would be more than 2^32. Rows do not depend on each other, so
+    every stretch of them equals its own call bit for bit, and the last ones the plain form."""
+    N, V = (1 << 24) + 5, 4
+    g = torch.Generator(device="cuda").manual_seed(3)
+    Z = torch.randn((N, V), device="cuda", generator=g).half()
+    ids = torch.randint(0, V, (N, 1), device="cuda", generator=g, dtype=torch.int32)
+    r = elmo.logprobs(Z, ids, k=2)
+    d = torch.randn((N, 1), device="cuda", generator=g)
+    dZ = elmo.logprobs_backward(Z, ids, r, d)
+    for a, b in ((0, 1000), ((1 << 23) - 3, (1 << 23) + 3), ((1 << 24) - 2, N)):
+        part = elmo.logprobs(Z[a:b], ids[a:b], k=2)
+        for x, y in zip(r, part):
+            assert torch.equal(x[a:b], y)
+        assert torch.equal(dZ[a:b], elmo.logprobs_backward(Z[a:b], ids[a:b], part, d[a:b]))
+    lp = Z[-7:].cpu().double().log_softmax(1)
+    err = (r.logp[-7:].cpu().double() - lp.gather(1, ids[-7:].cpu().long())).abs().max()
+    assert err <= _R(V) + 4 * U * lp.abs().max()
