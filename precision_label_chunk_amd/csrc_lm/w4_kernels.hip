@@ -45,6 +45,7 @@ struct W4Args {
   const uint16_t* X; int N; int64_t ldx;
   void* Y; int ytype; int64_t ldy;
   int64_t tiles;                      // ceil(L / 16)
+  int64_t tile0;                      // the launch's first tile (k_w4_int_deep)
   // the panel of D that a launch takes, in the kernel's units of features: rows of larger products do
   // not fit LDS at once, and their FP32 results are summed panel by panel
   int unit0, units, add;
@@ -502,7 +503,7 @@ __global__ __launch_bounds__(64 * KS) void k_w4_int_deep(W4Args a) {
   __shared__ float part[KS * V * 64];
   const int ks = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
   const int col = lane & 15, q = lane >> 4;
-  const int64_t tile = blockIdx.x;
+  const int64_t tile = a.tile0 + blockIdx.x;
   int64_t label = tile * 16 + col;
   if (label >= a.L) label = a.L - 1;
   float acc[V];
@@ -565,7 +566,7 @@ static int go_lds(const W4Args& a, hipStream_t st) {
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
 template <int NT, int LT, int KS>
-static int go_deep(const W4Args& a, hipStream_t st) {
+static int go_deep(const W4Args& a, hipStream_t st) {      // (2^32 threads are 2^28 labels here, over 300 GB of weights)
   hipLaunchKernelGGL((k_w4_mx_deep<NT, LT, KS>), dim3((unsigned)((a.tiles + LT - 1) / LT)), dim3(64 * KS), 0, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
@@ -644,8 +645,15 @@ static int pick_int(const W4Args& a, hipStream_t st) {
       },
       rc);
   if (done) return rc;
-  hipLaunchKernelGGL((k_w4_int_deep<G, NT, FEW, 8>), dim3((unsigned)a.tiles), dim3(512), 0, st, a);
-  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+  // a launch holds fewer than 2^32 threads: runs of at most 2^22 tiles (2^26 labels)
+  constexpr int64_t MOST = int64_t(1) << 22;
+  W4Args p = a;
+  for (; p.tile0 < a.tiles; p.tile0 += MOST) {
+    const int64_t left = a.tiles - p.tile0;
+    hipLaunchKernelGGL((k_w4_int_deep<G, NT, FEW, 8>), dim3((unsigned)(left < MOST ? left : MOST)), dim3(512), 0, st, p);
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  }
+  return ELMO_OK_;
 }
 template <int G>
 static int pick_rows(const W4Args& a, hipStream_t st) {

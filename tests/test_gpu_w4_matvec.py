@@ -232,3 +232,28 @@ def test_feature_rows_beyond_lds(elmo, fmt, N, L, D, G):
         assert bool((off <= tol).all()), f"off by {off.max():.3e}, {(off / tol).max():.3g} of the tolerance"
         off = (h[:, a:a + 4096].double() - ref).abs()
         assert bool((off <= tol + 2.0**-8 * ref.abs()).all())
+
+
+def test_integer_codes_of_more_labels_than_one_launch_holds(elmo):
+    """2^27 + 21 labels of 1920 features with 32 rows and 16-bit results: a block per 16 labels would be
+    more than 2^32 threads, and offsets pass 2^36 bytes. Stretches equal their own calls bit for bit."""
+    L, N, D, G = (1 << 27) + 21, 32, 1920, 128
+    need = L * (D // 2 + 2 * (D // G) + 2 * N) + (4 << 30)
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GiB of free device memory")
+    X = _x(N, D, 5)
+    W = torch.empty((L, D // 2), dtype=torch.uint8, device="cuda")
+    s = torch.empty((L, D // G), dtype=torch.bfloat16, device="cuda")
+    stretches = [(0, 37), ((1 << 26) - 16, (1 << 26) + 16), ((1 << 27) - 16, L)]
+    for a, b in stretches:
+        W[a:b], s[a:b], _ = _int4(b - a, D, G, a % 1000, False)
+    y = elmo.w4_matvec(W, X, wfmt=elmo.ELMO_W_INT4, scales=s, out_dtype=torch.bfloat16)
+    for a, b in stretches:
+        assert torch.equal(y[:, a:b], elmo.w4_matvec(W[a:b], X, wfmt=elmo.ELMO_W_INT4, scales=s[a:b], out_dtype=torch.bfloat16))
+    a, b = stretches[-1]
+    c, x, sc = _codes(W[a:b]).double(), X.cpu().double(), s[a:b].cpu().double().repeat_interleave(G, 1)
+    ref = x @ ((c - 8) * sc).t()
+    _check(y[:, a:b], ref, (12 + D / 128) * U * (x.abs() @ ((c + 8) * sc.abs()).t()), 2.0**-8)
+    del W, s, y
+    torch.cuda.empty_cache()
