@@ -542,6 +542,12 @@ __global__ __launch_bounds__(64 * KS) void k_w4_int_deep(W4Args a) {
 // ---- launchers -------------------------------------------------------------------------------------
 constexpr size_t W4_LDS = 160 << 10;                       // per CU and per block
 
+// Lets a kernel take all of it. The limit belongs to the process, so it is the same for every call: one
+// set to a call's own size could be lowered by another host thread between this and the launch.
+static bool raise_lds_limit(const void* kernel, size_t lds) {
+  return lds <= (64 << 10) || hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)W4_LDS) == hipSuccess;
+}
+
 template <int UNITS>
 static int go_regs(const W4Args& a, hipStream_t st) {
   const int64_t want = (a.tiles + 3) / 4, cap = 2 * (int64_t)device_cus();   // 2 waves per SIMD at 200-240 registers
@@ -559,9 +565,7 @@ static int go_lds(const W4Args& a, hipStream_t st) {
   if (per_cu > 16 / WAVES) per_cu = 16 / WAVES;            // 4 waves per SIMD
   if (per_cu < 1) per_cu = 1;
   const int64_t want = (a.tiles + GR - 1) / GR, cap = (int64_t)device_cus() * per_cu;
-  if (lds > (64 << 10) && hipFuncSetAttribute((const void*)k_w4_mx_lds<NT, KS, WAVES>, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                              (int)lds) != hipSuccess)
-    return ELMO_EHIP_;
+  if (!raise_lds_limit((const void*)k_w4_mx_lds<NT, KS, WAVES>, lds)) return ELMO_EHIP_;
   hipLaunchKernelGGL((k_w4_mx_lds<NT, KS, WAVES>), dim3((unsigned)(want < cap ? want : cap)), dim3(64 * WAVES), lds, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
@@ -624,9 +628,7 @@ static int go_int(const W4Args& a, hipStream_t st) {
   if (per_cu > 24 / WAVES) per_cu = 24 / WAVES;            // 6 waves per SIMD (65536 x 4096, one row: 36.5 us; at 4: 41.7)
   if (per_cu < 1) per_cu = 1;
   const int64_t want = (a.tiles + GR - 1) / GR, cap = (int64_t)device_cus() * per_cu;
-  if (lds > (64 << 10) && hipFuncSetAttribute((const void*)k_w4_int_lds<G, NT, FEW, KS, WAVES>,
-                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds) != hipSuccess)
-    return ELMO_EHIP_;
+  if (!raise_lds_limit((const void*)k_w4_int_lds<G, NT, FEW, KS, WAVES>, lds)) return ELMO_EHIP_;
   hipLaunchKernelGGL((k_w4_int_lds<G, NT, FEW, KS, WAVES>), dim3((unsigned)(want < cap ? want : cap)), dim3(64 * WAVES), lds, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
