@@ -602,8 +602,13 @@ static int pick_mx(const W4Args& a, hipStream_t st) {
   const bool done = in_panels(
       a, a.D / 256, [&](int n) { return mx_lds_bytes(a, n, NT, n < 8 ? 1 : 8, 8); },
       [&](const W4Args& p) {
-        if (p.units < 8)
-          return 2 * mx_lds_bytes(p, p.units, NT, 1, 4) > W4_LDS ? go_lds<NT, 1, 16>(p, st) : go_lds<NT, 1, 4>(p, st);
+        if (p.units < 8) {
+          // (16 rows of up to 7 units always leave room for two blocks)
+          if constexpr (NT > 1) {
+            if (2 * mx_lds_bytes(p, p.units, NT, 1, 4) > W4_LDS) return go_lds<NT, 1, 16>(p, st);
+          }
+          return go_lds<NT, 1, 4>(p, st);
+        }
         // where only one block fits a CU, 16 waves of it hide more latency than 8, unless there are too
         // few tiles to give both groups a share
         if (2 * mx_lds_bytes(p, p.units, NT, 8, 8) > W4_LDS && p.tiles >= 4 * device_cus() &&

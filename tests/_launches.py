@@ -60,3 +60,22 @@ def w4_matvec(fmt, N, L, D, group=32, ytype=0):
 
 def ckpt8_weight_grad(T, O, D, accumulate=0):
     return ("elmo_ckpt8_weight_grad", "plppliipipzp", [P, O, P, P, T, O, D, P, accumulate, P, 1 << 60, None])
+
+
+def logprobs(ztype, N, V, k):
+    return ("elmo_logprobs", "pilllpiipppppppzp",
+            [P, ztype, N, V, V, P, 1, k, P, P, P, P, P, P, P, 1 << 60, None])
+
+
+def logprobs_backward(ztype, N, V, entropy):
+    return ("elmo_logprobs_backward", "pilllpippppppplp",
+            [P, ztype, N, V, V, P, 1, P, P, P, P, P if entropy else None, None, 2 * P, V, None])
+
+
+def ckpt8(T, D, type, act):
+    """The calls of one activation: saved, restored, its gradient."""
+    y = 2 * P if act else None
+    save = ("elmo_ckpt8_save", "pililippplp", [P, type, T, D, D, act, P, P, y, D, None])
+    load = ("elmo_ckpt8_load", "pplipilp", [P, P, T, D, P, type, D, None])
+    grad = ("elmo_ckpt8_act_grad", "pililippplp", [P, type, T, D, D, act, P, P, 2 * P, D, None])
+    return [save, load, grad] if act else [save, load]

@@ -1,11 +1,13 @@
 """The launches of the language-model operators, from their host code alone (no GPU)."""
+import subprocess
+
 import pytest
 
 import _launches as R
 
 # (format, rows, labels, features, group): rows of features in LDS, many sizes per kernel
 SWEEP = [(fmt, N, L, D, g) for fmt, g in ((2, 32), (3, 32), (3, 64), (3, 128)) for N in (1, 3, 7, 16, 19, 32)
-         for L in (100, 5000, 70001) for D in range(256, 16385, 256)]
+         for L in (100, 5000, 70001) for D in [*range(256, 16385, 256), 32768, 65536]]
 
 
 @pytest.fixture(scope="module")
@@ -27,3 +29,19 @@ def test_lds_limit_does_not_depend_on_the_call(sweep):
             over += lds > 64 << 10
     assert over > 100                        # (the sweep does reach launches that need the raised limit)
     assert changes == 1, f"the limit of {kernel} was changed {changes} times"
+
+
+def test_every_kernel_is_reached(sweep, tmp_path):
+    """The library holds no kernel of these operators that no call launches."""
+    calls = [R.logprobs(t, N, V, k) for t in (0, 1, 2) for N in (1, 5000) for V in (100, 100000) for k in (0, 5)]
+    calls += [R.logprobs_backward(t, 3, 1000, h) for t in (0, 1, 2) for h in (False, True)]
+    calls += [c for t in (0, 1, 2) for act in range(4) for c in R.ckpt8(10, 64, t, act)]
+    calls += [R.ckpt8_weight_grad(T, O, D) for T in (100, 16384) for O, D in ((64, 64), (2048, 4096))]
+    rest, _ = R.record(tmp_path, calls)
+    assert all(rc == 0 for rc, _ in rest)
+    launched = {x[0] for _, one in sweep[0] + rest for x in one}
+    nm = subprocess.run(["nm", "-D", "--defined-only", R.LIB], capture_output=True, text=True, check=True).stdout
+    kernels = {ln.split()[-1] for ln in nm.splitlines()}
+    kernels = {k for k in kernels if any(n in k for n in ("k_w4_", "k_logprobs", "k_ckpt8_", "k_wgrad_")) and "__device_stub__" not in k}
+    assert len(kernels) > 60 and kernels >= launched
+    assert kernels == launched, f"no call launches {sorted(kernels - launched)}"
