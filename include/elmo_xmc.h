@@ -263,7 +263,9 @@ int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64
  * Products of a few feature rows with 4-bit weights with group scales, Y[n, j] = sum_k X[n, k] w[j, k]:
  * the logits of a 4-bit head, or any layer, for the rows of a decode step. The weights are read once;
  * features stay BF16 (elmo_xmc_logits casts them to E4M3 and reads D <= 1024), every product is exact
- * and sums are binary32.
+ * and sums are binary32. With integer codes the products are c x, summed over a group and joined with
+ * its zero point and scale as s (sum c x - z sum x): the rounding is that of sums of c |x| and z |x|, and
+ * these have to stay below 2^128 themselves.
  *   wdtype   ELMO_W_MXFP4: W holds L rows of 17 D / 32 bytes as described with the formats, D % 256 == 0,
  *            8-byte aligned; group = 32, scales = zeros = NULL.
  *            ELMO_W_INT4: W holds L rows of D/2 bytes, code c[2i] in the low nibble of byte i and
@@ -273,9 +275,11 @@ int elmo_logprobs_backward(const void* Z, int ztype, int64_t N, int64_t V, int64
  *   X        [N, D] BF16, 1 <= N <= ELMO_MAX_MATVEC_ROWS (N = 0: nothing is done), row n at X + n ldx;
  *            16-byte aligned rows (ldx % 8 == 0).
  *   Y        [N, L] of element type `ytype` (rounded once from binary32), row n at Y + n ldy.
- * 1 <= L < 2^31; D <= ELMO_MAX_MATVEC_D. An MXFP4 scale of 255 (NaN), a NaN weight scale or a NaN
- * feature makes the results it enters NaN; so does an infinite feature (with integer codes even
- * where the sum would be infinite). No workspace.
+ * 1 <= L < 2^31; D <= ELMO_MAX_MATVEC_D. No workspace. Values out of range stay in the row and label they enter:
+ * an MXFP4 scale of 255 (NaN), a NaN weight scale and a NaN feature make its results NaN. An MXFP4 weight of
+ * 2^128 or more (scale codes 253 and 254 with the largest elements) is infinite. An infinite feature or
+ * weight makes an MXFP4 result infinite (NaN against a zero, or against infinity of the other sign); an infinite
+ * feature makes a result of integer codes NaN.
  */
 enum { ELMO_W_INT4 = 3 };                 /* elmo_w4_matvec only */
 #define ELMO_MAX_MATVEC_ROWS 32

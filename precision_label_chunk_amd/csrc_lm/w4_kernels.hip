@@ -10,8 +10,8 @@
 //   A: lane l holds row m = l % 16, k = 8 (l / 16) + e;  B: column l % 16, the same k;
 //   C: lane l, register i holds column l % 16, row 4 (l / 16) + i.
 //
-// MXFP4 rows: the block's power-of-two scale is applied by the decode (exact in BF16), so row m of
-// A is feature row m and the sums run over all of D.
+// MXFP4 rows: the block's power-of-two scale is applied by the decode (exact in BF16 below 2^128, infinite
+// from there), so row m of A is feature row m and the sums run over all of D.
 //
 // Integer codes with a scale (and zero point) per group: w = (c - z) s, s any BF16 number, which no
 // exact BF16 weight holds. The codes 0..15 themselves are exact; the scale is applied to the
