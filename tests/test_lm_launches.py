@@ -45,3 +45,17 @@ def test_every_kernel_is_reached(sweep, tmp_path):
     kernels = {k for k in kernels if any(n in k for n in ("k_w4_", "k_logprobs", "k_ckpt8_", "k_wgrad_")) and "__device_stub__" not in k}
     assert len(kernels) > 60 and kernels >= launched
     assert kernels == launched, f"no call launches {sorted(kernels - launched)}"
+
+
+def test_large_tile_shapes_take_the_large_tile(tmp_path):
+    """The shapes of test_gpu_ckpt8_large_tile.py run the 256 x 256 weight-gradient tile, in one segment of
+    tokens and in several."""
+    from test_gpu_ckpt8_large_tile import SHAPES
+    calls, _ = R.record(tmp_path, [R.ckpt8_weight_grad(*s) for s in [*SHAPES, (8005, 1800, 1824)]])
+    segments = set()
+    for (T, O, D), (rc, launches) in zip(SHAPES, calls):
+        assert rc == 0 and "k_ckpt8_wgradILi4ELi4E" in launches[0][0], (T, O, D)
+        segs = launches[0][1] / (-(-O // 256) * -(-D // 256))
+        assert len(launches) == (1 if segs == 1 else 2)
+        segments.add(segs)
+    assert 1 in segments and len(segments) >= 3
