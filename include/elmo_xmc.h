@@ -227,7 +227,7 @@ enum { ELMO_T_F32 = 0, ELMO_T_BF16 = 1, ELMO_T_F16 = 2 };
  *   Z        [N, V] logits of element type `ztype`, row n at Z + n ldz elements (ldz >= V), elements
  *            of a row adjacent; any row alignment. -inf is a masked token.
  *   ids      [N, M] int32, 0 <= M <= ELMO_MAX_GIVEN (NULL if M = 0). A negative id stands for no
- *            token: its log probability is 0. An id >= V gives NaN.
+ *            token: its log probability is 0 in any row. An id >= V gives NaN in any row.
  *   k        alternatives per row, 0 <= k <= min(ELMO_MAX_TOPK, V).
  *   logp     [N, M] FP32: (z[id] - row_max) - log_sum.
  *   entropy  [N] FP32: -sum_v p_v log p_v.
@@ -235,9 +235,10 @@ enum { ELMO_T_F32 = 0, ELMO_T_BF16 = 1, ELMO_T_F16 = 2 };
  *            partition; apart they keep log_sum's digits at logits of any magnitude.
  *   top_idx, top_logp [N, k] int32 and FP32: tokens by (logit desc, token asc), NaN logits last, and
  *            their log probabilities (both NULL if k = 0).
- * A row of nothing but -inf has row_max -inf, log_sum 0, entropy 0 and every log probability -inf. A
- * NaN or +inf logit makes log_sum, entropy and every log probability of its row NaN (row_max skips
- * NaN). Results do not depend on the launch and repeat bit for bit on one device.
+ * A row of nothing but -inf has row_max -inf, log_sum 0, entropy 0 and every token's log probability -inf. A
+ * NaN or +inf logit makes log_sum, entropy and every token's log probability of its row NaN (row_max skips
+ * NaN: -inf if there is nothing else). Results repeat bit for bit on one device; the order of a row's sums,
+ * and with it their last bits, follows from N, V, ztype and the row's alignment to 16 bytes.
  * 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done).
  */
 #define ELMO_MAX_GIVEN 64
@@ -250,8 +251,8 @@ int elmo_logprobs(const void* Z, int ztype, int64_t N, int64_t V, int64_t ldz, c
  * (NULL if M = 0), dentropy [N] (nullable) and dlse [N] (nullable: of row_max + log_sum):
  *   dZ[n, v] = p_v (dlse - sum_j dlogp_j - dentropy (log p_v + H)) + sum_{j : ids_j = v} dlogp_j.
  * row_max, log_sum and entropy are elmo_logprobs' outputs for the same Z. A token given more than
- * once receives the sum of its gradients, a negative id none; an id >= V makes its row NaN, a row
- * of nothing but -inf has gradient 0.
+ * once receives the sum of its gradients, a negative id none. A row of nothing but -inf has gradient 0,
+ * whatever its ids; in any other row an id >= V makes the whole row NaN.
  *   dZ       [N, V] of type `ztype`, row n at dZ + n ldd. dZ = Z with ldd = ldz is allowed (in
  *            place); no other overlap is. No workspace.
  */
@@ -304,7 +305,8 @@ int elmo_w4_matvec(const void* W, int wdtype, int64_t L, int D, int group, const
 enum { ELMO_ACT_NONE = 0, ELMO_ACT_RELU = 1, ELMO_ACT_SILU = 2, ELMO_ACT_GELU = 3 };
 /* Saves x [T, D]; with act != NONE also y = act(x) of the unrounded x, in the same pass (y nullable
  * only with NONE, where it must be NULL). relu(x) = max(x, 0); silu(x) = x / (1 + e^-x); gelu(x) =
- * x Phi(x), Phi the normal distribution function (no tanh approximation). y must not overlap x. */
+ * x Phi(x), Phi the normal distribution function (no tanh approximation; results under 1e-37 may be 0, and so
+ * may slopes below). y must not overlap x. */
 int elmo_ckpt8_save(const void* x, int type, int64_t T, int D, int64_t ldx, int act, uint8_t* codes,
                     uint8_t* scales, void* y, int64_t ldy, void* stream);
 /* The saved activations, x' [T, D]: exact in FP32 and BF16 (as far as the type's range goes), rounded in FP16. */

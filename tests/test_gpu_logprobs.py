@@ -410,3 +410,29 @@ def test_more_rows_than_one_launch_holds(elmo):
     lp = Z[-7:].cpu().double().log_softmax(1)
     err = (r.logp[-7:].cpu().double() - lp.gather(1, ids[-7:].cpu().long())).abs().max()
     assert err <= _R(V) + 4 * U * lp.abs().max()
+
+
+def test_ids_that_name_no_token_in_empty_and_nan_rows(elmo):
+    """An id past the vocabulary gives NaN and a negative one 0 in any row; the gradient of a row without
+    tokens is 0 whatever its ids, that of any other row with an id past the vocabulary NaN."""
+    V = 1001
+    Z = _rows(4, V, torch.float32, 6)
+    Z[0], Z[1], Z[2, 5] = -math.inf, math.nan, math.inf
+    ids = torch.tensor([[V, -1, 3]] * 4, dtype=torch.int32, device="cuda")
+    r = elmo.logprobs(Z, ids, k=2)
+    assert bool(r.logp[:, 0].isnan().all()) and bool((r.logp[:, 1] == 0).all())
+    assert r.logp[0, 2] == -math.inf and bool(r.logp[1:3, 2].isnan().all()) and bool(torch.isfinite(r.logp[3, 2]))
+    assert r.row_max[:3].tolist() == [-math.inf, -math.inf, math.inf]
+    for dh in (None, torch.ones(4, device="cuda")):
+        dz = elmo.logprobs_backward(Z, ids, r, torch.ones((4, 3), device="cuda"), dentropy=dh)
+        assert bool((dz[0] == 0).all()) and bool(dz[1:].isnan().all())
+
+
+def test_a_row_gives_the_same_alternatives_in_any_batch(elmo):
+    """Rows are split differently in batches of different sizes: the alternatives stay, the sums within their bounds."""
+    Z = _rows(600, 70001, torch.bfloat16, 12)
+    r = elmo.logprobs(Z, k=20)
+    for n in (0, 1, 599):
+        one = elmo.logprobs(Z[n:n + 1], k=20)
+        assert torch.equal(one.top_idx[0], r.top_idx[n]) and one.row_max[0] == r.row_max[n]
+        assert abs(float(one.log_sum[0] - r.log_sum[n])) <= 2 * _R(70001)
