@@ -1,4 +1,4 @@
-"""Build step for the HIP library: compiles every source under csrc/ for gfx950 into
+"""Build step for the HIP library: compiles every source under csrc/ and csrc_lm/ for gfx950 into
 libelmo_xmc.so next to this file (in-tree, so it travels with the source tree).
 
 Each source is compiled to its own object (in parallel, under _build/ at the repository root),

@@ -149,7 +149,7 @@ __device__ __forceinline__ int64_t vec_at(int64_t i, int D, int64_t ld) {
 
 // Elementwise, bound by HBM: each thread takes 8 features (one 16-byte load of a 16-bit type), the
 // four threads of a block of 32 share their largest magnitude. 16384 x 4096 BF16 with gelu in 53 us
-// (6.4 TB/s), relu 52, kept alone 36 (5.6 TB/s).
+// (6.4 TB/s), relu 52, kept alone 37 (5.5 TB/s).
 template <typename E, int ACT, bool OUT>
 __global__ __launch_bounds__(256) void k_ckpt8_save(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(256) void k_ckpt8_load(Ckpt8Args a) {
 }
 
 // dx = dy act'(x) with x from its 8 bits; dx may be dy's own memory. Bound by HBM: 16384 x 4096 BF16 in
-// 53 us with relu (6.3 TB/s), 57 with silu and 59 with gelu (5.7), whose arithmetic is not all hidden.
+// 55 us with relu (6.2 TB/s), 57 with silu and 59 with gelu (5.7), whose arithmetic is not all hidden.
 template <typename E, int ACT>
 __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.n8; i += (int64_t)gridDim.x * 256) {
@@ -230,7 +230,8 @@ __global__ __launch_bounds__(256) void k_ckpt8_act_grad(Ckpt8Args a) {
 // conflicts counted). Bound by latency: one wave per SIMD has nothing to run while it waits. 16384
 // tokens, 2048 x 4096, the join included: 269 us on inputs used again and 294 (936 TFLOP/s) on inputs
 // that change from call to call, where the library's BF16 product of the decoded operands, timed in
-// turn with it, takes 245 and 255. On changing inputs the matrix cores are busy 41% of the cycles, LDS
+// turn with it, takes 245 and 255. (The product alone 271, the join 18; the first dozen launches after an
+// idle time take 300 to 345.) On changing inputs the matrix cores are busy 41% of the cycles, LDS
 // 21%, and the waves spend 39% of theirs waiting for data or at the barrier.
 // Few tiles split the tokens over `segs` blocks, whose partial tiles k_wgrad_join adds in order.
 constexpr int WG_BK = 32;

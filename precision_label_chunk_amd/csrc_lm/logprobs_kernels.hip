@@ -14,9 +14,10 @@
 // batches split every row over several blocks whose (m, s, t) and candidate keys a second kernel
 // joins in a fixed order.
 //
-// Bound by HBM: 4096 rows of 131072 BF16 logits in 180 us (5.95 TB/s), 256 rows of 670000 FP32 logits
-// in 112 us (6.1 TB/s). With alternatives the comparisons come close to the arithmetic that the read
-// hides: top 5 of the FP32 rows 117 us, top 20 of the BF16 rows 188 us, top 64 222 us.
+// Bound by HBM (medians of calls on logits that change from call to call): 4096 rows of 131072 BF16
+// logits in 185 us (5.8 TB/s), 256 rows of 670000 FP32 logits in 118 us (5.8 TB/s). With alternatives the
+// comparisons come close to the arithmetic that the read hides: top 5 of the FP32 rows 125 us, top 20 of
+// the BF16 rows 194 us, top 64 225 us.
 #include "elem_types.hpp"
 #include "lm_kernels.hpp"
 #include "wave_top.hpp"
@@ -346,8 +347,8 @@ __global__ __launch_bounds__(LP_THREADS) void k_logprobs_join(LogprobArgs a) {
 // With upstream gradients g_j of logp_j, gH of H and gL of log s + m (the log partition):
 //   dz_v = p_v (gL - sum_j g_j - gH (log p_v + H)) + sum_{j: id_j = v} g_j,
 // p_v = 2^((z_v - m) log2 e - log2 s). Elementwise, bound by HBM (the logits read, the gradient
-// written: 4096 x 131072 BF16 in 350 us, 6.1 TB/s). The few elements that a given token names are computed before the block's pass over its
-// segment and written after it, so that dZ may be the logits' own memory; a token given more than
+// written: 4096 x 131072 BF16 in 352 us, 6.1 TB/s, median). The few elements that a given token names are
+// computed before the block's pass over its segment and written after it, so that dZ may be the logits' own memory; a token given more than
 // once is summed in the order of its places, by the thread of its first.
 struct LogprobGradArgs {
   const void* Z; int64_t N, V, ldz;

@@ -119,9 +119,9 @@ __device__ __forceinline__ void store_tile(const W4Args& a, int64_t tile, int n0
 // D <= 256 UNITS and N <= 16: the feature rows stay in registers, 32 per unit, for all the tiles a wave
 // takes, and the loop reads nothing but weights, a whole tile (adjacent rows) at a time. The next
 // tile's codes are loaded before the present one's products.
-// Bound by HBM: 3M x 768 labels with one row in 220 us (5.6 TB/s), with 16 rows in 302 (4.7 TB/s: the
+// Bound by HBM: 3M x 768 labels with one row in 222 us (5.6 TB/s), with 16 rows in 302 (4.7 TB/s: the
 // results, 64 bytes to a row and tile, are written slower than weights are read); 131072 x 768 with
-// one row in 11 us (4.9 TB/s). Rows in LDS instead take 338 us against 304 at 3M x 768 with 16 rows,
+// one row in 13 us (4.1 TB/s; 11 where the 53 MB of weights are still in the last-level cache). Rows in LDS instead take 338 us against 304 at 3M x 768 with 16 rows,
 // the simple form that reads them again for every tile 640; non-temporal loads of the weights 379 against
 // 322 with plain ones (on an earlier form): adjacent rows share cache lines.
 template <int UNITS>
@@ -170,9 +170,10 @@ __global__ __launch_bounds__(256) void k_w4_mx_regs(W4Args a) {
 // from N on read row N - 1: row n of C depends on row n of A alone, and theirs is not stored. A block
 // keeps them for all the tiles it takes. KS waves share a tile, each taking every KS-th unit and the
 // sums joined through LDS; the next unit's codes are loaded before the present one's products. NT
-// tiles of 16 feature rows. Bound by HBM with one row (65536 x 4096 in 28 us, 5.2 TB/s); more rows fall
-// off from there (16 rows, 131072 x 4096: 66 us, 4.5 TB/s; 32 rows, 200000 x 768: 31 us, 3.5 TB/s),
-// where LDS leaves room for fewer waves.
+// tiles of 16 feature rows. Bound by HBM with one row (65536 x 4096 in 28 us, 5.1 TB/s); more rows fall
+// off from there (16 rows, 131072 x 4096: 67 us, 4.4 TB/s; 32 rows, 200000 x 768: 31 us, 3.5 TB/s),
+// where LDS leaves room for fewer waves and every KiB of codes takes 4 (at 32 rows 8) of fragments from
+// LDS. (Weights from HBM at each call; the first and the last take 26 us on weights kept in the last-level cache.)
 template <int NT, int KS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_w4_mx_lds(W4Args a) {
   constexpr int GR = WAVES / KS, V = 4 * NT;
@@ -245,8 +246,9 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_mx_lds(W4Args a) {
 }
 
 // Feature rows that do not fit LDS, where panels do not serve: KS waves share LT tiles, each taking every KS-th
-// unit; the rows come from the caches, once per LT tiles. Sums joined through LDS. 16
-// rows of 16384 features, 32768 labels, BF16 results: 122 us, 2.3 TB/s (FP32 results, in panels: 88).
+// unit; the rows come from the caches, once per LT tiles, which is more than the weights' own bytes. Sums
+// joined through LDS. 16 rows of 16384 features, 32768 labels, BF16 results: 123 us, 2.3 TB/s (FP32
+// results, in panels: 91).
 template <int NT, int LT, int KS>
 __global__ __launch_bounds__(64 * KS) void k_w4_mx_deep(W4Args a) {
   constexpr int V = LT * NT * 4;
@@ -410,9 +412,10 @@ __device__ __forceinline__ void int_unit(const IntUnit& m, float* acc, X&& frag,
 // Feature rows in LDS as in k_w4_mx_lds ([chunk of 8 features][row], in the decode's order within a
 // chunk, a unit of zeros behind the last; N <= 4: lanes outside their block read that at stride 0),
 // then the features' sums, [unit][4 q + b] (N <= 4) or [unit][group][row]. KS waves share a tile, each
-// taking every KS-th unit, one unit ahead. Groups of 128: one row, 65536 x 4096, in 37 us (3.7 TB/s),
-// four in 40, 16 rows, 131072 x 4096, in 103 (2.8 TB/s): below the MXFP4 form's
-// 5.2 and 4.5, which has no sums per group; what bounds this one has not been separated.
+// taking every KS-th unit, one unit ahead. Groups of 128: one row, 65536 x 4096, in 38 us (3.6 TB/s),
+// four in 42, 16 rows, 131072 x 4096, in 104 (2.7 TB/s): below the MXFP4 form's
+// 5.1 and 4.4, which has no sums per group and twice the bytes ahead per wave; what bounds this one has
+// not been separated.
 template <int G, int NT, bool FEW, int KS, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
   constexpr int GR = WAVES / KS, SB = FEW ? 4 : 128 / G, V = FEW ? 1 : 4 * NT, SR = FEW ? 4 : 16 * NT;
@@ -495,8 +498,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_w4_int_lds(W4Args a) {
 }
 
 // Feature rows that do not fit LDS, where panels do not serve: the rows from the caches, their sums as
-// products against ones. 24 rows of 8192 features, 32768 labels, BF16 results,
-// in 145 us (1.0 TB/s); with FP32 results, in panels, 101.
+// products against ones. 24 rows of 8192 features, 32768 labels, BF16 results, in 145 us (1.0 TB/s): the
+// rows are read once per tile, six times the weights' bytes. With FP32 results, in panels, 102.
 template <int G, int NT, bool FEW, int KS>
 __global__ __launch_bounds__(64 * KS) void k_w4_int_deep(W4Args a) {
   constexpr int V = FEW ? 1 : 4 * NT, GU = 128 / G;
