@@ -19,9 +19,10 @@ enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 // Phi(x) and e^(-x^2/2), the normal distribution and its unscaled density. With z = |x| / sqrt 2 and
 // t = 1 / (1 + c z), erfc(z) / 2 = e^(-z^2) t P(t), P fitted to erfcx(z) / (2 t) over z <= 11 for the
 // smallest relative error; the tail keeps its relative accuracy because nothing is subtracted from 1
-// there. For FP32 outputs c = 0.3 and degree 8 (2.0e-8; in binary32 within 9e-7 of Phi relative for
-// |x| < 5, 4e-6 beyond), for 16-bit ones c = 0.5 and degree 6 (1.7e-6, a two-hundredth of FP16's
-// rounding): the activation is as long as the memory traffic that hides it, and two operations less.
+// there. For FP32 outputs c = 0.3 and degree 8 (2.0e-8; in binary32 x Phi(x) is within 6e-7 relative down
+// to x = -13), for 16-bit ones c = 0.5, degree 6 (1.7e-6, a two-hundredth of FP16's rounding) and a plain
+// exponent (1.5e-5 at x = -13): the activation is as long as the memory traffic that hides it, and eight
+// operations less.
 template <bool FINE>
 __device__ __forceinline__ void normal_parts(float x, float& cdf, float& dens) {
   float t, p;
@@ -46,8 +47,19 @@ __device__ __forceinline__ void normal_parts(float x, float& cdf, float& dens) {
     p = __builtin_fmaf(p, t, 0.13899248838424683f);
     p = __builtin_fmaf(p, t, 0.14115135371685028f);
   }
-  const float u = x * 0.84932180028801904f;                // sqrt(log2(e) / 2)
-  dens = __builtin_amdgcn_exp2f(-(u * u));
+  if constexpr (FINE) {
+    // y = -x^2 log2(e) / 2 is rounded three times (the square, the constant, their product), which alone
+    // is x^2 / 2 times as large in the result: what they left out, dy, is put back as 1 + dy ln 2
+    const float c = __builtin_fminf(__builtin_fabsf(x), 16.0f), s = c * c, y = s * -0.72134751081466675f;
+    float dy = __builtin_fmaf(s, -0.72134751081466675f, -y);
+    dy = __builtin_fmaf(__builtin_fmaf(c, c, -s), -0.72134751081466675f, dy);
+    dy = __builtin_fmaf(s, -9.62981517e-09f, dy);
+    dens = __builtin_amdgcn_exp2f(y);
+    dens = __builtin_fmaf(dens, dy * 0.69314718f, dens);
+  } else {
+    const float u = x * 0.84932180028801904f;              // sqrt(log2(e) / 2)
+    dens = __builtin_amdgcn_exp2f(-(u * u));
+  }
   const float half = t * p * dens;
   cdf = x < 0.0f ? half : 1.0f - half;
 }

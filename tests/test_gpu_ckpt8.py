@@ -310,3 +310,20 @@ def test_weight_grad_workspace_is_device_bytes(elmo):
             elmo.ckpt8_weight_grad(dy, codes, scales, workspace=bad)
     fine = torch.zeros(need, dtype=torch.uint8, device="cuda")
     assert torch.equal(elmo.ckpt8_weight_grad(dy, codes, scales, workspace=fine), want)
+
+
+@pytest.mark.parametrize("lo,hi", [(-13, -10), (-10, -9), (-9, -7), (-7, -5), (-5, -3), (-3, 0), (0, 3), (3, 14)])
+def test_activations_over_their_ranges(elmo, lo, hi):
+    """FP32 silu and gelu of four million values each: within the bounds above everywhere, their tails included."""
+    g = torch.Generator(device="cuda").manual_seed(lo + 100)
+    x = (torch.rand((1024, 4096), generator=g, device="cuda", dtype=torch.float64) * (hi - lo) + lo).float()
+    for act in ("silu", "gelu"):
+        codes, scales, y = elmo.ckpt8_save(x, act=act)
+        for got, at, part in ((y, x.double(), 0),
+                              (elmo.ckpt8_act_grad(torch.ones_like(x), codes, scales, act),
+                               elmo.ckpt8_load(codes, scales, dtype=torch.float32).double(), 1)):
+            v = _act64(at, act)
+            ref, tol = v[part], v[part + 2]
+            off = (got.double() - ref).abs()
+            over = off / (tol + U * ref.abs() + TINY[torch.float32])
+            assert bool((over <= 1).all()), f"{act} {'slope' if part else 'value'}: {over.max():.3f} of the tolerance at {at.flatten()[int(over.argmax())]}"
