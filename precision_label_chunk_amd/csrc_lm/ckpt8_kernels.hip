@@ -21,7 +21,7 @@ enum { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 // smallest relative error; the tail keeps its relative accuracy because nothing is subtracted from 1
 // there. For FP32 outputs c = 0.3 and degree 8 (2.0e-8; in binary32 x Phi(x) is within 6e-7 relative down
 // to x = -13), for 16-bit ones c = 0.5, degree 6 (1.7e-6, a two-hundredth of FP16's rounding) and a plain
-// exponent (1.5e-5 at x = -13): the activation is as long as the memory traffic that hides it, and eight
+// exponent (1.3e-5 at x = -13): the activation is as long as the memory traffic that hides it, and eight
 // operations less.
 template <bool FINE>
 __device__ __forceinline__ void normal_parts(float x, float& cdf, float& dens) {
