@@ -324,6 +324,48 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
                            int D, float* dW, int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Log probabilities of given labels straight from features X and head weights W, without the logits
+ * Z = X W^T ever being kept: the softmax cross entropy of a linear head over a large vocabulary.
+ *
+ *   X        [N, D], W [V, D] of element type `type` (BF16 or FP16), rows of adjacent elements at pitches
+ *            ldx, ldw (elements, >= D, below 2^22 - 63); 16-byte aligned rows.
+ *   ids      [N, M] int32, 0 <= M <= ELMO_MAX_GIVEN (NULL if M = 0); negative: no label (log probability 0 in
+ *            any row); an id >= V gives NaN.
+ *   logp     [N, M] FP32: (z[id] - row_max) - log_sum.
+ *   row_max, log_sum  [N] FP32: max_v z_v and log sum_v e^(z_v - row_max); their sum is the log partition.
+ * Products of exact operands, binary32 sums; logits below 2^126 in magnitude. A row of nothing but -inf logits has row_max
+ * -inf, log_sum 0 and its labels' log probabilities -inf; a NaN or +inf logit makes log_sum and logp of its
+ * row NaN (row_max skips NaN). Results repeat bit for bit on one device.
+ * D % 32 == 0, 32 <= D <= ELMO_MAX_LINEAR_D; 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). The workspace
+ * takes 8 bytes for 128 logits.
+ */
+#define ELMO_MAX_LINEAR_D 65536
+size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int M);
+int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
+                         const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, void* workspace,
+                         size_t workspace_bytes, void* stream);
+/*
+ * The gradients of the above with respect to X and W, from the upstream gradients dlogp [N, M] (NULL if
+ * M = 0) and dlse [N] (nullable: of row_max + log_sum):
+ *   G[n, v] = p_v (dlse - sum_j dlogp_j) + sum_{j : ids_j = v} dlogp_j;  dX = G W;  dW = G^T X.
+ * row_max and log_sum are elmo_linear_logprobs' outputs for the same X and W. The vocabulary goes in pieces
+ * of `chunk` labels (rounded up to a multiple of 256; 0: the library's choice, about 2^26 / N): a piece's logits
+ * are computed again and G held in the workspace in X's type, the one rounding below 32 bits, relative to
+ * each element; sums are binary32. A label given more than once receives the sum of its gradients, a negative
+ * id none. A row of nothing but -inf logits has G = 0; an id >= V makes G NaN in the whole row.
+ *   dX       [N, D] of type `dx_type` (any), dW [V, D] of type `dw_type`, 16-byte aligned rows at pitches lddx,
+ *            lddw; either may be NULL. accumulate: dW is added to, in binary32, and rounded once.
+ * N = 0 leaves dW zero (or as it is with accumulate). Results repeat bit for bit on one device.
+ */
+size_t elmo_linear_logprobs_backward_workspace_bytes(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx,
+                                                     int need_dw);
+int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx,
+                                  int64_t ldw, const int32_t* ids, int M, const float* row_max, const float* log_sum,
+                                  const float* dlogp, const float* dlse, void* dX, int dx_type, int64_t lddx, void* dW,
+                                  int dw_type, int64_t lddw, int accumulate, int64_t chunk, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
  * Test hook: the device codec, stochastic rounding and RNG applied elementwise to n elements.
  *   op 0  BF16 RNE encode:      in0 float[n]            -> out uint16[n]
  *   op 1  E4M3 RNE-sat encode:  in0 float[n]            -> out uint8[n]

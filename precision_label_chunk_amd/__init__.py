@@ -97,6 +97,15 @@ def lib():
         L.elmo_ckpt8_weight_grad_workspace_bytes.restype = sz
         L.elmo_ckpt8_weight_grad.argtypes = [P, i64, P, P, i64, i32, i32, P, i32, P, sz, P]
         L.elmo_ckpt8_weight_grad.restype = i32
+        L.elmo_linear_logprobs_workspace_bytes.argtypes = [i64, i64, i32]
+        L.elmo_linear_logprobs_workspace_bytes.restype = sz
+        L.elmo_linear_logprobs.argtypes = [P, P, i32, i64, i64, i32, i64, i64, P, i32, P, P, P, P, sz, P]
+        L.elmo_linear_logprobs.restype = i32
+        L.elmo_linear_logprobs_backward_workspace_bytes.argtypes = [i64, i64, i32, i32, i64, i32, i32]
+        L.elmo_linear_logprobs_backward_workspace_bytes.restype = sz
+        L.elmo_linear_logprobs_backward.argtypes = [P, P, i32, i64, i64, i32, i64, i64, P, i32, P, P, P, P, P, i32, i64, P, i32,
+                                                    i64, i32, i64, P, sz, P]
+        L.elmo_linear_logprobs_backward.restype = i32
         _lib = L
     return _lib
 
@@ -523,6 +532,80 @@ def ckpt8_weight_grad(dy, codes, scales, out=None, accumulate=False, workspace=N
         dy.data_ptr(), ld, codes.data_ptr(), scales.data_ptr(), T, O, D, out.data_ptr(), int(accumulate),
         workspace.data_ptr(), workspace.numel(), _stream_of(codes.device)))
     return out
+
+
+class LinearLogProbs(NamedTuple):
+    """What linear_logprobs() returns; row_max + log_sum is each row's log partition."""
+    logp: torch.Tensor                   # [N, M]
+    row_max: torch.Tensor                # [N]
+    log_sum: torch.Tensor                # [N]
+
+
+def _linear(X, W, ids):
+    """(element type, N, V, D, M, pitches) of features and head weights."""
+    e = _etype(X)
+    N, D, ldx = _rows("X", X)
+    V, d, ldw = _rows("W", W)
+    if W.dtype != X.dtype or W.device != X.device or d != D:
+        raise ValueError("W must have X's type, device and number of features")
+    M = 0 if ids is None else ids.shape[-1]
+    _like("ids", ids, (N, M), torch.int32, X.device)
+    return e, N, V, D, M, ldx, ldw
+
+
+def linear_logprobs(X, W, ids=None, workspace=None) -> LinearLogProbs:
+    """Log probabilities of the labels `ids` [N, M] int32 under the logits X W^T, which are never kept: X
+    [N, D] and W [V, D] bfloat16 or float16 (D % 32 == 0, any row pitch of whole 16 bytes), with each
+    row's largest logit and log sum. Negative ids stand for no label. See elmo_linear_logprobs in
+    elmo_xmc.h."""
+    e, N, V, D, M, ldx, ldw = _linear(X, W, ids)
+    logp = X.new_empty((N, M), dtype=torch.float32)
+    row_max, log_sum = X.new_empty((2, N), dtype=torch.float32).unbind(0)
+    need = lib().elmo_linear_logprobs_workspace_bytes(N, V, M) if N else 0
+    workspace = _scratch(workspace, need, X)
+    _chk("elmo_linear_logprobs", lib().elmo_linear_logprobs(
+        X.data_ptr(), W.data_ptr(), e, N, V, D, ldx, ldw, _at(ids) if M else None, M, _at(logp) if M else None,
+        row_max.data_ptr(), log_sum.data_ptr(), workspace.data_ptr(), workspace.numel(), _stream_of(X.device)))
+    return LinearLogProbs(logp, row_max, log_sum)
+
+
+def linear_logprobs_backward(X, W, ids, stats: LinearLogProbs, dlogp, dlse=None, need_dx=True, need_dw=True, dx=None,
+                             dw=None, accumulate=False, chunk=0, workspace=None):
+    """(dX [N, D], dW [V, D]) of linear_logprobs(X, W, ids) for the upstream gradients dlogp [N, M] and dlse
+    [N] (of the log partition), from the forward's result `stats`; in X's and W's type, or in that of dx and
+    dw (float32, bfloat16, float16) where given. accumulate=True adds to dw. One that is not needed is None.
+    `chunk` labels are taken at a time (0: the library's choice). See elmo_linear_logprobs_backward in
+    elmo_xmc.h."""
+    e, N, V, D, M, ldx, ldw = _linear(X, W, ids)
+    dev = X.device
+    if M and dlogp is None:
+        raise ValueError("dlogp is missing")
+    _like("dlogp", dlogp, (N, M), torch.float32, dev)
+    _like("dlse", dlse, (N,), torch.float32, dev)
+    _like("row_max", stats.row_max, (N,), torch.float32, dev)
+    _like("log_sum", stats.log_sum, (N,), torch.float32, dev)
+    if not (need_dx or need_dw):
+        raise ValueError("neither dX nor dW is needed")
+    if accumulate and (dw is None or not need_dw):
+        raise ValueError("accumulate needs dw")
+
+    def result(name, t, need, like):
+        if not need:
+            return None, 0, 0
+        if t is None:
+            t = like.new_empty(like.shape)
+        elif t.shape != like.shape or t.device != dev:
+            raise ValueError(f"{name} must be {tuple(like.shape)} on {dev}")
+        return t, _etype(t), _rows(name, t)[2]
+    dx, xt, lddx = result("dx", dx, need_dx, X)
+    dw, wt, lddw = result("dw", dw, need_dw, W)
+    need = lib().elmo_linear_logprobs_backward_workspace_bytes(N, V, D, M, chunk, need_dx, need_dw) if N else 0
+    workspace = _scratch(workspace, need, X)
+    _chk("elmo_linear_logprobs_backward", lib().elmo_linear_logprobs_backward(
+        X.data_ptr(), W.data_ptr(), e, N, V, D, ldx, ldw, _at(ids) if M else None, M, stats.row_max.data_ptr(),
+        stats.log_sum.data_ptr(), _at(dlogp) if M else None, _at(dlse), _at(dx), xt, lddx, _at(dw), wt, lddw,
+        int(accumulate), chunk, workspace.data_ptr(), workspace.numel(), _stream_of(dev)))
+    return dx, dw
 
 
 def numerics_probe(op, in0=None, in1=None, n=None, seed=0, step=0, idx0=0):

@@ -1,0 +1,654 @@
+// Log probabilities of given labels straight from features and weights, and the gradient: softmax cross
+// entropy of a linear head whose logits are never kept.
+//
+// Forward: Z = X W^T tile by tile (256 labels x 256 rows); each wave reduces its 128 labels x 64 rows to a
+// maximum and a sum of e^(z - max) per row, 8 bytes for 128 logits, and picks the given labels' logits
+// out. A second kernel joins the parts of a row.
+//
+// Backward, a piece of the vocabulary at a time: the piece's logits again, as G = c_n p + (given labels'
+// gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch. G is the one
+// rounding below 32 bits: half a unit of its type per element, of its own size (c p of a label that was
+// not given, c p + g of one that was, added before it is rounded, so that a label of probability near 1
+// keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
+// a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38.
+#include "lm_kernels.hpp"
+#include "tile_product.hpp"
+
+namespace elmo {
+
+constexpr float L2E = 1.44269502162933349609375f;          // FP32(log2 e)
+constexpr int LIN_WN = 4, LIN_NBUF = 4, LIN_THREADS = 128 * LIN_WN, LIN_TN = 64 * LIN_WN;
+constexpr int GROUP = 8;                                   // label tiles that are taken together over the rows
+
+// ---- logits ----------------------------------------------------------------------------------------
+struct LogitTiles {
+  const char* X; const char* W;
+  int64_t ldx, ldw;                                        // bytes
+  int64_t N, v0, v1;                                       // rows; labels of the piece
+  int stages, row_tiles, label_tiles;
+  __device__ __forceinline__ void place(int u, int& lt, int& nt) const {
+    const int per = GROUP * row_tiles, g = u / per, r = u % per;
+    const int wide = label_tiles - g * GROUP < GROUP ? label_tiles - g * GROUP : GROUP;
+    nt = r / wide;
+    lt = g * GROUP + r % wide;
+  }
+  __device__ __forceinline__ TileUnit unit(int u) const {
+    int lt, nt;
+    place(u, lt, nt);
+    const int64_t l = v0 + (int64_t)lt * TILE_M, n = (int64_t)nt * LIN_TN;
+    return {{W + l * ldw, ldw, v1 - l, 0}, {X + n * ldx, ldx, N - n, 0}, stages};
+  }
+};
+
+// where a wave's tile of labels from l0 on has a given label: 32 i + 8 (r / 4) + r % 4 of the lane that
+// holds it, else negative
+__device__ __forceinline__ int given_place(int id, int64_t l0, int64_t v1, int half) {
+  const int64_t at = (int64_t)id - l0;
+  if (at < 0 || at >= 128 || id >= v1 || (((int)at >> 2) & 1) != half) return -1;
+  return (int)at - 4 * half;
+}
+
+struct StatArgs {
+  LogitTiles t;
+  const int32_t* ids; int M;
+  float2* part;                                            // [2 label tiles][N]: maximum, sum
+  float* given;                                            // [N][M]: logits of the given labels
+};
+
+struct StatJob : StatArgs {
+  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
+  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+    int lt, nt;
+    t.place(u, lt, nt);
+    const int64_t l0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
+    const int half = lane >> 5;
+    const int64_t left = t.v1 - l0;                        // (wave-uniform)
+    int64_t n[2];
+    int first[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      n[j] = n0 + 32 * j + (lane & 31);
+      first[j] = M > 0 && n[j] < t.N ? ids[n[j] * M] : -1;
+    }
+    if (left < 128) {
+      const int mine = (int)(left < -128 ? -128 : left) - 4 * half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * i + 8 * (r / 4) + r % 4 >= mine) acc[i][0][r] = acc[i][1][r] = -__builtin_inff();
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // e^(z - top) as 2^(z L2E - b), b = FP32(top L2E): what b's rounding leaves out is a factor of the sum
+      const float ref = top == -__builtin_inff() ? 0.0f : top;
+      const float b = ref * L2E, rest = __builtin_fmaf(ref, L2E, -b);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -b));
+        sum += s;
+      }
+      sum += __shfl_xor(sum, 32);
+      sum *= __builtin_amdgcn_exp2f(-rest);
+      if (half == 0 && n[j] < t.N) part[((int64_t)lt * 2 + wm) * t.N + n[j]] = make_float2(top, sum);
+      for (int g = 0; g < M; ++g) {
+        const int id = g == 0 ? first[j] : (n[j] < t.N ? ids[n[j] * M + g] : -1);
+        const int at = given_place(id, l0, t.v1, half);
+        const bool hit = at >= 0;
+        if (__any(hit)) {
+          float z = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (at == 32 * i + 8 * (r / 4) + r % 4) z = acc[i][j][r];
+          if (hit) given[n[j] * M + g] = z;
+        }
+      }
+    }
+  }
+};
+
+template <class Mul>
+__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_stats(StatArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
+  StatJob job;
+  (StatArgs&)job = a;
+  const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
+  tile_stream<Mul, false, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+}
+
+// The parts of 16 rows joined: 16 rows x 64 runs of parts per block, then the runs in the order of a tree.
+__global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t parts, int64_t N, int64_t V, const int32_t* ids,
+                                                   int M, const float* given, float* logp, float* row_max, float* log_sum) {
+  __shared__ float tops[64][16], sums[64][16];
+  const int x = (int)threadIdx.x & 15, y = (int)threadIdx.x >> 4;
+  const int64_t n = (int64_t)blockIdx.x * 16 + x;
+  float top = -__builtin_inff(), sum = 0.0f;
+  auto add = [&](float m, float s) {
+    const float hi = fmaxf(top, m);
+    const float ref = hi == -__builtin_inff() ? 0.0f : hi;
+    sum = sum * __builtin_amdgcn_exp2f((top - ref) * L2E) + s * __builtin_amdgcn_exp2f((m - ref) * L2E);
+    top = hi;
+  };
+  if (n < N) {
+#pragma unroll 4
+    for (int64_t p = y; p < parts; p += 64) {
+      const float2 v = part[p * N + n];
+      add(v.x, v.y);
+    }
+  }
+  tops[y][x] = top;
+  sums[y][x] = sum;
+  for (int k = 32; k > 0; k >>= 1) {
+    __syncthreads();
+    if (y < k) {
+      add(tops[y + k][x], sums[y + k][x]);
+      tops[y][x] = top;
+      sums[y][x] = sum;
+    }
+  }
+  __syncthreads();
+  if (n >= N) return;
+  top = tops[0][x];
+  sum = sums[0][x];
+  const bool empty = top == -__builtin_inff() && sum == 0.0f;
+  const float logs = empty ? 0.0f : logf(sum);
+  if (y == 0) {
+    row_max[n] = top;
+    log_sum[n] = logs;
+  }
+  for (int g = y; g < M; g += 64) {
+    const int id = ids[n * M + g];
+    float v = 0.0f;
+    if (id >= V) v = __builtin_nanf("");
+    else if (id >= 0) v = empty ? -__builtin_inff() : (given[n * M + g] - top) - logs;
+    logp[n * M + g] = v;
+  }
+}
+
+// ---- gradient --------------------------------------------------------------------------------------
+struct CoefArgs {
+  int64_t N, V; int M;
+  const int32_t* ids;
+  const float *row_max, *log_sum, *dlogp, *dlse;
+  float2* most; int parts;                                 // maxima of runs of rows, if taken by themselves
+  float2* coef;                                            // [N]: b, c 2^(what b's rounding left out), scaled
+  float* up;                                               // [N][M]: the given labels' gradients, scaled
+  float* inv;                                              // 1 / scale
+  int f16;
+};
+
+// the largest given gradient of a row, and the bound of |G| in it (finite ones only)
+__device__ __forceinline__ float2 row_bound(const CoefArgs& a, int64_t n) {
+  float most = 0.0f, all = a.dlse ? fabsf(a.dlse[n]) : 0.0f;
+  for (int g = 0; g < a.M; ++g)
+    if (a.ids[n * a.M + g] >= 0) {
+      const float d = fabsf(a.dlogp[n * a.M + g]);
+      if (d < __builtin_inff()) most = fmaxf(most, d);
+      all += 2.0f * d;
+    }
+  return make_float2(most, all < __builtin_inff() ? all : 0.0f);
+}
+__device__ __forceinline__ float2 block_max(float2 v, float2* s) {
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) {
+    v.x = fmaxf(v.x, __shfl_xor(v.x, k));
+    v.y = fmaxf(v.y, __shfl_xor(v.y, k));
+  }
+  if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    v.x = fmaxf(v.x, s[w].x);
+    v.y = fmaxf(v.y, s[w].y);
+  }
+  return v;
+}
+
+__global__ __launch_bounds__(256) void k_lin_bound(CoefArgs a) {
+  __shared__ float2 s[4];
+  float2 v = make_float2(0.0f, 0.0f);
+  for (int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x; n < a.N; n += (int64_t)gridDim.x * 256) {
+    const float2 r = row_bound(a, n);
+    v.x = fmaxf(v.x, r.x);
+    v.y = fmaxf(v.y, r.y);
+  }
+  v = block_max(v, s);
+  if (threadIdx.x == 0) a.most[blockIdx.x] = v;
+}
+
+__global__ __launch_bounds__(256) void k_lin_coef(CoefArgs a) {
+  __shared__ float2 s[4];
+  float2 v = make_float2(0.0f, 0.0f);
+  if (a.parts > 0) {
+    for (int i = (int)threadIdx.x; i < a.parts; i += 256) {
+      v.x = fmaxf(v.x, a.most[i].x);
+      v.y = fmaxf(v.y, a.most[i].y);
+    }
+  } else {
+    for (int64_t n = threadIdx.x; n < a.N; n += 256) {
+      const float2 r = row_bound(a, n);
+      v.x = fmaxf(v.x, r.x);
+      v.y = fmaxf(v.y, r.y);
+    }
+  }
+  v = block_max(v, s);
+  // unit: what becomes 1 (the largest given gradient, or else the bound); FP16: times the power of two
+  // that brings the bound into [2^14, 2^15)
+  float unit = v.x > 0.0f ? v.x : v.y;
+  unit = fminf(fmaxf(unit, 1e-30f), 1e30f);
+  if (a.f16) {
+    const float ratio = fmaxf(v.y / unit, 1e-30f);
+    unit = ldexpf(unit, __builtin_amdgcn_frexp_expf(ratio) - 15);
+  }
+  const float scale = 1.0f / unit;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = unit;
+  const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+  if (n >= a.N) return;
+  const double lse = (double)a.row_max[n] + (double)a.log_sum[n];
+  const bool empty = lse == -__builtin_inf();
+  float c = a.dlse ? a.dlse[n] : 0.0f;
+  for (int g = 0; g < a.M; ++g) {
+    const int id = a.ids[n * a.M + g];
+    float d = 0.0f;
+    if (id >= 0) d = a.dlogp[n * a.M + g];
+    if (id >= a.V) c = __builtin_nanf("");
+    c -= d;
+    a.up[n * a.M + g] = empty ? 0.0f : d * scale;
+  }
+  // p = 2^(z L2E - lse L2E): exact for z = lse, where 1 - p needs it
+  const double bd = empty ? 0.0 : lse * (double)L2E;
+  const float b = (float)bd;
+  a.coef[n] = make_float2(b, empty ? 0.0f : c * scale * __builtin_amdgcn_exp2f(-(float)(bd - (double)b)));
+}
+
+template <class Mul>
+__device__ __forceinline__ int pack16(float lo, float hi) {
+  if constexpr (std::is_same_v<Mul, MulF16>) {
+    typedef _Float16 f16x2_v __attribute__((ext_vector_type(2)));
+    typedef float f32x2_v __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(int, __builtin_convertvector((f32x2_v){lo, hi}, f16x2_v));
+  } else {
+    return (int)pack_bf16x2(lo, hi);
+  }
+}
+
+struct GradArgs {
+  LogitTiles t;
+  const int32_t* ids; int M;
+  const float2* coef; const float* up;
+  char* G; int64_t ldg;                                    // [N] rows of the piece's labels; bytes
+};
+
+template <class Mul>
+struct GradJob : GradArgs {
+  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
+  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+    int lt, nt;
+    t.place(u, lt, nt);
+    const int64_t col0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
+    const int half = lane >> 5;
+    const int64_t l0 = t.v0 + col0, left = t.v1 - l0;      // (wave-uniform)
+    int64_t n[2];
+    float2 cf[2];
+    int first[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      n[j] = n0 + 32 * j + (lane & 31);
+      const bool in = n[j] < t.N;
+      cf[j] = in ? coef[n[j]] : make_float2(0.0f, 0.0f);
+      first[j] = M > 0 && in ? ids[n[j] * M] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -cf[j].x)) * cf[j].y;
+      for (int g = 0; g < M; ++g) {
+        const int id = g == 0 ? first[j] : (n[j] < t.N ? ids[n[j] * M + g] : -1);
+        const int at = given_place(id, l0, t.v1, half);
+        const bool hit = at >= 0;
+        if (__any(hit)) {
+          const float d = hit ? up[n[j] * M + g] : 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (at == 32 * i + 8 * (r / 4) + r % 4) acc[i][j][r] += d;
+        }
+      }
+    }
+    if (left < 128) {                                      // labels past the last: no share in dX
+      const int mine = (int)(left < -128 ? -128 : left) - 4 * half;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * i + 8 * (r / 4) + r % 4 >= mine) acc[i][0][r] = acc[i][1][r] = 0.0f;
+    }
+    // a lane has 4 labels of every 8; it swaps with the lane of the other half, so that each stores 8
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      char* row = G + n[j] * ldg + 2 * (col0 + 8 * half);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; q += 2) {
+          int lo[2], hi[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            lo[k] = pack16<Mul>(acc[i][j][4 * q + 2 * k], acc[i][j][4 * q + 2 * k + 1]);
+            hi[k] = pack16<Mul>(acc[i][j][4 * q + 4 + 2 * k], acc[i][j][4 * q + 5 + 2 * k]);
+            auto sw = __builtin_amdgcn_permlane32_swap(lo[k], hi[k], false, false);
+            lo[k] = (int)sw[0];
+            hi[k] = (int)sw[1];
+          }
+          if (n[j] < t.N) *(i32x4_t*)(row + 2 * (32 * i + 8 * q)) = i32x4_t{lo[0], lo[1], hi[0], hi[1]};
+        }
+    }
+  }
+};
+
+template <class Mul>
+__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_grad_logits(GradArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
+  GradJob<Mul> job;
+  (GradArgs&)job = a;
+  const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
+  tile_stream<Mul, false, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+}
+
+// dW = G^T X: rows of the result are labels (n of the tile), its columns features (m)
+struct OutArgs { void* out; int64_t ld; int type; int accumulate; };   // ld in elements
+struct ProductArgs {
+  const char* X; int64_t ldx;
+  const char* W; int64_t ldw;
+  const char* G; int64_t ldg;
+  int64_t N, v0, v1, cols;                                 // cols: the piece's labels, a multiple of 256
+  int D, d_tiles;
+  const float* inv;
+  // dW: the tokens in w_slots runs of w_per; one run goes to the result, several to `wpart`
+  int w_units, w_slots; int64_t w_per;
+  float* wpart; OutArgs dW;
+  // dX: the piece's labels in x_slots runs of x_per, each added to its partial sum
+  int x_units, x_slots, first; int64_t x_per;
+  float* xpart;
+};
+
+__device__ __forceinline__ void store4(const OutArgs& o, int64_t row, int64_t col, f32x4_t v) {
+  if (o.type == T_F32_) {
+    f32x4_t* p = (f32x4_t*)((float*)o.out + row * o.ld + col);
+    *p = o.accumulate ? *p + v : v;
+  } else {
+    uint16_t* p = (uint16_t*)o.out + row * o.ld + col;
+    i32x2_t w = *(const i32x2_t*)p;
+    if (o.type == T_BF16_) {
+      if (o.accumulate) v += f32x4_t{bf16_to_f32(w[0] & 0xffff), bf16_to_f32((uint32_t)w[0] >> 16), bf16_to_f32(w[1] & 0xffff), bf16_to_f32((uint32_t)w[1] >> 16)};
+      w = i32x2_t{pack16<MulBF16>(v[0], v[1]), pack16<MulBF16>(v[2], v[3])};
+    } else {
+      if (o.accumulate)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += (float)__builtin_bit_cast(_Float16, (uint16_t)((uint32_t)w[i / 2] >> 16 * (i % 2)));
+      w = i32x2_t{pack16<MulF16>(v[0], v[1]), pack16<MulF16>(v[2], v[3])};
+    }
+    *(i32x2_t*)p = w;
+  }
+}
+
+struct WeightJob : ProductArgs {
+  __device__ __forceinline__ void place(int u, int& dt, int& vt, int& slot) const {
+    dt = u % d_tiles;
+    slot = u / d_tiles % w_slots;
+    vt = u / d_tiles / w_slots;
+  }
+  __device__ __forceinline__ TileUnit unit(int u) const {
+    int dt, vt, slot;
+    place(u, dt, vt, slot);
+    const int64_t t0 = slot * w_per, left = N - t0, rows = left < w_per ? left : w_per;
+    const int d0 = dt * TILE_M, v = vt * LIN_TN;
+    const int dc = D - d0 < TILE_M ? D - d0 : TILE_M;
+    return {{X + t0 * ldx + 2 * d0, ldx, rows, 2 * dc}, {G + t0 * ldg + 2 * (int64_t)v, ldg, rows, 2 * LIN_TN}, (int)((rows + 31) / 32)};
+  }
+  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+    int dt, vt, slot;
+    place(u, dt, vt, slot);
+    const float f = *inv;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t c = (int64_t)vt * LIN_TN + 64 * wn + 32 * j + (lane & 31), v = v0 + c;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = dt * TILE_M + 128 * wm + 32 * i + 8 * q + 4 * (lane >> 5);
+          const f32x4_t s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (v < v1 && d < D) {
+            if (w_slots > 1) *(f32x4_t*)(wpart + ((int64_t)slot * cols + c) * D + d) = s;
+            else store4(dW, v, d, s * f);
+          }
+        }
+    }
+  }
+};
+
+struct FeatureJob : ProductArgs {
+  __device__ __forceinline__ void place(int u, int& dt, int& nt, int& slot) const {
+    dt = u % d_tiles;
+    slot = u / d_tiles % x_slots;
+    nt = u / d_tiles / x_slots;
+  }
+  __device__ __forceinline__ TileUnit unit(int u) const {
+    int dt, nt, slot;
+    place(u, dt, nt, slot);
+    const int64_t c0 = slot * x_per, n = (int64_t)nt * LIN_TN;
+    const int64_t left = cols - c0, len = left < x_per ? left : x_per;
+    const int d0 = dt * TILE_M, dc = D - d0 < TILE_M ? D - d0 : TILE_M;
+    return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, N - n, 0}, (int)(len / 32)};
+  }
+  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+    int dt, nt, slot;
+    place(u, dt, nt, slot);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t n = (int64_t)nt * LIN_TN + 64 * wn + 32 * j + (lane & 31);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int d = dt * TILE_M + 128 * wm + 32 * i + 8 * q + 4 * (lane >> 5);
+          f32x4_t s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          if (n < N && d < D) {
+            f32x4_t* p = (f32x4_t*)(xpart + ((int64_t)slot * N + n) * D + d);
+            if (!first) s += *p;
+            *p = s;
+          }
+        }
+    }
+  }
+};
+
+template <class Mul>
+__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_products(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
+  if (a.w_units > 0) {
+    WeightJob job;
+    (ProductArgs&)job = a;
+    const UnitRange r = xcd_units(a.w_units);
+    tile_stream<Mul, true, true, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+  }
+  if (a.x_units > 0) {
+    FeatureJob job;
+    (ProductArgs&)job = a;
+    const UnitRange r = xcd_units(a.x_units);
+    tile_stream<Mul, true, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+  }
+}
+
+// rows [r0, r0 + rows) of a result from the partial sums of `slots` runs, in the order of the runs
+__global__ __launch_bounds__(256) void k_lin_sum(const float* part, int64_t stride, int slots, int64_t r0, int64_t rows, int D,
+                                                 const float* inv, OutArgs o) {
+  const float f = *inv;
+  const int d4 = D / 4;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < rows * d4; i += (int64_t)gridDim.x * 256) {
+    f32x4_t s = *(const f32x4_t*)(part + i * 4);
+    for (int k = 1; k < slots; ++k) s += *(const f32x4_t*)(part + k * stride + i * 4);
+    store4(o, r0 + i / d4, i % d4 * 4, s * f);
+  }
+}
+
+// ---- launchers -------------------------------------------------------------------------------------
+static unsigned blocks_for(int64_t units) {
+  const int64_t cus = device_cus();
+  return (unsigned)(units < cus ? units : cus);
+}
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+LinearLayout linear_layout(int64_t N, int64_t V, int M) {
+  LinearLayout s{};
+  s.parts = 2 * ceil_div(V, TILE_M);
+  s.part = 0;
+  s.given = up256((size_t)s.parts * N * 8);
+  s.total = s.given + up256((size_t)N * (M > 0 ? M : 1) * 4);
+  return s;
+}
+
+static LogitTiles tiles_of(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t N, int64_t v0, int64_t v1, int D) {
+  LogitTiles t{};
+  t.X = (const char*)X; t.W = (const char*)W; t.ldx = 2 * ldx; t.ldw = 2 * ldw;
+  t.N = N; t.v0 = v0; t.v1 = v1; t.stages = D / 32;
+  t.row_tiles = (int)ceil_div(N, LIN_TN); t.label_tiles = (int)ceil_div(v1 - v0, TILE_M);
+  return t;
+}
+
+int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
+                        const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, const LinearLayout& s,
+                        void* workspace, hipStream_t st) {
+  char* ws = (char*)workspace;
+  StatArgs a{};
+  a.t = tiles_of(X, ldx, W, ldw, N, 0, V, D);
+  a.ids = ids; a.M = M; a.part = (float2*)(ws + s.part); a.given = (float*)(ws + s.given);
+  const unsigned grid = blocks_for((int64_t)a.t.row_tiles * a.t.label_tiles);
+  if (type == T_BF16_) hipLaunchKernelGGL(k_lin_stats<MulBF16>, dim3(grid), dim3(LIN_THREADS), 0, st, a);
+  else hipLaunchKernelGGL(k_lin_stats<MulF16>, dim3(grid), dim3(LIN_THREADS), 0, st, a);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  hipLaunchKernelGGL(k_lin_join, dim3((unsigned)ceil_div(N, 16)), dim3(1024), 0, st, a.part, s.parts, N, V, ids, M, a.given, logp,
+                     row_max, log_sum);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+// The piece: 2^26 gradient codes (128 MiB, which the last-level cache holds) or the caller's number of
+// labels, a multiple of 256; pieces of about equal length. Runs: so many that a launch has a unit for
+// every compute unit, as long as a run keeps 16 stages.
+LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
+  LinearGradLayout s{};
+  const int64_t whole = ceil_div(V, TILE_M) * TILE_M;
+  int64_t piece = chunk > 0 ? ceil_div(chunk, TILE_M) * TILE_M : (int64_t(1) << 26) / N / TILE_M * TILE_M;
+  if (piece < TILE_M) piece = TILE_M;
+  if (piece > whole) piece = whole;
+  const int64_t pieces = ceil_div(whole, piece);
+  s.piece = ceil_div(ceil_div(whole, pieces), TILE_M) * TILE_M;
+  const int64_t cus = device_cus(), dt = ceil_div(D, TILE_M);
+  const int64_t wt = s.piece / LIN_TN * dt, xt = ceil_div(N, LIN_TN) * dt;   // tiles of dW and dX
+  const int64_t wst = ceil_div(N, 32), xst = s.piece / 32;                   // their stages
+  s.w_slots = s.x_slots = 1;
+  // runs of about the same number of stages in both, no more than it takes to fill the device
+  const int64_t stages = (need_dw ? wt * wst : 0) + (need_dx ? xt * xst : 0);
+  int64_t run = ceil_div(stages, cus);
+  if (run < 16) run = 16;
+  auto slots_of = [&](int64_t st) { const int64_t k = (st + run / 2) / run; return k < 1 ? 1 : k; };
+  s.x_slots = (int)slots_of(xst);
+  s.x_per = ceil_div(xst, s.x_slots) * 32;
+  s.x_slots = (int)ceil_div(s.piece, s.x_per);
+  s.w_slots = wt >= cus ? 1 : (int)slots_of(wst);
+  s.w_per = ceil_div(wst, s.w_slots) * 32;
+  s.w_slots = (int)ceil_div(N, s.w_per);
+  size_t at = 0;
+  s.most = at; at += up256(256 * 8);
+  s.inv = at; at += 256;
+  s.coef = at; at += up256((size_t)N * 8);
+  s.up = at; at += up256((size_t)N * (M > 0 ? M : 1) * 4);
+  s.G = at; at += up256((size_t)N * s.piece * 2);
+  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * N * D * 4);
+  s.wpart = at; if (need_dw && s.w_slots > 1) at += up256((size_t)s.w_slots * s.piece * D * 4);
+  s.total = at;
+  return s;
+}
+
+template <class Mul>
+static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws, hipStream_t st) {
+  CoefArgs k{};
+  k.N = c.N; k.V = c.V; k.M = c.M; k.ids = c.ids; k.row_max = c.row_max; k.log_sum = c.log_sum; k.dlogp = c.dlogp; k.dlse = c.dlse;
+  k.most = (float2*)(ws + s.most); k.coef = (float2*)(ws + s.coef); k.up = (float*)(ws + s.up); k.inv = (float*)(ws + s.inv);
+  k.f16 = std::is_same_v<Mul, MulF16>;
+  // rows that every block can go through by itself need no launch for their bound
+  k.parts = c.N <= 8192 ? 0 : 256;
+  if (k.parts) hipLaunchKernelGGL(k_lin_bound, dim3(k.parts), dim3(256), 0, st, k);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  hipLaunchKernelGGL(k_lin_coef, dim3((unsigned)ceil_div(c.N, 256)), dim3(256), 0, st, k);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  for (int64_t v0 = 0; v0 < c.V; v0 += s.piece) {
+    const int64_t v1 = v0 + s.piece < c.V ? v0 + s.piece : c.V;
+    GradArgs g{};
+    g.t = tiles_of(c.X, c.ldx, c.W, c.ldw, c.N, v0, v1, c.D);
+    g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.G = ws + s.G; g.ldg = 2 * s.piece;
+    hipLaunchKernelGGL(k_lin_grad_logits<Mul>, dim3(blocks_for((int64_t)g.t.row_tiles * g.t.label_tiles)), dim3(LIN_THREADS), 0, st, g);
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+    ProductArgs p{};
+    p.X = (const char*)c.X; p.ldx = 2 * c.ldx; p.W = (const char*)c.W; p.ldw = 2 * c.ldw; p.G = ws + s.G; p.ldg = 2 * s.piece;
+    p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, TILE_M); p.inv = k.inv;
+    p.cols = ceil_div(v1 - v0, TILE_M) * TILE_M;
+    p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
+    p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
+    p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0; p.xpart = (float*)(ws + s.xpart);
+    p.w_units = c.dW ? (int)(p.cols / LIN_TN) * p.d_tiles * p.w_slots : 0;
+    p.x_units = c.dX ? (int)ceil_div(c.N, LIN_TN) * p.d_tiles * p.x_slots : 0;
+    hipLaunchKernelGGL(k_lin_products<Mul>, dim3(blocks_for((int64_t)p.w_units + p.x_units)), dim3(LIN_THREADS), 0, st, p);
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+    if (c.dW && p.w_slots > 1) {
+      const int64_t n = (v1 - v0) * (c.D / 4);
+      const int64_t want = ceil_div(n, 256), cap = 16 * (int64_t)device_cus();
+      hipLaunchKernelGGL(k_lin_sum, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, p.wpart, p.cols * c.D, p.w_slots, v0,
+                         v1 - v0, c.D, (const float*)k.inv, p.dW);
+      if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+    }
+  }
+  if (c.dX) {
+    const int64_t n = c.N * (c.D / 4), want = ceil_div(n, 256), cap = 16 * (int64_t)device_cus();
+    hipLaunchKernelGGL(k_lin_sum, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, (const float*)(ws + s.xpart), c.N * c.D,
+                       s.x_slots, (int64_t)0, c.N, c.D, (const float*)k.inv, OutArgs{c.dX, c.lddx, c.dx_type, 0});
+    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  }
+  return ELMO_OK_;
+}
+
+// a gradient over no rows
+__global__ __launch_bounds__(256) void k_lin_zero(OutArgs o, int64_t rows, int D) {
+  const int d4 = D / 4;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < rows * d4; i += (int64_t)gridDim.x * 256)
+    store4(o, i / d4, i % d4 * 4, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+}
+
+int run_zero_rows(void* out, int type, int64_t rows, int D, int64_t ld, hipStream_t st) {
+  const int64_t want = ceil_div(rows * (D / 4), 256), cap = 16 * (int64_t)device_cus();
+  hipLaunchKernelGGL(k_lin_zero, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, OutArgs{out, ld, type, 0}, rows, D);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+int run_linear_logprobs_grad(const LinearGradCall& c, const LinearGradLayout& s, void* workspace, hipStream_t st) {
+  return c.type == T_BF16_ ? grad_as<MulBF16>(c, s, (char*)workspace, st) : grad_as<MulF16>(c, s, (char*)workspace, st);
+}
+
+}  // namespace elmo

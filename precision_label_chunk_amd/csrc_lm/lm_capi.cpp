@@ -32,6 +32,17 @@ int check_ckpt8(int type, int64_t T, int D) {
   return ELMO_OK;
 }
 
+// features and head weights of 16-bit elements, K = D: 16-byte aligned rows, 256 of them within 2^31 bytes
+constexpr int64_t MAX_LINEAR_LD = (1 << 22) - 64;
+int check_linear(int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw, int M) {
+  if (type != ELMO_T_BF16 && type != ELMO_T_F16) return ELMO_EDTYPE;
+  if (N < 0 || N >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (D < 32 || D % 32 != 0 || D > ELMO_MAX_LINEAR_D || M < 0 || M > ELMO_MAX_GIVEN) return ELMO_ESHAPE;
+  if (ldx < D || ldw < D || ldx > MAX_LINEAR_LD || ldw > MAX_LINEAR_LD) return ELMO_ESHAPE;
+  if (((N + 255) / 256) * ((V + 255) / 256) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  return ELMO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -145,6 +156,61 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
   const elmo::WgradLayout s = elmo::wgrad_layout(T, O, D);
   if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
   return elmo::run_ckpt8_wgrad(dY, ldy, codes, scales, T, O, D, dW, accumulate, s, workspace, (hipStream_t)stream);
+}
+
+size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int M) {
+  if (N < 1 || check_linear(ELMO_T_BF16, N, V, 32, 32, 32, M) != ELMO_OK) return 0;
+  return elmo::linear_layout(N, V, M).total;
+}
+
+int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
+                         const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const int rc = check_linear(type, N, V, D, ldx, ldw, M);
+  if (rc != ELMO_OK) return rc;
+  if (N == 0) return ELMO_OK;
+  if (!X || !W || !row_max || !log_sum || (M > 0 && (!ids || !logp))) return ELMO_EINVAL;
+  if (!rows16(X, type, ldx) || !rows16(W, type, ldw)) return ELMO_EINVAL;
+  for (const void* p : {(const void*)ids, (const void*)logp, (const void*)row_max, (const void*)log_sum})
+    if (!aligned_to(p, 4)) return ELMO_EINVAL;
+  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
+  const elmo::LinearLayout s = elmo::linear_layout(N, V, M);
+  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  return elmo::run_linear_logprobs(X, W, type, N, V, D, ldx, ldw, ids, M, logp, row_max, log_sum, s, workspace,
+                                   (hipStream_t)stream);
+}
+
+size_t elmo_linear_logprobs_backward_workspace_bytes(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx,
+                                                     int need_dw) {
+  if (N < 1 || chunk < 0 || check_linear(ELMO_T_BF16, N, V, D, D, D, M) != ELMO_OK) return 0;
+  return elmo::linear_grad_layout(N, V, D, M, chunk, need_dx, need_dw).total;
+}
+
+int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx,
+                                  int64_t ldw, const int32_t* ids, int M, const float* row_max, const float* log_sum,
+                                  const float* dlogp, const float* dlse, void* dX, int dx_type, int64_t lddx, void* dW,
+                                  int dw_type, int64_t lddw, int accumulate, int64_t chunk, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  const int rc = check_linear(type, N, V, D, ldx, ldw, M);
+  if (rc != ELMO_OK) return rc;
+  if ((dX && !known_type(dx_type)) || (dW && !known_type(dw_type))) return ELMO_EDTYPE;
+  if (chunk < 0 || (dX && lddx < D) || (dW && lddw < D)) return ELMO_ESHAPE;
+  if (!dX && !dW) return ELMO_EINVAL;
+  if (N == 0 && !dW) return ELMO_OK;
+  if ((dX && !rows16(dX, dx_type, lddx)) || (dW && !rows16(dW, dw_type, lddw))) return ELMO_EINVAL;
+  if (N == 0) return accumulate ? ELMO_OK : elmo::run_zero_rows(dW, dw_type, V, D, lddw, (hipStream_t)stream);
+  if (!X || !W || !row_max || !log_sum || (M > 0 && (!ids || !dlogp))) return ELMO_EINVAL;
+  if (!rows16(X, type, ldx) || !rows16(W, type, ldw)) return ELMO_EINVAL;
+  for (const void* p : {(const void*)ids, (const void*)dlogp, (const void*)row_max, (const void*)log_sum, (const void*)dlse})
+    if (!aligned_to(p, 4)) return ELMO_EINVAL;
+  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
+  const elmo::LinearGradLayout s = elmo::linear_grad_layout(N, V, D, M, chunk, dX != nullptr, dW != nullptr);
+  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  elmo::LinearGradCall c{};
+  c.X = X; c.W = W; c.type = type; c.N = N; c.V = V; c.D = D; c.ldx = ldx; c.ldw = ldw; c.ids = ids; c.M = M;
+  c.row_max = row_max; c.log_sum = log_sum; c.dlogp = dlogp; c.dlse = dlse;
+  c.dX = dX; c.dx_type = dx_type; c.lddx = lddx; c.dW = dW; c.dw_type = dw_type; c.lddw = lddw; c.accumulate = accumulate;
+  return elmo::run_linear_logprobs_grad(c, s, workspace, (hipStream_t)stream);
 }
 
 }  // extern "C"

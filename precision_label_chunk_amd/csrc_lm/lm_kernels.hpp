@@ -35,4 +35,26 @@ WgradLayout wgrad_layout(int64_t T, int O, int D);
 int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O, int D,
                     float* dW, int accumulate, const WgradLayout& s, void* workspace, hipStream_t st);
 
+// log probabilities of given labels from features and weights, and the gradients of both
+struct LinearLayout { int64_t parts; size_t part, given, total; };
+LinearLayout linear_layout(int64_t N, int64_t V, int M);
+int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
+                        const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, const LinearLayout& s,
+                        void* workspace, hipStream_t st);
+struct LinearGradLayout {
+  int64_t piece, x_per, w_per;                             // labels per piece; labels / tokens per run
+  int x_slots, w_slots;                                    // runs
+  size_t most, inv, coef, up, G, xpart, wpart, total;
+};
+struct LinearGradCall {
+  const void *X, *W; int type; int64_t N, V; int D; int64_t ldx, ldw;
+  const int32_t* ids; int M;
+  const float *row_max, *log_sum, *dlogp, *dlse;
+  void* dX; int dx_type; int64_t lddx;
+  void* dW; int dw_type; int64_t lddw; int accumulate;
+};
+LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw);
+int run_zero_rows(void* out, int type, int64_t rows, int D, int64_t ld, hipStream_t st);
+int run_linear_logprobs_grad(const LinearGradCall& c, const LinearGradLayout& s, void* workspace, hipStream_t st);
+
 }  // namespace elmo

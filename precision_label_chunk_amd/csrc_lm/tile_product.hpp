@@ -1,0 +1,247 @@
+// Matrix products in tiles, C[m, n] = sum_k A[m, k] B[n, k], for kernels that do something of their
+// own with the sums of a tile (softmax statistics, a gradient, scales) instead of storing them.
+//
+// A block of 2 x WN waves computes 256 x 64 WN tiles, a wave 128 x 64 of it in 4 x 2 sums of 32 x 32
+// (128 registers). The depth goes in stages of 64 bytes of K per row (32 elements of 16 bits, 64 of 8),
+// copied from memory to LDS without passing registers, NBUF - 1 stages ahead, one barrier a stage. The
+// stages of a block's tiles follow each other without a break: the first stages of the next tile are on
+// their way while the sums of the last one are used.
+//
+// An operand is K-contiguous (rows of m or n, its elements of a row along K) or K-major (rows of k, 16-bit
+// elements along m or n, read from LDS by the transposing reads). Both are 16 KiB of LDS per 256 rows
+// and stage. The copies write 16 bytes a lane in lane order, so what a lane fetches is permuted instead:
+//   K-contiguous  row r's four 16-byte pieces at p = c ^ f(r), f(r) = (r >> 1 & 3) ^ (r >> 3 & 1): the 8
+//                 rows that a read serves at once touch all 32 banks once, any 16 rows all 64 once
+//   K-major       row k's 16-byte piece c at c ^ 2 X(k & 3), X = 0, 2, 5, 7: the same for the 4 rows x
+//                 32 (64) bytes of a transposing read
+#pragma once
+#include "elem_types.hpp"
+
+namespace elmo {
+
+typedef __attribute__((address_space(3))) char lds_char_t;
+
+// The matrix instruction of an element type: 32 x 32 sums over 32 bytes of K per row, 16 bytes a lane
+// (row lane % 32, the K half lane / 32).
+struct MulBF16 {
+  typedef s16x8_t frag;
+  typedef f32x16_t acc;
+  typedef float sum;
+  static constexpr int BYTES = 2;
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) { return mfma_bf16(a, b, c); }
+};
+struct MulF16 {
+  typedef s16x8_t frag;
+  typedef f32x16_t acc;
+  typedef float sum;
+  static constexpr int BYTES = 2;
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) {
+    typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_v;
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_v, a), __builtin_bit_cast(f16x8_v, b), c, 0, 0, 0);
+  }
+};
+typedef __attribute__((ext_vector_type(16))) int i32x16_t;
+struct MulI8 {
+  typedef i32x4_t frag;
+  typedef i32x16_t acc;
+  typedef int sum;
+  static constexpr int BYTES = 1;
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+  }
+};
+
+// One operand of a tile: where its first stage starts, and how far it reaches. K-contiguous: `rows` valid
+// rows (of m or n) at pitch `ld` bytes. K-major: `rows` valid rows of k, of which `cols` bytes belong to
+// the tile and the matrix. What lies outside reads as zero, or as other elements of the matrix where it
+// reaches only sums that nobody uses.
+struct Operand { const char* at; int64_t ld; int64_t rows; int cols; };
+struct TileUnit { Operand a, b; int stages; };
+
+constexpr int TILE_M = 256, STAGE_K = 64;                  // rows of A per tile; bytes of K per stage
+
+template <int WN> constexpr int tile_n() { return 64 * WN; }
+template <int WN, int NBUF> constexpr int tile_lds() { return NBUF * (TILE_M + 64 * WN) * STAGE_K; }
+
+__device__ __forceinline__ int kc_swizzle(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
+__device__ __forceinline__ int km_swizzle(int k) { const int r = k & 3; return 2 * (2 * r | (r >> 1)); }
+
+// every wave of the block has all but its last N vector memory operations and all its LDS reads behind it
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// One operand's copies: ROWS of m or n per stage, THREADS threads.
+template <bool KM, int ROWS, int THREADS, int BYTES>
+struct StageCopy {
+  static constexpr int COPIES = ROWS * 4 / THREADS;        // 16-byte pieces per thread and stage
+  static constexpr int KROWS = STAGE_K / BYTES;            // rows of k per stage
+  static constexpr int PER_ROW = ROWS * BYTES / 16;        // K-major: pieces per row of k
+  int off;                                                 // byte offset of the thread's first piece
+  int step;                                                // and of the next one from it
+  Operand o;
+  __device__ __forceinline__ void start(const Operand& op, int tid) {
+    o = op;
+    const int ld = (int)op.ld;
+    if constexpr (KM) {
+      const int k = tid / PER_ROW, c = (tid % PER_ROW) ^ km_swizzle(k);
+      off = k * ld + c * 16;
+      step = THREADS / PER_ROW * ld;
+    } else {
+      const int r = tid / 4, c = (tid % 4) ^ kc_swizzle(r);
+      off = r * ld + c * 16;
+      step = THREADS / 4 * ld;
+    }
+  }
+  // the copies of stage s into the LDS bytes at `to` (a wave's part of each starts at wave * 1024)
+  __device__ __forceinline__ void copy(int s, char* to, int wave, bool live) const {
+    const char* base = o.at;
+    int64_t bytes;
+    if constexpr (KM) {
+      const int64_t left = o.rows - (int64_t)s * KROWS;
+      base += (int64_t)s * KROWS * o.ld;
+      bytes = left > 0 ? ((left < KROWS ? left : KROWS) - 1) * o.ld + o.cols : 0;
+    } else {
+      base += (int64_t)s * STAGE_K;
+      bytes = o.rows > 0 ? ((o.rows < ROWS ? o.rows : ROWS) - 1) * o.ld + STAGE_K : 0;
+    }
+    const auto buf = buffer_rsrc(base, live ? (int)bytes : 0);
+#pragma unroll
+    for (int i = 0; i < COPIES; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_char_t*)(to + i * THREADS * 16 + wave * 1024), 16, off + i * step, 0, 0, 0);
+  }
+};
+
+// A wave's fragments of a stage: F of 32 rows each from row `first` on.
+template <bool KM, int ROWS, int F, class Mul>
+struct StageRead {
+  int at[KM ? F : 1];
+  __device__ __forceinline__ void start(int first, int lane) {
+    if constexpr (KM) {
+      // lane's place in a transposing read: group g of 16 lanes takes columns 16 (g & 1) .. + 16 and k rows
+      // 8 (g >> 1) .. + 4 (then + 4 .. + 8); lane j of it supplies row j / 4, columns 4 (j % 4) .. + 4
+      const int g = lane >> 4, j = lane & 15, k = 8 * (g >> 1) + (j >> 2);
+      const int col = first + 16 * (g & 1) + 4 * (j & 3);
+#pragma unroll
+      for (int f = 0; f < F; ++f) at[f] = k * (ROWS * 2) + (((col + 32 * f) >> 3) ^ km_swizzle(k)) * 16 + (col & 7) * 2;
+    } else {
+      const int r = first + (lane & 31);
+      at[0] = r * STAGE_K + ((lane >> 5) ^ kc_swizzle(r)) * 16;
+    }
+  }
+  // half h of the stage
+  __device__ __forceinline__ void read(const char* from, int h, typename Mul::frag* out) const {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      if constexpr (KM) {
+        const char* p = from + at[f] + h * 16 * ROWS * 2;
+        out[f] = join(lds_read_tr16((const uint16_t*)p), lds_read_tr16((const uint16_t*)(p + 4 * ROWS * 2)));
+      } else {
+        out[f] = *(const typename Mul::frag*)(from + (at[0] ^ (32 * h)) + f * 32 * STAGE_K);
+      }
+    }
+  }
+};
+
+// The products of the units first, first + step, .. below `end`; job.unit(u) describes a unit,
+// job.finish(u, acc, wm, wn, lane) uses its sums: acc[i][j][r] of wave (wm, wn) is row
+// m = 128 wm + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 and column n = 64 wn + 32 j + lane % 32 of the tile.
+// Every unit has at least one stage. All threads of the block call it.
+template <class Mul, bool AKM, bool BKM, int WN, int NBUF, class Job>
+__device__ __forceinline__ void tile_stream(const Job& job, int first, int step, int end, char* lds) {
+  constexpr int THREADS = 128 * WN, A_BYTES = TILE_M * STAGE_K, BUF = A_BYTES + 64 * WN * STAGE_K;
+  typedef typename Mul::frag frag;
+  const int tid = (int)threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  if (first >= end) return;
+
+  StageCopy<AKM, TILE_M, THREADS, Mul::BYTES> ca;
+  StageCopy<BKM, 64 * WN, THREADS, Mul::BYTES> cb;
+  constexpr int COPIES = decltype(ca)::COPIES + decltype(cb)::COPIES;
+  int lu = first, ls = 0, lstages;                         // the unit and stage to be copied next
+  int fill = 0;                                            // and its buffer
+  {
+    const TileUnit t = job.unit(lu);
+    ca.start(t.a, tid);
+    cb.start(t.b, tid);
+    lstages = t.stages;
+  }
+  auto fetch = [&]() __attribute__((always_inline)) {
+    char* to = lds + fill * BUF;
+    ca.copy(ls, to, wave, lu < end);                       // (past the last unit: copies of nothing, for the count)
+    cb.copy(ls, to + A_BYTES, wave, lu < end);
+    fill = fill + 1 == NBUF ? 0 : fill + 1;
+    if (++ls == lstages) {
+      ls = 0;
+      lu += step;
+      if (lu < end) {
+        const TileUnit t = job.unit(lu);
+        ca.start(t.a, tid);
+        cb.start(t.b, tid);
+        lstages = t.stages;
+      }
+    }
+  };
+
+  StageRead<AKM, TILE_M, 4, Mul> ra;
+  StageRead<BKM, 64 * WN, 2, Mul> rb;
+  ra.start(128 * wm, lane);
+  rb.start(64 * wn, lane);
+  frag fa[2][4], fb[2][2];
+  typename Mul::acc acc[4][2];
+  auto products = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = Mul::mul(fa[h][i], fb[h][j], acc[i][j]);
+  };
+  auto frags = [&](const char* from, int h) __attribute__((always_inline)) {
+    rb.read(from + A_BYTES, h, fb[h]);
+    ra.read(from, h, fa[h]);
+  };
+
+#pragma unroll
+  for (int s = 0; s < NBUF - 1; ++s) fetch();
+  int use = 0;
+  // stage: its copies have landed (this wave's by the count, the others' by the barrier), and every wave has
+  // read the buffer that the next copies go to; the last half's products run while its fragments are read
+  auto stage = [&](bool go_on) __attribute__((always_inline)) {
+    wait_copies<COPIES*(NBUF - 2)>();
+    const char* from = lds + use * BUF;
+    use = use + 1 == NBUF ? 0 : use + 1;
+    frags(from, 0);
+    fetch();
+    if (go_on) products(1);
+    frags(from, 1);
+    products(0);
+  };
+  for (int u = first; u < end; u += step) {
+    const int stages = job.unit(u).stages;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+    stage(false);
+    for (int s = 1; s < stages; ++s) stage(true);
+    products(1);
+    job.finish(u, acc, wm, wn, lane);
+  }
+  wait_copies<0>();                                        // no copy is on its way when the block's LDS is given back
+}
+
+// Blocks go to the 8 XCDs in turn; each XCD gets a run of the units, which its blocks take in turn, so
+// that units next to each other share an L2. (first, step, end) of this block's.
+struct UnitRange { int first, step, end; };
+__device__ __forceinline__ UnitRange xcd_units(int units) {
+  const int n = (int)gridDim.x, b = (int)blockIdx.x;
+  if (n < 8) return {b, n, units};
+  const int xcd = b & 7, per = units / 8, more = units % 8;
+  const int start = xcd * per + (xcd < more ? xcd : more), len = per + (xcd < more);
+  return {start + (b >> 3), (n - xcd + 7) / 8, start + len};
+}
+
+}  // namespace elmo
