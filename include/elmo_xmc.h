@@ -366,6 +366,43 @@ int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_
                                   size_t workspace_bytes, void* stream);
 
 /*
+ * Products of rows held in 8-bit integers, with a scale for each row of both operands (each token, each
+ * output channel): Y[n, v] = x_scales[n] w_scales[v] sum_k X[n, k] W[v, k]. The sum is exact; it is rounded to
+ * binary32, multiplied by x_scales[n], then by w_scales[v], and rounded to `ytype`.
+ *   X [N, D], W [L, D] int8 (any of -128 .. 127), row-major without gaps, 16-byte aligned; D % 64 == 0,
+ *   64 <= D <= ELMO_MAX_I8_D. x_scales [N], w_scales [L] FP32. Y [N, L] of element type `ytype`, row n at Y + n ldy,
+ *   any pitch and element alignment. 1 <= L < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). A NaN scale stays
+ *   in its row or column.
+ * elmo_i8_quantize makes such rows from x [N, D] (element type `type`, 16-byte aligned rows at pitch ldx):
+ *   scale = max_k |x[k]| / 127, code = 127 x / max|x| to the nearest whole number, halves to the even one, of the
+ *   exact quotient. A zero row has scale 0 and codes 0; a row with a NaN or an infinity has scale NaN and
+ *   codes 0.
+ */
+#define ELMO_MAX_I8_D 65536
+int elmo_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, void* stream);
+size_t elmo_i8_matmul_workspace_bytes(int64_t N, int64_t L, int D);
+int elmo_i8_matmul(const int8_t* X, const float* x_scales, const int8_t* W, const float* w_scales, int64_t N, int64_t L,
+                   int D, void* Y, int ytype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Dropout from the generator of the stochastic rounding, with a mask that is never stored:
+ *   y[t, d] = residual[t, d] + (kept ? x[t, d] 65536 / (65536 - limit) : 0), limit = floor(65536 p + 1/2);
+ * element i = first + t D + d is kept if its 16 random bits are >= limit: Philox4x32-10 with key = `seed` and
+ * counter (i >> 3, step), half (i & 1) of output word (i >> 1) & 3, as the weights' update draws (a call with
+ * elmo_xmc_step's own seed and step shares its draws). In binary32, rounded once; dropped elements are 0
+ * whatever they hold. The gradient with respect to x is the same call on dy without a residual.
+ *   x, y, residual (nullable)  T rows of D elements of `type`, any pitch and element alignment. y = x or
+ *            y = residual with equal pitches is allowed.
+ *   p        0 <= p <= 1 (1: everything is dropped).
+ *   step_at  device address of a number added to `step` when the work runs (NULL: none; 8-byte aligned): a
+ *            recorded graph that counts it up draws a new mask at each replay.
+ *   first    the index of x[0, 0]: parts of a batch draw what the whole would.
+ * 0 <= T < 2^31 (0: nothing is done), 1 <= D < 2^31. No workspace.
+ */
+int elmo_dropout(const void* x, int type, int64_t T, int64_t D, int64_t ldx, const void* residual, int64_t ldr, double p,
+                 uint64_t seed, uint64_t step, const uint64_t* step_at, uint64_t first, void* y, int64_t ldy, void* stream);
+
+/*
  * Test hook: the device codec, stochastic rounding and RNG applied elementwise to n elements.
  *   op 0  BF16 RNE encode:      in0 float[n]            -> out uint16[n]
  *   op 1  E4M3 RNE-sat encode:  in0 float[n]            -> out uint8[n]

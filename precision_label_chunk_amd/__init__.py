@@ -106,6 +106,11 @@ def lib():
         L.elmo_linear_logprobs_backward.argtypes = [P, P, i32, i64, i64, i32, i64, i64, P, i32, P, P, P, P, P, i32, i64, P, i32,
                                                     i64, i32, i64, P, sz, P]
         L.elmo_linear_logprobs_backward.restype = i32
+        L.elmo_i8_quantize.argtypes = [P, i32, i64, i32, i64, P, P, P]; L.elmo_i8_quantize.restype = i32
+        L.elmo_i8_matmul_workspace_bytes.argtypes = [i64, i64, i32]; L.elmo_i8_matmul_workspace_bytes.restype = sz
+        L.elmo_i8_matmul.argtypes = [P, P, P, P, i64, i64, i32, P, i32, i64, P, sz, P]; L.elmo_i8_matmul.restype = i32
+        L.elmo_dropout.argtypes = [P, i32, i64, i64, i64, P, i64, ctypes.c_double, u64, u64, P, u64, P, i64, P]
+        L.elmo_dropout.restype = i32
         _lib = L
     return _lib
 
@@ -606,6 +611,77 @@ def linear_logprobs_backward(X, W, ids, stats: LinearLogProbs, dlogp, dlse=None,
         stats.log_sum.data_ptr(), _at(dlogp) if M else None, _at(dlse), _at(dx), xt, lddx, _at(dw), wt, lddw,
         int(accumulate), chunk, workspace.data_ptr(), workspace.numel(), _stream_of(dev)))
     return dx, dw
+
+
+def i8_quantize(x):
+    """(codes int8 [N, D], scales float32 [N]) of the rows of x [N, D] (float32, bfloat16 or float16, D % 64
+    == 0): scale = max|x| / 127, codes to the nearest. See elmo_i8_quantize in elmo_xmc.h."""
+    e = _etype(x)
+    N, D, ld = _rows("x", x)
+    codes = x.new_empty((N, D), dtype=torch.int8)
+    scales = x.new_empty((N,), dtype=torch.float32)
+    _chk("elmo_i8_quantize", lib().elmo_i8_quantize(x.data_ptr(), e, N, D, ld, codes.data_ptr(), scales.data_ptr(),
+                                                    _stream_of(x.device)))
+    return codes, scales
+
+
+def i8_matmul(X, x_scales, W, w_scales, out_dtype=torch.bfloat16, out=None, workspace=None):
+    """Y [N, L] = x_scales[n] w_scales[v] X W^T for int8 rows X [N, D] and W [L, D] with a scale each
+    (float32; D % 64 == 0), any number of rows. See elmo_i8_matmul in elmo_xmc.h."""
+    dev = X.device
+    for name, t in (("X", X), ("W", W)):
+        if t.dtype != torch.int8 or t.dim() != 2 or not t.is_cuda or not t.is_contiguous() or t.device != dev:
+            raise ValueError(f"{name} must be a contiguous 2-D int8 CUDA tensor on X's device")
+    (N, D), (L, d) = X.shape, W.shape
+    if d != D:
+        raise ValueError(f"X has {D} features, W {d}")
+    _like("x_scales", x_scales, (N,), torch.float32, dev)
+    _like("w_scales", w_scales, (L,), torch.float32, dev)
+    if out is None:
+        out = X.new_empty((N, L), dtype=out_dtype)
+    elif tuple(out.shape) != (N, L) or out.device != dev:
+        raise ValueError("out must be [N, L] on X's device")
+    e, ldy = _etype(out), _rows("out", out)[2]
+    if L == 0:
+        return out
+    workspace = _scratch(workspace, lib().elmo_i8_matmul_workspace_bytes(N, L, D) if N else 0, X)
+    _chk("elmo_i8_matmul", lib().elmo_i8_matmul(X.data_ptr(), x_scales.data_ptr(), W.data_ptr(), w_scales.data_ptr(), N, L, D,
+                                                out.data_ptr(), e, ldy, workspace.data_ptr(), workspace.numel(),
+                                                _stream_of(dev)))
+    return out
+
+
+def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
+    """y = residual + (kept ? x / (1 - p) : 0) for x [T, D] or [D] (float32, bfloat16 or float16), elements kept by
+    the counter-based generator keyed by (seed, step) and their index first + t D + d; the mask is not stored. `step` is
+    a whole number, or a CUDA int64 tensor of one element that is read when the work runs (for recorded graphs). out = x
+    or out = residual writes over it. See elmo_dropout in elmo_xmc.h."""
+    e = _etype(x)
+    if out is None:
+        out = x.new_empty(x.shape)
+    for name, t in (("out", out), ("residual", residual)):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device):
+            raise ValueError(f"{name} must have x's shape, type and device")
+    a, y, r = ((t if t is None or t.dim() != 1 else t.unsqueeze(0)) for t in (x, out, residual))
+    T, D, ld = _rows("x", a)
+    at = None
+    if isinstance(step, torch.Tensor):
+        if step.dtype != torch.int64 or step.numel() != 1 or step.device != x.device:
+            raise ValueError(f"a step tensor must hold one int64 on {x.device}")
+        step, at = 0, step.data_ptr()
+    if D == 0:
+        return out
+    low = (1 << 64) - 1
+    _chk("elmo_dropout", lib().elmo_dropout(
+        x.data_ptr(), e, T, D, ld, _at(residual), _rows("residual", r)[2] if r is not None else 0, p, seed & low, step & low,
+        at, first & low, out.data_ptr(), _rows("out", y)[2], _stream_of(x.device)))
+    return out
+
+
+def dropout_backward(dy, p, seed, step=0, first=0, out=None):
+    """The gradient with respect to x of dropout(x, p, seed, step, .., first) from dy: the mask drawn again. (The
+    residual's gradient is dy itself.) out = dy writes over it."""
+    return dropout(dy, p, seed, step, first=first, out=out)
 
 
 def numerics_probe(op, in0=None, in1=None, n=None, seed=0, step=0, idx0=0):

@@ -1,0 +1,375 @@
+// Matrix products in 8-bit integers with a scale for each row of both operands, and the quantisation that
+// makes such rows.
+//
+// y[n, v] = sx[n] sw[v] sum_k x[n, k] w[v, k]: the sum is exact (D <= 65536 products of at most 2^14 stay
+// within 2^30), so its split along K and its order change nothing; what rounds is its conversion, the two
+// scales and the result.
+#include "lm_kernels.hpp"
+#include "tile_product.hpp"
+
+namespace elmo {
+
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---- quantisation ----------------------------------------------------------------------------------
+// q = the whole number nearest to 127 x / top (halves to even), scale = top / 127. The quotient comes from
+// one product with 127 / top; within 2^-13 of a half, where its roundings (at most 127 x 1.5 x 2^-23 < 2^-15)
+// could decide, 254 |x| is compared with (2 k + 1) top, both exact in binary64.
+__device__ __forceinline__ int quantise(float x, float inv, float top) {
+  const float r = x * inv, k = __builtin_rintf(r);
+  const float off = __builtin_fabsf(r - k);
+  if (__builtin_expect(off > 0.4998f, 0)) {
+    const float lo = __builtin_floorf(__builtin_fabsf(r));
+    // |r| lies near lo + 1/2 (or, where floor took the wrong side, near lo - 1/2 or lo + 3/2: not within 2^-13)
+    const double a = 254.0 * (double)__builtin_fabsf(x), b = (2.0 * (double)lo + 1.0) * (double)top;
+    int q = (int)lo;
+    if (a > b || (a == b && (q & 1))) ++q;
+    return x < 0.0f ? -q : q;
+  }
+  return (int)k;
+}
+
+// A row per group of G threads (a wave, or the block); a thread's first VECS vectors of 8 elements stay in
+// registers between the maximum and the codes, the rest is read again.
+template <typename E>
+__device__ __forceinline__ void load8(const typename E::raw* p, float* f) {
+#pragma unroll
+  for (int h = 0; h < 8 / E::VEC; ++h) E::widen(*(const i32x4_t*)(p + h * E::VEC), f + h * E::VEC);
+}
+template <typename E, int G>
+__global__ __launch_bounds__(256) void k_i8_quantize(const typename E::raw* x, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales) {
+  constexpr int VECS = 4;
+  __shared__ float tops[4];
+  const int lane = (int)threadIdx.x % G;
+  const int64_t n = G == 64 ? blockIdx.x * (int64_t)4 + threadIdx.x / 64 : (int64_t)blockIdx.x;
+  if (n >= N) return;                                      // (a whole wave, or the whole block)
+  const typename E::raw* row = x + n * ldx;
+  float f[VECS][8];
+  float top = 0.0f;
+  bool bad = false;
+  auto see = [&](const float* v) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = __builtin_fabsf(v[i]);
+      bad |= !(a < __builtin_inff());
+      top = fmaxf(top, a);
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    const int d = (v * G + lane) * 8;
+    if (d < D) {
+      load8<E>(row + d, f[v]);
+      see(f[v]);
+    }
+  }
+  for (int d = (VECS * G + lane) * 8; d < D; d += G * 8) {
+    float g[8];
+    load8<E>(row + d, g);
+    see(g);
+  }
+  if (bad) top = __builtin_inff();
+#pragma unroll
+  for (int k = 32; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor(top, k));
+  if constexpr (G == 256) {
+    if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  }
+  // a row with a NaN or an infinity: no codes, its scale NaN. 127 / top may leave binary32's normal range for
+  // rows under 2^-100: those are scaled up first, by a power of two
+  const bool none = !(top < __builtin_inff());
+  const bool tiny = top < 7.8886090522101181e-31f;
+  const float up = tiny ? 1.2676506002282294e30f : 1.0f;
+  const float t = top * up, inv = none || top == 0.0f ? 0.0f : 127.0f / t;
+  auto put = [&](int d, const float* v) __attribute__((always_inline)) {
+    int w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int q = none ? 0 : quantise(v[i] * up, inv, t);
+      w[i / 4] |= (q & 255) << 8 * (i % 4);
+    }
+    *(i32x2_t*)(codes + n * D + d) = i32x2_t{w[0], w[1]};
+  };
+#pragma unroll
+  for (int v = 0; v < VECS; ++v) {
+    const int d = (v * G + lane) * 8;
+    if (d < D) put(d, f[v]);
+  }
+  for (int d = (VECS * G + lane) * 8; d < D; d += G * 8) {
+    float g[8];
+    load8<E>(row + d, g);
+    put(d, g);
+  }
+  if (lane == 0) scales[n] = none ? __builtin_nanf("") : top / 127.0f;
+}
+
+template <typename E>
+static void quantize_as(const void* x, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st) {
+  const typename E::raw* p = (const typename E::raw*)x;
+  // a wave holds 2048 features of a row in registers, a block 8192
+  if (D <= 2048)
+    hipLaunchKernelGGL((k_i8_quantize<E, 64>), dim3((unsigned)ceil_div(N, 4)), dim3(256), 0, st, p, N, D, ldx, codes, scales);
+  else
+    hipLaunchKernelGGL((k_i8_quantize<E, 256>), dim3((unsigned)N), dim3(256), 0, st, p, N, D, ldx, codes, scales);
+}
+
+int run_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st) {
+  if (type == T_F32_) quantize_as<ElemF32>(x, N, D, ldx, codes, scales, st);
+  else if (type == T_BF16_) quantize_as<ElemBF16>(x, N, D, ldx, codes, scales, st);
+  else quantize_as<ElemF16>(x, N, D, ldx, codes, scales, st);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+// ---- products --------------------------------------------------------------------------------------
+struct I8Args {
+  const char* X; const char* W;
+  const float* sx; const float* sw;
+  void* Y; int64_t ldy;                                    // elements
+  int64_t N, L; int D;
+  int row_tiles, label_tiles, slots, per;                  // runs of K: `per` stages each
+  int* part;                                               // [slots][N][L4]: whole sums of the runs
+  int64_t L4;
+};
+
+typedef i32x4_t __attribute__((aligned(4))) i32x4_a4_t;
+typedef i32x4_t __attribute__((aligned(2))) i32x4_a2_t;
+typedef i32x2_t __attribute__((aligned(2))) i32x2_a2_t;
+
+// four results of a row, labels v .. v + 3
+template <typename E>
+__device__ __forceinline__ void store_results(typename E::raw* p, int64_t left, const float* y) {
+  if (left >= 4) {
+    if constexpr (E::VEC == 4) {
+      *(i32x4_a4_t*)p = E::narrow(y);
+    } else {
+      const float z[8] = {y[0], y[1], y[2], y[3], 0, 0, 0, 0};
+      const i32x4_t w = E::narrow(z);
+      *(i32x2_a2_t*)p = i32x2_t{w[0], w[1]};
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < left) E::store(p + i, y[i]);
+  }
+}
+// scales of labels v .. v + 3, zero past the last
+__device__ __forceinline__ f32x4_t scales4(const float* sw, int64_t v, int64_t L) {
+  f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (v + i < L) s[i] = sw[v + i];
+  return s;
+}
+
+constexpr int I8_WN = 4, I8_NBUF = 4, I8_THREADS = 128 * I8_WN, I8_TN = 64 * I8_WN, I8_GROUP = 8;
+
+template <typename E, bool PARTS>
+struct I8Job : I8Args {
+  __device__ __forceinline__ void place(int u, int& lt, int& nt, int& slot) const {
+    const int tiles = row_tiles * label_tiles;
+    slot = u / tiles;
+    u %= tiles;
+    const int group = I8_GROUP * row_tiles, g = u / group, r = u % group;
+    const int wide = label_tiles - g * I8_GROUP < I8_GROUP ? label_tiles - g * I8_GROUP : I8_GROUP;
+    nt = r / wide;
+    lt = g * I8_GROUP + r % wide;
+  }
+  __device__ __forceinline__ TileUnit unit(int u) const {
+    int lt, nt, slot;
+    place(u, lt, nt, slot);
+    const int64_t l = (int64_t)lt * TILE_M, n = (int64_t)nt * I8_TN;
+    const int s0 = slot * per, all = D / STAGE_K, len = all - s0 < per ? all - s0 : per;
+    return {{W + l * D + s0 * STAGE_K, D, L - l, 0}, {X + n * D + s0 * STAGE_K, D, N - n, 0}, len};
+  }
+  __device__ __forceinline__ void finish(int u, i32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+    int lt, nt, slot;
+    place(u, lt, nt, slot);
+    const int64_t v0 = (int64_t)lt * TILE_M + 128 * wm + 4 * (lane >> 5), n0 = (int64_t)nt * I8_TN + 64 * wn + (lane & 31);
+    float s[2];
+    if constexpr (!PARTS) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j] = n0 + 32 * j < N ? sx[n0 + 32 * j] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t v = v0 + 32 * i + 8 * q;
+        f32x4_t t;
+        if constexpr (!PARTS) t = scales4(sw, v, L);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int64_t n = n0 + 32 * j;
+          if (n < N && v < L) {
+            if constexpr (PARTS) {
+              *(i32x4_t*)(part + ((int64_t)slot * N + n) * L4 + v) =
+                  i32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+            } else {
+              float y[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) y[k] = (float)acc[i][j][4 * q + k] * s[j] * t[k];
+              store_results<E>((typename E::raw*)Y + n * ldy + v, L - v, y);
+            }
+          }
+        }
+      }
+  }
+};
+
+template <typename E, bool PARTS>
+__global__ __launch_bounds__(I8_THREADS, 2) void k_i8_tiles(I8Args a) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<I8_WN, I8_NBUF>()];
+  I8Job<E, PARTS> job;
+  (I8Args&)job = a;
+  const UnitRange r = xcd_units(a.label_tiles * a.row_tiles * a.slots);
+  tile_stream<MulI8, false, false, I8_WN, I8_NBUF>(job, r.first, r.step, r.end, lds);
+}
+
+// the runs' sums joined, scaled and rounded
+template <typename E>
+__global__ __launch_bounds__(256) void k_i8_join(I8Args a) {
+  const int64_t l4 = a.L4 / 4, stride = a.N * a.L4;
+  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < a.N * l4; i += (int64_t)gridDim.x * 256) {
+    const int64_t n = i / l4, v = i % l4 * 4;
+    i32x4_t s = *(const i32x4_t*)(a.part + n * a.L4 + v);
+    for (int k = 1; k < a.slots; ++k) s += *(const i32x4_t*)(a.part + k * stride + n * a.L4 + v);
+    const f32x4_t t = scales4(a.sw, v, a.L);
+    const float f = a.sx[n];
+    float y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y[k] = (float)s[k] * f * t[k];
+    store_results<E>((typename E::raw*)a.Y + n * a.ldy + v, a.L - v, y);
+  }
+}
+
+// Up to 32 rows: weights straight from memory to the matrix cores. A wave takes 16 labels x all rows, 64 bytes
+// of K per product; KS waves of a block share a tile's K where there are few tiles.
+__device__ __forceinline__ i32x4_t mul_i8_16(i32x4_t a, i32x4_t b, i32x4_t c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+}
+template <typename E, int NT, int KS>
+__global__ __launch_bounds__(KS > 4 ? 64 * KS : 256) void k_i8_rows(I8Args a) {
+  constexpr int WAVES = KS > 4 ? KS : 4, TILES = WAVES / KS;
+  __shared__ i32x4_t sums[KS > 1 ? WAVES : 1][NT][64];
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int64_t tile = (int64_t)blockIdx.x * TILES + wave / KS;
+  const int64_t v0 = tile * 16;
+  const int ks = wave % KS, steps = a.D / 64, s0 = (int)((int64_t)steps * ks / KS), s1 = (int)((int64_t)steps * (ks + 1) / KS);
+  // rows past the last read the last one again; their results are not stored
+  const int64_t row = v0 + (lane & 15) < a.L ? v0 + (lane & 15) : a.L - 1;
+  const char* w = a.W + row * a.D + 16 * (lane >> 4);
+  const char* x[NT];
+  i32x4_t acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t n = 16 * j + (lane & 15);
+    x[j] = a.X + (n < a.N ? n : a.N - 1) * a.D + 16 * (lane >> 4);
+    acc[j] = i32x4_t{0, 0, 0, 0};
+  }
+  constexpr int AHEAD = 8 / NT;                            // products whose operands are on their way together
+  auto steps_of = [&](int s, auto count) __attribute__((always_inline)) {
+    constexpr int C = count;
+    i32x4_t fw[C], fx[NT][C];
+#pragma unroll
+    for (int k = 0; k < C; ++k) {
+      fw[k] = *(const i32x4_t*)(w + (int64_t)(s + k) * 64);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fx[j][k] = *(const i32x4_t*)(x[j] + (int64_t)(s + k) * 64);
+    }
+#pragma unroll
+    for (int k = 0; k < C; ++k)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = mul_i8_16(fw[k], fx[j][k], acc[j]);
+  };
+  int s = s0;
+  for (; s + AHEAD <= s1; s += AHEAD) steps_of(s, std::integral_constant<int, AHEAD>{});
+  for (; s < s1; ++s) steps_of(s, std::integral_constant<int, 1>{});
+  if constexpr (KS > 1) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) sums[wave][j][lane] = acc[j];
+    __syncthreads();
+    if (ks != 0) return;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll 5
+      for (int k = 1; k < KS; ++k) acc[j] += sums[wave + k][j][lane];
+  }
+  const int64_t v = v0 + 4 * (lane >> 4);
+  if (v >= a.L) return;
+  const f32x4_t t = scales4(a.sw, v, a.L);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t n = 16 * j + (lane & 15);
+    if (n < a.N) {
+      const float f = a.sx[n];
+      float y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = (float)acc[j][k] * f * t[k];
+      store_results<E>((typename E::raw*)a.Y + n * a.ldy + v, a.L - v, y);
+    }
+  }
+}
+
+constexpr int I8_ROWS = 32;                                // rows that the streaming kernel takes
+
+I8Layout i8_layout(int64_t N, int64_t L, int D) {
+  I8Layout s{};
+  s.slots = 1;
+  s.per = D / STAGE_K;
+  s.L4 = ceil_div(L, 4) * 4;
+  if (N > I8_ROWS) {
+    // fewer tiles than compute units: runs of K, as long as one keeps 8 stages
+    const int64_t tiles = ceil_div(L, TILE_M) * ceil_div(N, I8_TN), cus = device_cus(), all = D / STAGE_K;
+    int64_t k = cus / tiles;
+    if (k > all / 8) k = all / 8;
+    if (k > 1) {
+      s.per = (int)ceil_div(all, k);
+      s.slots = (int)ceil_div(all, s.per);
+    }
+  }
+  s.total = s.slots > 1 ? (size_t)s.slots * N * s.L4 * 4 : 256;
+  return s;
+}
+
+template <typename E>
+static int matmul_as(I8Args& a, hipStream_t st) {
+  if (a.N <= I8_ROWS) {
+    const int64_t tiles = ceil_div(a.L, 16), cus = device_cus();
+    // waves that share a tile: until there are 8 for every compute unit
+    const int ks = tiles >= 8 * cus ? 1 : tiles >= 2 * cus ? 4 : 16;
+    const unsigned grid = (unsigned)(ks == 1 ? ceil_div(tiles, 4) : tiles);
+#define ELMO_I8_ROWS(NT, KS) hipLaunchKernelGGL((k_i8_rows<E, NT, KS>), dim3(grid), dim3(KS > 4 ? 64 * KS : 256), 0, st, a)
+    if (a.N <= 16) {
+      if (ks == 1) ELMO_I8_ROWS(1, 1); else if (ks == 4) ELMO_I8_ROWS(1, 4); else ELMO_I8_ROWS(1, 16);
+    } else {
+      if (ks == 1) ELMO_I8_ROWS(2, 1); else if (ks == 4) ELMO_I8_ROWS(2, 4); else ELMO_I8_ROWS(2, 16);
+    }
+#undef ELMO_I8_ROWS
+    return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+  }
+  const int64_t units = (int64_t)a.row_tiles * a.label_tiles * a.slots, cus = device_cus();
+  const dim3 grid((unsigned)(units < cus ? units : cus));
+  if (a.slots == 1) {
+    hipLaunchKernelGGL((k_i8_tiles<E, false>), grid, dim3(I8_THREADS), 0, st, a);
+    return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+  }
+  hipLaunchKernelGGL((k_i8_tiles<ElemF32, true>), grid, dim3(I8_THREADS), 0, st, a);
+  if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  const int64_t want = ceil_div(a.N * (a.L4 / 4), 256), cap = 16 * cus;
+  hipLaunchKernelGGL(k_i8_join<E>, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
+  return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
+}
+
+int run_i8_matmul(const int8_t* X, const float* sx, const int8_t* W, const float* sw, int64_t N, int64_t L, int D, void* Y,
+                  int ytype, int64_t ldy, const I8Layout& s, void* workspace, hipStream_t st) {
+  I8Args a{};
+  a.X = (const char*)X; a.W = (const char*)W; a.sx = sx; a.sw = sw; a.Y = Y; a.ldy = ldy; a.N = N; a.L = L; a.D = D;
+  a.row_tiles = (int)ceil_div(N, I8_TN); a.label_tiles = (int)ceil_div(L, TILE_M); a.slots = s.slots; a.per = s.per;
+  a.part = (int*)workspace; a.L4 = s.L4;
+  if (ytype == T_F32_) return matmul_as<ElemF32>(a, st);
+  if (ytype == T_BF16_) return matmul_as<ElemBF16>(a, st);
+  return matmul_as<ElemF16>(a, st);
+}
+
+}  // namespace elmo

@@ -43,6 +43,13 @@ int check_linear(int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw
   return ELMO_OK;
 }
 
+int check_i8(int64_t N, int64_t L, int D) {
+  if (N < 0 || N >= (int64_t(1) << 31) || L < 1 || L >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (D < 64 || D % 64 != 0 || D > ELMO_MAX_I8_D) return ELMO_ESHAPE;
+  if (((N + 255) / 256) * ((L + 255) / 256) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  return ELMO_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,6 +218,51 @@ int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_
   c.row_max = row_max; c.log_sum = log_sum; c.dlogp = dlogp; c.dlse = dlse;
   c.dX = dX; c.dx_type = dx_type; c.lddx = lddx; c.dW = dW; c.dw_type = dw_type; c.lddw = lddw; c.accumulate = accumulate;
   return elmo::run_linear_logprobs_grad(c, s, workspace, (hipStream_t)stream);
+}
+
+int elmo_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, void* stream) {
+  if (!known_type(type)) return ELMO_EDTYPE;
+  const int rc = check_i8(N, 1, D);
+  if (rc != ELMO_OK) return rc;
+  if (ldx < D) return ELMO_ESHAPE;
+  if (N == 0) return ELMO_OK;
+  if (!x || !codes || !scales || !rows16(x, type, ldx) || !aligned16(codes) || !aligned_to(scales, 4)) return ELMO_EINVAL;
+  return elmo::run_i8_quantize(x, type, N, D, ldx, codes, scales, (hipStream_t)stream);
+}
+
+size_t elmo_i8_matmul_workspace_bytes(int64_t N, int64_t L, int D) {
+  if (N < 1 || check_i8(N, L, D) != ELMO_OK) return 0;
+  return elmo::i8_layout(N, L, D).total;
+}
+
+int elmo_i8_matmul(const int8_t* X, const float* x_scales, const int8_t* W, const float* w_scales, int64_t N, int64_t L,
+                   int D, void* Y, int ytype, int64_t ldy, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!known_type(ytype)) return ELMO_EDTYPE;
+  const int rc = check_i8(N, L, D);
+  if (rc != ELMO_OK) return rc;
+  if (ldy < L) return ELMO_ESHAPE;
+  if (N == 0) return ELMO_OK;
+  if (!X || !W || !x_scales || !w_scales || !Y || !aligned16(X) || !aligned16(W) || !aligned_to(x_scales, 4) ||
+      !aligned_to(w_scales, 4) || !aligned_to(Y, type_bytes(ytype)))
+    return ELMO_EINVAL;
+  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
+  const elmo::I8Layout s = elmo::i8_layout(N, L, D);
+  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  return elmo::run_i8_matmul(X, x_scales, W, w_scales, N, L, D, Y, ytype, ldy, s, workspace, (hipStream_t)stream);
+}
+
+int elmo_dropout(const void* x, int type, int64_t T, int64_t D, int64_t ldx, const void* residual, int64_t ldr, double p,
+                 uint64_t seed, uint64_t step, const uint64_t* step_at, uint64_t first, void* y, int64_t ldy, void* stream) {
+  if (!known_type(type)) return ELMO_EDTYPE;
+  if (T < 0 || T >= (int64_t(1) << 31) || D < 1 || D >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (ldx < D || ldy < D || (residual && ldr < D) || (y == x && ldy != ldx) || (residual && y == residual && ldy != ldr))
+    return ELMO_ESHAPE;
+  if (!(p >= 0.0 && p <= 1.0) || first + (uint64_t)(T * D) < first) return ELMO_EINVAL;
+  if (T == 0) return ELMO_OK;
+  const size_t e = type_bytes(type);
+  if (!x || !y || !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(residual, e) || !aligned_to(step_at, 8)) return ELMO_EINVAL;
+  return elmo::run_dropout(x, type, T, D, ldx, residual, ldr, (uint32_t)(p * 65536.0 + 0.5), seed, step, step_at, first, y, ldy,
+                           (hipStream_t)stream);
 }
 
 }  // extern "C"

@@ -57,4 +57,15 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
 int run_zero_rows(void* out, int type, int64_t rows, int D, int64_t ld, hipStream_t st);
 int run_linear_logprobs_grad(const LinearGradCall& c, const LinearGradLayout& s, void* workspace, hipStream_t st);
 
+// rows in 8-bit integers with a scale each, and products of such rows
+struct I8Layout { int slots, per; int64_t L4; size_t total; };
+int run_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st);
+I8Layout i8_layout(int64_t N, int64_t L, int D);
+int run_i8_matmul(const int8_t* X, const float* sx, const int8_t* W, const float* sw, int64_t N, int64_t L, int D, void* Y,
+                  int ytype, int64_t ldy, const I8Layout& s, void* workspace, hipStream_t st);
+
+// dropout from a counter-based generator (r: residual or NULL; step_at: added to step, or NULL)
+int run_dropout(const void* x, int type, int64_t T, int64_t D, int64_t ldx, const void* r, int64_t ldr, uint32_t limit,
+                uint64_t seed, uint64_t step, const uint64_t* step_at, uint64_t first, void* y, int64_t ldy, hipStream_t st);
+
 }  // namespace elmo
