@@ -153,6 +153,20 @@ __device__ __forceinline__ void store_results(typename E::raw* p, int64_t left, 
       if (i < left) E::store(p + i, y[i]);
   }
 }
+// a piece of 16 bytes of results, `left` of them present
+template <typename E>
+__device__ __forceinline__ void store_piece(typename E::raw* p, int64_t left, i32x4_t x) {
+  if (left >= E::VEC) {
+    if constexpr (E::VEC == 4) *(i32x4_a4_t*)p = x;
+    else *(i32x4_a2_t*)p = x;
+  } else {
+    float y[8];
+    E::widen(x, y);
+#pragma unroll
+    for (int i = 0; i < E::VEC - 1; ++i)
+      if (i < left) E::store(p + i, y[i]);
+  }
+}
 // scales of labels v .. v + 3, zero past the last
 __device__ __forceinline__ f32x4_t scales4(const float* sw, int64_t v, int64_t L) {
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -162,7 +176,7 @@ __device__ __forceinline__ f32x4_t scales4(const float* sw, int64_t v, int64_t L
   return s;
 }
 
-constexpr int I8_WN = 4, I8_NBUF = 4, I8_THREADS = 128 * I8_WN, I8_TN = 64 * I8_WN, I8_GROUP = 8;
+constexpr int I8_WN = 4, I8_NBUF = 3, I8_THREADS = 128 * I8_WN, I8_TN = 64 * I8_WN, I8_GROUP = 8;
 
 template <typename E, bool PARTS>
 struct I8Job : I8Args {
@@ -182,44 +196,63 @@ struct I8Job : I8Args {
     const int s0 = slot * per, all = D / STAGE_K, len = all - s0 < per ? all - s0 : per;
     return {{W + l * D + s0 * STAGE_K, D, L - l, 0}, {X + n * D + s0 * STAGE_K, D, N - n, 0}, len};
   }
-  __device__ __forceinline__ void finish(int u, i32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+  static constexpr int STORES = PARTS || E::VEC == 4 ? 32 : 16;
+  __device__ __forceinline__ bool finish(int u, i32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int lt, nt, slot;
     place(u, lt, nt, slot);
-    const int64_t v0 = (int64_t)lt * TILE_M + 128 * wm + 4 * (lane >> 5), n0 = (int64_t)nt * I8_TN + 64 * wn + (lane & 31);
-    float s[2];
-    if constexpr (!PARTS) {
+    const int64_t v0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * I8_TN + 64 * wn;
+    const int64_t left = L - v0;                           // (scales past the last label read as zero)
+    const auto scales = buffer_rsrc(PARTS ? nullptr : sw + v0, PARTS ? 0 : 4 * (int)(left < 0 ? 0 : left < 128 ? left : 128));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) s[j] = n0 + 32 * j < N ? sx[n0 + 32 * j] : 0.0f;
-    }
+    for (int j = 0; j < 2; ++j) {
+      const int64_t r0 = n0 + 32 * j;
+      if constexpr (!PARTS) {                              // the results take the sums' place
+        const float s = r0 + (lane & 31) < N ? sx[r0 + (lane & 31)] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t v = v0 + 32 * i + 8 * q;
-        f32x4_t t;
-        if constexpr (!PARTS) t = scales4(sw, v, L);
+          for (int q = 0; q < 4; ++q) {
+            const i32x4_t t = buffer_load16(scales, 16 * (8 * i + 2 * q + (lane >> 5)));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t n = n0 + 32 * j;
-          if (n < N && v < L) {
-            if constexpr (PARTS) {
-              *(i32x4_t*)(part + ((int64_t)slot * N + n) * L4 + v) =
-                  i32x4_t{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-            } else {
-              float y[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) y[k] = (float)acc[i][j][4 * q + k] * s[j] * t[k];
-              store_results<E>((typename E::raw*)Y + n * ldy + v, L - v, y);
-            }
+            for (int k = 0; k < 4; ++k) acc[i][j][4 * q + k] = (int)f2u((float)acc[i][j][4 * q + k] * s * u2f((uint32_t)t[k]));
           }
-        }
       }
+      if constexpr (PARTS || E::VEC == 4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          i32x4_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const i32x16_t& a = acc[2 * h + k / 4][j];
+            const int q = 4 * (k % 4);
+            v[k] = i32x4_t{a[q], a[q + 1], a[q + 2], a[q + 3]};
+          }
+          put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+            const int64_t n = r0 + row, l = v0 + 64 * h + 4 * c;
+            if (n >= N || l >= L) return;
+            if constexpr (PARTS) *(i32x4_t*)(part + ((int64_t)slot * N + n) * L4 + l) = x;
+            else store_piece<E>((typename E::raw*)Y + n * ldy + l, L - l, x);
+          });
+        }
+      } else {
+        i32x4_t v[8];
+        pieces16(acc, j, v, [](int lo, int hi) {
+          const float z[8] = {u2f((uint32_t)lo), u2f((uint32_t)hi), 0, 0, 0, 0, 0, 0};
+          return E::narrow(z)[0];
+        });
+        put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+          const int64_t n = r0 + row, l = v0 + 8 * c;
+          if (n < N && l < L) store_piece<E>((typename E::raw*)Y + n * ldy + l, L - l, x);
+        });
+      }
+    }
+    return n0 + 64 <= N && left >= 128;
   }
 };
 
 template <typename E, bool PARTS>
 __global__ __launch_bounds__(I8_THREADS, 2) void k_i8_tiles(I8Args a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<I8_WN, I8_NBUF>()];
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<I8_WN, I8_NBUF, true>()];
   I8Job<E, PARTS> job;
   (I8Args&)job = a;
   const UnitRange r = xcd_units(a.label_tiles * a.row_tiles * a.slots);

@@ -17,7 +17,8 @@
 namespace elmo {
 
 constexpr float L2E = 1.44269502162933349609375f;          // FP32(log2 e)
-constexpr int LIN_WN = 4, LIN_NBUF = 4, LIN_THREADS = 128 * LIN_WN, LIN_TN = 64 * LIN_WN;
+constexpr int LIN_WN = 4, LIN_NBUF = 3, LIN_THREADS = 128 * LIN_WN, LIN_TN = 64 * LIN_WN;
+constexpr int COEF_THREADS = 1024;
 constexpr int GROUP = 8;                                   // label tiles that are taken together over the rows
 
 // ---- logits ----------------------------------------------------------------------------------------
@@ -56,8 +57,9 @@ struct StatArgs {
 };
 
 struct StatJob : StatArgs {
+  static constexpr int STORES = 2;
   __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
-  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int lt, nt;
     t.place(u, lt, nt);
     const int64_t l0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
@@ -115,12 +117,13 @@ struct StatJob : StatArgs {
         }
       }
     }
+    return n0 + 64 <= t.N;
   }
 };
 
 template <class Mul>
 __global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_stats(StatArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, false>()];
   StatJob job;
   (StatArgs&)job = a;
   const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
@@ -191,12 +194,12 @@ struct CoefArgs {
 // the largest given gradient of a row, and the bound of |G| in it (finite ones only)
 __device__ __forceinline__ float2 row_bound(const CoefArgs& a, int64_t n) {
   float most = 0.0f, all = a.dlse ? fabsf(a.dlse[n]) : 0.0f;
-  for (int g = 0; g < a.M; ++g)
-    if (a.ids[n * a.M + g] >= 0) {
-      const float d = fabsf(a.dlogp[n * a.M + g]);
-      if (d < __builtin_inff()) most = fmaxf(most, d);
-      all += 2.0f * d;
-    }
+  for (int g = 0; g < a.M; ++g) {
+    const int id = a.ids[n * a.M + g];                     // (both loads are on their way together)
+    const float d = fabsf(a.dlogp[n * a.M + g]);
+    if (id >= 0 && d < __builtin_inff()) most = fmaxf(most, d);
+    if (id >= 0) all += 2.0f * d;
+  }
   return make_float2(most, all < __builtin_inff() ? all : 0.0f);
 }
 __device__ __forceinline__ float2 block_max(float2 v, float2* s) {
@@ -208,17 +211,17 @@ __device__ __forceinline__ float2 block_max(float2 v, float2* s) {
   if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = v;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < COEF_THREADS / 64; ++w) {
     v.x = fmaxf(v.x, s[w].x);
     v.y = fmaxf(v.y, s[w].y);
   }
   return v;
 }
 
-__global__ __launch_bounds__(256) void k_lin_bound(CoefArgs a) {
-  __shared__ float2 s[4];
+__global__ __launch_bounds__(COEF_THREADS) void k_lin_bound(CoefArgs a) {
+  __shared__ float2 s[COEF_THREADS / 64];
   float2 v = make_float2(0.0f, 0.0f);
-  for (int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x; n < a.N; n += (int64_t)gridDim.x * 256) {
+  for (int64_t n = blockIdx.x * (int64_t)COEF_THREADS + threadIdx.x; n < a.N; n += (int64_t)gridDim.x * COEF_THREADS) {
     const float2 r = row_bound(a, n);
     v.x = fmaxf(v.x, r.x);
     v.y = fmaxf(v.y, r.y);
@@ -227,16 +230,17 @@ __global__ __launch_bounds__(256) void k_lin_bound(CoefArgs a) {
   if (threadIdx.x == 0) a.most[blockIdx.x] = v;
 }
 
-__global__ __launch_bounds__(256) void k_lin_coef(CoefArgs a) {
-  __shared__ float2 s[4];
+__global__ __launch_bounds__(COEF_THREADS) void k_lin_coef(CoefArgs a) {
+  __shared__ float2 s[COEF_THREADS / 64];
   float2 v = make_float2(0.0f, 0.0f);
   if (a.parts > 0) {
-    for (int i = (int)threadIdx.x; i < a.parts; i += 256) {
+    for (int i = (int)threadIdx.x; i < a.parts; i += COEF_THREADS) {
       v.x = fmaxf(v.x, a.most[i].x);
       v.y = fmaxf(v.y, a.most[i].y);
     }
   } else {
-    for (int64_t n = threadIdx.x; n < a.N; n += 256) {
+#pragma unroll 4
+    for (int64_t n = threadIdx.x; n < a.N; n += COEF_THREADS) {
       const float2 r = row_bound(a, n);
       v.x = fmaxf(v.x, r.x);
       v.y = fmaxf(v.y, r.y);
@@ -253,7 +257,7 @@ __global__ __launch_bounds__(256) void k_lin_coef(CoefArgs a) {
   }
   const float scale = 1.0f / unit;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = unit;
-  const int64_t n = blockIdx.x * (int64_t)256 + threadIdx.x;
+  const int64_t n = blockIdx.x * (int64_t)COEF_THREADS + threadIdx.x;
   if (n >= a.N) return;
   const double lse = (double)a.row_max[n] + (double)a.log_sum[n];
   const bool empty = lse == -__builtin_inf();
@@ -292,8 +296,9 @@ struct GradArgs {
 
 template <class Mul>
 struct GradJob : GradArgs {
+  static constexpr int STORES = 16;
   __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
-  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int lt, nt;
     t.place(u, lt, nt);
     const int64_t col0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
@@ -326,7 +331,7 @@ struct GradJob : GradArgs {
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-              if (at == 32 * i + 8 * (r / 4) + r % 4) acc[i][j][r] += d;
+              acc[i][j][r] += at == 32 * i + 8 * (r / 4) + r % 4 ? d : 0.0f;
         }
       }
     }
@@ -338,32 +343,22 @@ struct GradJob : GradArgs {
         for (int r = 0; r < 16; ++r)
           if (32 * i + 8 * (r / 4) + r % 4 >= mine) acc[i][0][r] = acc[i][1][r] = 0.0f;
     }
-    // a lane has 4 labels of every 8; it swaps with the lane of the other half, so that each stores 8
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      char* row = G + n[j] * ldg + 2 * (col0 + 8 * half);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          int lo[2], hi[2];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            lo[k] = pack16<Mul>(acc[i][j][4 * q + 2 * k], acc[i][j][4 * q + 2 * k + 1]);
-            hi[k] = pack16<Mul>(acc[i][j][4 * q + 4 + 2 * k], acc[i][j][4 * q + 5 + 2 * k]);
-            auto sw = __builtin_amdgcn_permlane32_swap(lo[k], hi[k], false, false);
-            lo[k] = (int)sw[0];
-            hi[k] = (int)sw[1];
-          }
-          if (n[j] < t.N) *(i32x4_t*)(row + 2 * (32 * i + 8 * q)) = i32x4_t{lo[0], lo[1], hi[0], hi[1]};
-        }
+      i32x4_t v[8];
+      pieces16(acc, j, v, [](float lo, float hi) { return pack16<Mul>(lo, hi); });
+      const int64_t r0 = n0 + 32 * j;
+      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+        if (r0 + row < t.N) *(i32x4_t*)(G + (r0 + row) * ldg + 2 * col0 + 16 * c) = x;
+      });
     }
+    return n0 + 64 <= t.N;
   }
 };
 
 template <class Mul>
 __global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_grad_logits(GradArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, true>()];
   GradJob<Mul> job;
   (GradArgs&)job = a;
   const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
@@ -377,13 +372,13 @@ struct ProductArgs {
   const char* W; int64_t ldw;
   const char* G; int64_t ldg;
   int64_t N, v0, v1, cols;                                 // cols: the piece's labels, a multiple of 256
-  int D, d_tiles;
+  int D, d_tiles, row_tiles;
   const float* inv;
   // dW: the tokens in w_slots runs of w_per; one run goes to the result, several to `wpart`
   int w_units, w_slots; int64_t w_per;
   float* wpart; OutArgs dW;
   // dX: the piece's labels in x_slots runs of x_per, each added to its partial sum
-  int x_units, x_slots, first; int64_t x_per;
+  int x_units, x_slots, x_heavy, x_light, first; int64_t x_per;
   float* xpart;
 };
 
@@ -407,7 +402,44 @@ __device__ __forceinline__ void store4(const OutArgs& o, int64_t row, int64_t co
   }
 }
 
+// A wave's 64 rows x 128 columns of a result in rows: tile row r of the result is row r0 + r, present below `rows`; the
+// columns start at c0, present below `cols` (a multiple of 8). Scaled by f, in o's type, added to or not. Returns whether all of it is
+// present (then it took 16 stores at least).
+__device__ __forceinline__ bool store_tile(const OutArgs& o, f32x16_t (&acc)[4][2], float f, int64_t r0, int64_t rows, int c0, int cols,
+                                           int lane, char* lds) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t rj = r0 + 32 * j;
+    if (o.type == T_F32_ || o.accumulate) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        i32x4_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const f32x16_t& s = acc[2 * h + k / 4][j];
+          const int q = 4 * (k % 4);
+          v[k] = i32x4_t{(int)f2u(s[q] * f), (int)f2u(s[q + 1] * f), (int)f2u(s[q + 2] * f), (int)f2u(s[q + 3] * f)};
+        }
+        put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+          const int col = c0 + 64 * h + 4 * c;
+          if (rj + row < rows && col < cols) store4(o, rj + row, col, __builtin_bit_cast(f32x4_t, x));
+        });
+      }
+    } else {
+      i32x4_t v[8];
+      if (o.type == T_BF16_) pieces16(acc, j, v, [f](float lo, float hi) { return pack16<MulBF16>(lo * f, hi * f); });
+      else pieces16(acc, j, v, [f](float lo, float hi) { return pack16<MulF16>(lo * f, hi * f); });
+      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+        const int col = c0 + 8 * c;
+        if (rj + row < rows && col < cols) *(i32x4_t*)((uint16_t*)o.out + (rj + row) * o.ld + col) = x;
+      });
+    }
+  }
+  return r0 + 64 <= rows && c0 + 128 <= cols;
+}
+
 struct WeightJob : ProductArgs {
+  static constexpr int STORES = 16;
   __device__ __forceinline__ void place(int u, int& dt, int& vt, int& slot) const {
     dt = u % d_tiles;
     slot = u / d_tiles % w_slots;
@@ -421,33 +453,22 @@ struct WeightJob : ProductArgs {
     const int dc = D - d0 < TILE_M ? D - d0 : TILE_M;
     return {{X + t0 * ldx + 2 * d0, ldx, rows, 2 * dc}, {G + t0 * ldg + 2 * (int64_t)v, ldg, rows, 2 * LIN_TN}, (int)((rows + 31) / 32)};
   }
-  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int dt, vt, slot;
     place(u, dt, vt, slot);
-    const float f = *inv;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t c = (int64_t)vt * LIN_TN + 64 * wn + 32 * j + (lane & 31), v = v0 + c;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = dt * TILE_M + 128 * wm + 32 * i + 8 * q + 4 * (lane >> 5);
-          const f32x4_t s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          if (v < v1 && d < D) {
-            if (w_slots > 1) *(f32x4_t*)(wpart + ((int64_t)slot * cols + c) * D + d) = s;
-            else store4(dW, v, d, s * f);
-          }
-        }
-    }
+    const int64_t c = (int64_t)vt * LIN_TN + 64 * wn;
+    const int d = dt * TILE_M + 128 * wm;
+    if (w_slots > 1) return store_tile(OutArgs{wpart + (int64_t)slot * cols * D, D, T_F32_, 0}, acc, 1.0f, c, cols, d, D, lane, lds);
+    return store_tile(dW, acc, *inv, v0 + c, v1, d, D, lane, lds);
   }
 };
 
 struct FeatureJob : ProductArgs {
+  static constexpr int STORES = 16;
   __device__ __forceinline__ void place(int u, int& dt, int& nt, int& slot) const {
     dt = u % d_tiles;
-    slot = u / d_tiles % x_slots;
-    nt = u / d_tiles / x_slots;
+    nt = u / d_tiles % row_tiles;
+    slot = u / d_tiles / row_tiles;                        // (units of one run share its weights)
   }
   __device__ __forceinline__ TileUnit unit(int u) const {
     int dt, nt, slot;
@@ -457,54 +478,62 @@ struct FeatureJob : ProductArgs {
     const int d0 = dt * TILE_M, dc = D - d0 < TILE_M ? D - d0 : TILE_M;
     return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, N - n, 0}, (int)(len / 32)};
   }
-  __device__ __forceinline__ void finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int dt, nt, slot;
     place(u, dt, nt, slot);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int64_t n = (int64_t)nt * LIN_TN + 64 * wn + 32 * j + (lane & 31);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int d = dt * TILE_M + 128 * wm + 32 * i + 8 * q + 4 * (lane >> 5);
-          f32x4_t s = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-          if (n < N && d < D) {
-            f32x4_t* p = (f32x4_t*)(xpart + ((int64_t)slot * N + n) * D + d);
-            if (!first) s += *p;
-            *p = s;
-          }
-        }
-    }
+    return store_tile(OutArgs{xpart + (int64_t)slot * N * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * LIN_TN + 64 * wn, N,
+               dt * TILE_M + 128 * wm, D, lane, lds);
   }
 };
 
+// A block takes the units of dW in turn with the others (the first w_units % blocks take one more), then a
+// run of units of dX, x_heavy or x_light of them, so that both kinds of block end together. Blocks of
+// an XCD have neighbouring numbers here.
 template <class Mul>
 __global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_products(ProductArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF>()];
-  if (a.w_units > 0) {
+  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, true>()];
+  const int blocks = (int)gridDim.x, per = blocks / 8;
+  const int b = blocks % 8 == 0 ? ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3) : (int)blockIdx.x;
+  {
     WeightJob job;
     (ProductArgs&)job = a;
-    const UnitRange r = xcd_units(a.w_units);
-    tile_stream<Mul, true, true, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+    tile_stream<Mul, true, true, LIN_WN, LIN_NBUF>(job, b, blocks, a.w_units, lds);
   }
-  if (a.x_units > 0) {
+  {
     FeatureJob job;
     (ProductArgs&)job = a;
-    const UnitRange r = xcd_units(a.x_units);
-    tile_stream<Mul, true, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+    const int heavy = a.w_units % blocks;
+    const int first = b < heavy ? b * a.x_heavy : heavy * a.x_heavy + (b - heavy) * a.x_light;
+    const int end = first + (b < heavy ? a.x_heavy : a.x_light);
+    tile_stream<Mul, true, false, LIN_WN, LIN_NBUF>(job, first, 1, end < a.x_units ? end : a.x_units, lds);
   }
 }
 
-// rows [r0, r0 + rows) of a result from the partial sums of `slots` runs, in the order of the runs
+// rows [r0, r0 + rows) of a result from the partial sums of `slots` runs. Thread (x, y) of a block of 64 x 4 sums the runs
+// y, y + 4, .. of vector x; the four sums are added in the order of y.
 __global__ __launch_bounds__(256) void k_lin_sum(const float* part, int64_t stride, int slots, int64_t r0, int64_t rows, int D,
                                                  const float* inv, OutArgs o) {
+  __shared__ f32x4_t sums[4][64];
+  const int x = (int)threadIdx.x & 63, y = (int)threadIdx.x >> 6;
   const float f = *inv;
   const int d4 = D / 4;
-  for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < rows * d4; i += (int64_t)gridDim.x * 256) {
-    f32x4_t s = *(const f32x4_t*)(part + i * 4);
-    for (int k = 1; k < slots; ++k) s += *(const f32x4_t*)(part + k * stride + i * 4);
-    store4(o, r0 + i / d4, i % d4 * 4, s * f);
+  const int64_t n4 = rows * d4;
+  for (int64_t i0 = blockIdx.x * (int64_t)64; i0 < n4; i0 += (int64_t)gridDim.x * 64) {
+    const int64_t i = i0 + x;
+    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (i < n4) {
+#pragma unroll 8
+      for (int k = y; k < slots; k += 4) s += *(const f32x4_t*)(part + k * stride + i * 4);
+    }
+    sums[y][x] = s;
+    __syncthreads();
+    if (y == 0 && i < n4) {
+      s += sums[1][x];
+      s += sums[2][x];
+      s += sums[3][x];
+      store4(o, r0 + i / d4, i % d4 * 4, s * f);
+    }
+    __syncthreads();
   }
 }
 
@@ -514,6 +543,10 @@ static unsigned blocks_for(int64_t units) {
   return (unsigned)(units < cus ? units : cus);
 }
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static unsigned sum_grid(int64_t rows, int D) {
+  const int64_t want = ceil_div(rows * (D / 4), 64), cap = 32 * (int64_t)device_cus();
+  return (unsigned)(want < cap ? want : cap);
+}
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 LinearLayout linear_layout(int64_t N, int64_t V, int M) {
@@ -549,30 +582,69 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
 
-// The piece: 2^26 gradient codes (128 MiB, which the last-level cache holds) or the caller's number of
-// labels, a multiple of 256; pieces of about equal length. Runs: so many that a launch has a unit for
-// every compute unit, as long as a run keeps 16 stages.
+// How one piece's products are spread over the device: the time (us) of a launch whose dX is cut into x_slots
+// runs and dW into w_slots, by what a stage (1 us with every compute unit at work), a unit's start and its
+// results take; and how many units of dX a block takes that has one unit of dW more than the others
+// (heavy) or not (light).
+static double products_time(int64_t tiles, int64_t wst, int64_t row_tiles, int64_t dt, int64_t w_slots, int64_t x_slots, bool add,
+                            bool dw, bool dx, int* heavy, int* light) {
+  const int64_t cus = device_cus();
+  const double tw = 3.0 + (double)ceil_div(wst, w_slots), tx = (add ? 10.0 : 4.0) + (double)ceil_div(tiles * 8, x_slots);
+  const int64_t uw = dw ? tiles * dt * w_slots : 0, ux = dx ? row_tiles * dt * x_slots : 0;
+  const int64_t base = uw / cus, rem = uw % cus;
+  const double floor_w = (double)base * tw, top_w = (double)(base + 1) * tw;
+  double best = 0.0;
+  for (int k = 0; k < 2; ++k)
+    for (int64_t m = 0;; ++m) {
+      const double T = (k ? top_w : floor_w) + (double)m * tx;
+      if (best > 0.0 && T >= best) break;
+      if (rem > 0 && T < top_w) continue;
+      const int64_t h = rem > 0 ? (int64_t)((T - top_w) / tx + 1e-6) : 0, l = (int64_t)((T - floor_w) / tx + 1e-6);
+      if (rem * h + (cus - rem) * l >= ux) {
+        best = T > 0.0 ? T : 1e-3;
+        *heavy = (int)h;
+        *light = (int)l;
+        break;
+      }
+    }
+  return best;
+}
+
+// The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache) and the runs,
+// by the time they are expected to take: more pieces fill the device's last round better or worse, runs fill it
+// with less in each, but are summed apart (dX by adding to memory, dW by another launch). 4096 rows x 131,072
+// labels x 768: equal pieces and one run per round of blocks took 324 us a piece, runs alone 25% less.
+constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
   LinearGradLayout s{};
-  const int64_t whole = ceil_div(V, TILE_M) * TILE_M;
-  int64_t piece = chunk > 0 ? ceil_div(chunk, TILE_M) * TILE_M : (int64_t(1) << 26) / N / TILE_M * TILE_M;
-  if (piece < TILE_M) piece = TILE_M;
-  if (piece > whole) piece = whole;
-  const int64_t pieces = ceil_div(whole, piece);
-  s.piece = ceil_div(ceil_div(whole, pieces), TILE_M) * TILE_M;
-  const int64_t cus = device_cus(), dt = ceil_div(D, TILE_M);
-  const int64_t wt = s.piece / LIN_TN * dt, xt = ceil_div(N, LIN_TN) * dt;   // tiles of dW and dX
-  const int64_t wst = ceil_div(N, 32), xst = s.piece / 32;                   // their stages
-  s.w_slots = s.x_slots = 1;
-  // runs of about the same number of stages in both, no more than it takes to fill the device
-  const int64_t stages = (need_dw ? wt * wst : 0) + (need_dx ? xt * xst : 0);
-  int64_t run = ceil_div(stages, cus);
-  if (run < 16) run = 16;
-  auto slots_of = [&](int64_t st) { const int64_t k = (st + run / 2) / run; return k < 1 ? 1 : k; };
-  s.x_slots = (int)slots_of(xst);
-  s.x_per = ceil_div(xst, s.x_slots) * 32;
+  const int64_t cus = device_cus(), dt = ceil_div(D, TILE_M), row_tiles = ceil_div(N, LIN_TN);
+  const int64_t whole = ceil_div(V, TILE_M);               // label tiles
+  int64_t most = chunk > 0 ? ceil_div(chunk, TILE_M) : (int64_t(1) << 27) / N / TILE_M;
+  most = most < 1 ? 1 : (most > whole ? whole : most);
+  if (most > MAX_PIECE / TILE_M) most = MAX_PIECE / TILE_M;
+  const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most);
+  const double rd = (double)N * D * 4e-6 / 5.0;            // us for dX's size in FP32 to memory
+  double least = 0.0;
+  for (int64_t pieces = fewest; pieces <= (chunk > 0 ? fewest : fewest + 4) && pieces <= whole; ++pieces) {
+    const int64_t tiles = chunk > 0 ? most : ceil_div(whole, pieces), used = ceil_div(whole, tiles);
+    const double logits = (double)ceil_div(row_tiles * tiles, cus) * (6.0 + D / 32) + 4.0;
+    for (int64_t ws = 1; ws <= 16; ws *= 2) {
+      if (ws > 1 && (!need_dw || ws * 2 > wst || tiles * dt * ws > 2 * cus)) break;
+      for (int64_t xs = 1; xs <= 16 || (xs <= 64 && row_tiles * dt * xs <= cus); xs = xs < 8 ? xs + 1 : xs + xs / 4) {
+        if (xs > 1 && (!need_dx || xs * 2 > tiles * 8)) break;
+        int h = 0, l = 0;
+        double us = products_time(tiles, wst, row_tiles, dt, ws, xs, used > 1, need_dw, need_dx, &h, &l) + logits + 4.0;
+        if (ws > 1) us += 4.0 + (double)(ws + 1) * tiles * TILE_M * D * 4e-6 / 5.0;
+        us = us * (double)used + (double)xs * rd;
+        if (least == 0.0 || us < least) {
+          least = us;
+          s.piece = tiles * TILE_M; s.x_slots = (int)xs; s.w_slots = (int)ws;
+        }
+      }
+    }
+  }
+  s.x_per = ceil_div(s.piece / 32, s.x_slots) * 32;
   s.x_slots = (int)ceil_div(s.piece, s.x_per);
-  s.w_slots = wt >= cus ? 1 : (int)slots_of(wst);
   s.w_per = ceil_div(wst, s.w_slots) * 32;
   s.w_slots = (int)ceil_div(N, s.w_per);
   size_t at = 0;
@@ -594,10 +666,10 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
   k.most = (float2*)(ws + s.most); k.coef = (float2*)(ws + s.coef); k.up = (float*)(ws + s.up); k.inv = (float*)(ws + s.inv);
   k.f16 = std::is_same_v<Mul, MulF16>;
   // rows that every block can go through by itself need no launch for their bound
-  k.parts = c.N <= 8192 ? 0 : 256;
-  if (k.parts) hipLaunchKernelGGL(k_lin_bound, dim3(k.parts), dim3(256), 0, st, k);
+  k.parts = c.N * (c.M + 1) <= 16384 ? 0 : 256;
+  if (k.parts) hipLaunchKernelGGL(k_lin_bound, dim3(k.parts), dim3(COEF_THREADS), 0, st, k);
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-  hipLaunchKernelGGL(k_lin_coef, dim3((unsigned)ceil_div(c.N, 256)), dim3(256), 0, st, k);
+  hipLaunchKernelGGL(k_lin_coef, dim3((unsigned)ceil_div(c.N, COEF_THREADS)), dim3(COEF_THREADS), 0, st, k);
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   for (int64_t v0 = 0; v0 < c.V; v0 += s.piece) {
     const int64_t v1 = v0 + s.piece < c.V ? v0 + s.piece : c.V;
@@ -613,21 +685,28 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
     p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0; p.xpart = (float*)(ws + s.xpart);
+    p.row_tiles = (int)ceil_div(c.N, LIN_TN);
     p.w_units = c.dW ? (int)(p.cols / LIN_TN) * p.d_tiles * p.w_slots : 0;
-    p.x_units = c.dX ? (int)ceil_div(c.N, LIN_TN) * p.d_tiles * p.x_slots : 0;
-    hipLaunchKernelGGL(k_lin_products<Mul>, dim3(blocks_for((int64_t)p.w_units + p.x_units)), dim3(LIN_THREADS), 0, st, p);
+    p.x_units = c.dX ? p.row_tiles * p.d_tiles * p.x_slots : 0;
+    const int64_t cus = device_cus();
+    const unsigned grid = blocks_for((int64_t)p.w_units + p.x_units);
+    if (grid < cus) {                                      // a unit for each block
+      p.x_heavy = 0;
+      p.x_light = 1;
+    } else {
+      products_time(p.cols / TILE_M, ceil_div(c.N, 32), p.row_tiles, p.d_tiles, p.w_slots, p.x_slots, s.piece < c.V, c.dW != nullptr,
+                    c.dX != nullptr, &p.x_heavy, &p.x_light);
+    }
+    hipLaunchKernelGGL(k_lin_products<Mul>, dim3(grid), dim3(LIN_THREADS), 0, st, p);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
     if (c.dW && p.w_slots > 1) {
-      const int64_t n = (v1 - v0) * (c.D / 4);
-      const int64_t want = ceil_div(n, 256), cap = 16 * (int64_t)device_cus();
-      hipLaunchKernelGGL(k_lin_sum, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, p.wpart, p.cols * c.D, p.w_slots, v0,
+      hipLaunchKernelGGL(k_lin_sum, dim3(sum_grid(v1 - v0, c.D)), dim3(256), 0, st, p.wpart, p.cols * c.D, p.w_slots, v0,
                          v1 - v0, c.D, (const float*)k.inv, p.dW);
       if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
     }
   }
   if (c.dX) {
-    const int64_t n = c.N * (c.D / 4), want = ceil_div(n, 256), cap = 16 * (int64_t)device_cus();
-    hipLaunchKernelGGL(k_lin_sum, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, (const float*)(ws + s.xpart), c.N * c.D,
+    hipLaunchKernelGGL(k_lin_sum, dim3(sum_grid(c.N, c.D)), dim3(256), 0, st, (const float*)(ws + s.xpart), c.N * c.D,
                        s.x_slots, (int64_t)0, c.N, c.D, (const float*)k.inv, OutArgs{c.dX, c.lddx, c.dx_type, 0});
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   }

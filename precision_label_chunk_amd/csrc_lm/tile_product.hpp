@@ -3,7 +3,8 @@
 //
 // A block of 2 x WN waves computes 256 x 64 WN tiles, a wave 128 x 64 of it in 4 x 2 sums of 32 x 32
 // (128 registers). The depth goes in stages of 64 bytes of K per row (32 elements of 16 bits, 64 of 8),
-// copied from memory to LDS without passing registers, NBUF - 1 stages ahead, one barrier a stage. The
+// copied from memory to LDS without passing registers, NBUF - 1 stages ahead, one barrier a stage (NBUF = 3: 4 and
+// 5 are no faster, 96 KiB leave room for results on their way out). The
 // stages of a block's tiles follow each other without a break: the first stages of the next tile are on
 // their way while the sums of the last one are used.
 //
@@ -61,7 +62,7 @@ struct TileUnit { Operand a, b; int stages; };
 constexpr int TILE_M = 256, STAGE_K = 64;                  // rows of A per tile; bytes of K per stage
 
 template <int WN> constexpr int tile_n() { return 64 * WN; }
-template <int WN, int NBUF> constexpr int tile_lds() { return NBUF * (TILE_M + 64 * WN) * STAGE_K; }
+template <int WN, int NBUF, bool PUT> constexpr int tile_lds() { return NBUF * (TILE_M + 64 * WN) * STAGE_K + (PUT ? 2 * WN * 8192 : 0); }
 
 __device__ __forceinline__ int kc_swizzle(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
 __device__ __forceinline__ int km_swizzle(int k) { const int r = k & 3; return 2 * (2 * r | (r >> 1)); }
@@ -106,7 +107,7 @@ struct StageCopy {
       base += (int64_t)s * STAGE_K;
       bytes = o.rows > 0 ? ((o.rows < ROWS ? o.rows : ROWS) - 1) * o.ld + STAGE_K : 0;
     }
-    const auto buf = buffer_rsrc(base, live ? (int)bytes : 0);
+    const auto buf = buffer_rsrc(base, (int)bytes & (live ? -1 : 0));
 #pragma unroll
     for (int i = 0; i < COPIES; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_char_t*)(to + i * THREADS * 16 + wave * 1024), 16, off + i * step, 0, 0, 0);
@@ -144,10 +145,53 @@ struct StageRead {
   }
 };
 
+// A wave's results, on their way to memory in rows: 32 rows of 16 pieces of 16 bytes, of which a lane holds
+// pieces 2 k + lane / 32 (k = 0 .. 7) of row lane % 32. They go through 8 KiB of LDS of the wave's own, so
+// that 16 lanes write 256 bytes of a row: put(row, piece, value) 8 times. Straight from the sums a store reaches
+// 32 rows with 16 or 32 bytes in each, and a 256 x 256 tile of 16-bit results took 20 us to write, of 16-bit
+// gradient codes 4.
+template <class F>
+__device__ __forceinline__ void put_rows(char* lds, int lane, const i32x4_t (&v)[8], F&& put) {
+  asm volatile("" : "+v"(lane));                           // (no address is held across the products)
+  const int r = lane & 31;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) *(i32x4_t*)(lds + r * 256 + (((2 * k + (lane >> 5)) ^ (r & 15)) * 16)) = v[k];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int row = 4 * k + (lane >> 4), c = lane & 15;
+    put(row, c, *(const i32x4_t*)(lds + row * 256 + ((c ^ (row & 15)) * 16)));
+  }
+  sched_fence();                                           // (the next rows' values are not formed ahead: registers)
+}
+constexpr int PUT_BYTES = 8192;                            // of LDS per wave
+
+// 128 rows of m of one column as 16-bit pieces for put_rows: a lane has 4 of every 8, and swaps with the lane of
+// the other half, so that each holds 8. pack(lo, hi) rounds two sums.
+template <class Acc, class Pack>
+__device__ __forceinline__ void pieces16(const Acc& acc, int j, i32x4_t (&v)[8], Pack&& pack) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      int lo[2], hi[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        lo[k] = pack(acc[i][j][4 * q + 2 * k], acc[i][j][4 * q + 2 * k + 1]);
+        hi[k] = pack(acc[i][j][4 * q + 4 + 2 * k], acc[i][j][4 * q + 5 + 2 * k]);
+        auto s = __builtin_amdgcn_permlane32_swap(lo[k], hi[k], false, false);
+        lo[k] = (int)s[0];
+        hi[k] = (int)s[1];
+      }
+      v[2 * i + q / 2] = i32x4_t{lo[0], lo[1], hi[0], hi[1]};
+    }
+}
+
 // The products of the units first, first + step, .. below `end`; job.unit(u) describes a unit,
-// job.finish(u, acc, wm, wn, lane) uses its sums: acc[i][j][r] of wave (wm, wn) is row
+// job.finish(u, acc, wm, wn, lane, lds) uses its sums (lds: PUT_BYTES of the wave's own behind the buffers, if the
+// block has them): acc[i][j][r] of wave (wm, wn) is row
 // m = 128 wm + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 and column n = 64 wn + 32 j + lane % 32 of the tile.
-// Every unit has at least one stage. All threads of the block call it.
+// It returns whether the wave has issued at least
+// Job::STORES stores (the same for all its lanes). Every unit has at least one stage. All threads of the block call it.
 template <class Mul, bool AKM, bool BKM, int WN, int NBUF, class Job>
 __device__ __forceinline__ void tile_stream(const Job& job, int first, int step, int end, char* lds) {
   constexpr int THREADS = 128 * WN, A_BYTES = TILE_M * STAGE_K, BUF = A_BYTES + 64 * WN * STAGE_K;
@@ -207,16 +251,20 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
   int use = 0;
   // stage: its copies have landed (this wave's by the count, the others' by the barrier), and every wave has
   // read the buffer that the next copies go to; the last half's products run while its fragments are read
-  auto stage = [&](bool go_on) __attribute__((always_inline)) {
-    wait_copies<COPIES*(NBUF - 2)>();
+  // (behind a unit's end its stores are younger than the copies of the next NBUF - 1 stages: they need not be
+  // waited for. job.finish says whether this wave has made all of its STORES.)
+  auto stage = [&](bool go_on, bool stores) __attribute__((always_inline)) {
+    if (stores) wait_copies<COPIES*(NBUF - 2) + Job::STORES>();
+    else wait_copies<COPIES*(NBUF - 2)>();
     const char* from = lds + use * BUF;
     use = use + 1 == NBUF ? 0 : use + 1;
     frags(from, 0);
-    fetch();
     if (go_on) products(1);
     frags(from, 1);
+    fetch();                                               // (behind the reads: 1.2 times faster K-major than before them)
     products(0);
   };
+  bool stored = false;
   for (int u = first; u < end; u += step) {
     const int stages = job.unit(u).stages;
 #pragma unroll
@@ -225,10 +273,12 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
-    stage(false);
-    for (int s = 1; s < stages; ++s) stage(true);
+    stage(false, stored);
+    int s = 1;
+    for (; s < NBUF - 1 && s < stages; ++s) stage(true, stored);
+    for (; s < stages; ++s) stage(true, false);
     products(1);
-    job.finish(u, acc, wm, wn, lane);
+    stored = job.finish(u, acc, wm, wn, lane, lds + NBUF * BUF + wave * PUT_BYTES);
   }
   wait_copies<0>();                                        // no copy is on its way when the block's LDS is given back
 }
