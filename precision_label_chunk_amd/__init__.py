@@ -657,13 +657,27 @@ def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
     a whole number, or a CUDA int64 tensor of one element that is read when the work runs (for recorded graphs). out = x
     or out = residual writes over it. See elmo_dropout in elmo_xmc.h."""
     e = _etype(x)
-    if out is None:
-        out = x.new_empty(x.shape)
-    for name, t in (("out", out), ("residual", residual)):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype or t.device != x.device):
+    D, ld, matrix = x.shape[-1], 0, x.dim() == 2
+    if matrix:
+        T, D, ld = _rows("x", x)
+    elif x.dim() == 1 and x.is_cuda and x.is_contiguous():
+        T, ld = 1, D
+    else:
+        raise ValueError("x must be a 2-D CUDA tensor, or a contiguous 1-D one")
+
+    def pitch(name, t):
+        if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device:
             raise ValueError(f"{name} must have x's shape, type and device")
-    a, y, r = ((t if t is None or t.dim() != 1 else t.unsqueeze(0)) for t in (x, out, residual))
-    T, D, ld = _rows("x", a)
+        if matrix:
+            return _rows(name, t)[2]
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, as x is")
+        return D
+    ldr = 0 if residual is None else pitch("residual", residual)
+    if out is None:
+        out, ldy = x.new_empty(x.shape), D
+    else:
+        ldy = pitch("out", out)
     at = None
     if isinstance(step, torch.Tensor):
         if step.dtype != torch.int64 or step.numel() != 1 or step.device != x.device:
@@ -672,9 +686,10 @@ def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
     if D == 0:
         return out
     low = (1 << 64) - 1
-    _chk("elmo_dropout", lib().elmo_dropout(
-        x.data_ptr(), e, T, D, ld, _at(residual), _rows("residual", r)[2] if r is not None else 0, p, seed & low, step & low,
-        at, first & low, out.data_ptr(), _rows("out", y)[2], _stream_of(x.device)))
+    rc = lib().elmo_dropout(x.data_ptr(), e, T, D, ld, _at(residual), ldr, p, seed & low, step & low, at, first & low,
+                            out.data_ptr(), ldy, _stream_of(x.device))
+    if rc:
+        raise ElmoError("elmo_dropout", rc)
     return out
 
 

@@ -509,29 +509,32 @@ __global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_products(ProductArgs a) 
   }
 }
 
-// rows [r0, r0 + rows) of a result from the partial sums of `slots` runs. Thread (x, y) of a block of 64 x 4 sums the runs
-// y, y + 4, .. of vector x; the four sums are added in the order of y.
-__global__ __launch_bounds__(256) void k_lin_sum(const float* part, int64_t stride, int slots, int64_t r0, int64_t rows, int D,
-                                                 const float* inv, OutArgs o) {
+// Rows [r0, r0 + rows) of a result from the partial sums of `slots` runs, `stride` floats apart. Thread (x, y) of a block of
+// 64 x 4 sums the runs y, y + 4, .. of vector x; the four sums are added in the order of y. Two results share a
+// launch: the first `blocks` blocks take the first.
+struct SumArgs { const float* part; int64_t stride, r0, rows; int slots, D; OutArgs o; };
+__global__ __launch_bounds__(256) void k_lin_sum(SumArgs a, SumArgs b, int blocks, const float* inv) {
   __shared__ f32x4_t sums[4][64];
   const int x = (int)threadIdx.x & 63, y = (int)threadIdx.x >> 6;
   const float f = *inv;
-  const int d4 = D / 4;
-  const int64_t n4 = rows * d4;
-  for (int64_t i0 = blockIdx.x * (int64_t)64; i0 < n4; i0 += (int64_t)gridDim.x * 64) {
+  const bool second = (int)blockIdx.x >= blocks;
+  const SumArgs& s = second ? b : a;
+  const int d4 = s.D / 4;
+  const int64_t n4 = s.rows * d4, block = second ? blockIdx.x - blocks : blockIdx.x, all = second ? gridDim.x - blocks : blocks;
+  for (int64_t i0 = block * 64; i0 < n4; i0 += all * 64) {
     const int64_t i = i0 + x;
-    f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (i < n4) {
 #pragma unroll 8
-      for (int k = y; k < slots; k += 4) s += *(const f32x4_t*)(part + k * stride + i * 4);
+      for (int k = y; k < s.slots; k += 4) v += *(const f32x4_t*)(s.part + k * s.stride + i * 4);
     }
-    sums[y][x] = s;
+    sums[y][x] = v;
     __syncthreads();
     if (y == 0 && i < n4) {
-      s += sums[1][x];
-      s += sums[2][x];
-      s += sums[3][x];
-      store4(o, r0 + i / d4, i % d4 * 4, s * f);
+      v += sums[1][x];
+      v += sums[2][x];
+      v += sums[3][x];
+      store4(s.o, s.r0 + i / d4, i % d4 * 4, v * f);
     }
     __syncthreads();
   }
@@ -588,25 +591,32 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
 // (heavy) or not (light).
 static double products_time(int64_t tiles, int64_t wst, int64_t row_tiles, int64_t dt, int64_t w_slots, int64_t x_slots, bool add,
                             bool dw, bool dx, int* heavy, int* light) {
-  const int64_t cus = device_cus();
+  const int cus = device_cus();
   const double tw = 3.0 + (double)ceil_div(wst, w_slots), tx = (add ? 10.0 : 4.0) + (double)ceil_div(tiles * 8, x_slots);
   const int64_t uw = dw ? tiles * dt * w_slots : 0, ux = dx ? row_tiles * dt * x_slots : 0;
-  const int64_t base = uw / cus, rem = uw % cus;
-  const double floor_w = (double)base * tw, top_w = (double)(base + 1) * tw;
+  const int rem = (int)(uw % cus);
+  const double low = (double)(uw / cus) * tw, top = rem > 0 ? low + tw : low;
+  *heavy = *light = 0;
+  if (ux == 0) return top;
+  // the blocks end after m units of dX, counted from the end of dW's units of either kind: no earlier than the
+  // work shared out evenly, and soon after that
+  const double even = ((double)uw * tw + (double)ux * tx) / cus, from = even > top ? even : top;
   double best = 0.0;
-  for (int k = 0; k < 2; ++k)
-    for (int64_t m = 0;; ++m) {
-      const double T = (k ? top_w : floor_w) + (double)m * tx;
+  for (int k = 0; k < (rem > 0 ? 2 : 1); ++k) {
+    const double start = k ? top : low;
+    for (double m = (double)(int64_t)((from - start) / tx);; m += 1.0) {
+      const double T = start + m * tx;
       if (best > 0.0 && T >= best) break;
-      if (rem > 0 && T < top_w) continue;
-      const int64_t h = rem > 0 ? (int64_t)((T - top_w) / tx + 1e-6) : 0, l = (int64_t)((T - floor_w) / tx + 1e-6);
-      if (rem * h + (cus - rem) * l >= ux) {
-        best = T > 0.0 ? T : 1e-3;
+      if (T < top) continue;
+      const double h = rem > 0 ? (double)(int64_t)((T - top) / tx + 1e-6) : 0.0, l = (double)(int64_t)((T - low) / tx + 1e-6);
+      if (rem * h + (cus - rem) * l >= (double)ux) {
+        best = T;
         *heavy = (int)h;
         *light = (int)l;
         break;
       }
     }
+  }
   return best;
 }
 
@@ -625,16 +635,17 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most);
   const double rd = (double)N * D * 4e-6 / 5.0;            // us for dX's size in FP32 to memory
   double least = 0.0;
-  for (int64_t pieces = fewest; pieces <= (chunk > 0 ? fewest : fewest + 4) && pieces <= whole; ++pieces) {
+  const int64_t last = chunk > 0 || fewest == 1 ? fewest : fewest + 4;
+  for (int64_t pieces = fewest; pieces <= last && pieces <= whole; ++pieces) {
     const int64_t tiles = chunk > 0 ? most : ceil_div(whole, pieces), used = ceil_div(whole, tiles);
     const double logits = (double)ceil_div(row_tiles * tiles, cus) * (6.0 + D / 32) + 4.0;
     for (int64_t ws = 1; ws <= 16; ws *= 2) {
       if (ws > 1 && (!need_dw || ws * 2 > wst || tiles * dt * ws > 2 * cus)) break;
-      for (int64_t xs = 1; xs <= 16 || (xs <= 64 && row_tiles * dt * xs <= cus); xs = xs < 8 ? xs + 1 : xs + xs / 4) {
-        if (xs > 1 && (!need_dx || xs * 2 > tiles * 8)) break;
-        int h = 0, l = 0;
+      for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
+        if (xs > 1 && (!need_dx || xs * 2 > tiles * 8 || row_tiles * dt * xs > 2 * cus)) break;
+        int h, l;
         double us = products_time(tiles, wst, row_tiles, dt, ws, xs, used > 1, need_dw, need_dx, &h, &l) + logits + 4.0;
-        if (ws > 1) us += 4.0 + (double)(ws + 1) * tiles * TILE_M * D * 4e-6 / 5.0;
+        if (ws > 1) us += 2.0 + (double)(ws + 1) * tiles * TILE_M * D * 4e-6 / 5.0;
         us = us * (double)used + (double)xs * rd;
         if (least == 0.0 || us < least) {
           least = us;
@@ -699,15 +710,13 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     }
     hipLaunchKernelGGL(k_lin_products<Mul>, dim3(grid), dim3(LIN_THREADS), 0, st, p);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-    if (c.dW && p.w_slots > 1) {
-      hipLaunchKernelGGL(k_lin_sum, dim3(sum_grid(v1 - v0, c.D)), dim3(256), 0, st, p.wpart, p.cols * c.D, p.w_slots, v0,
-                         v1 - v0, c.D, (const float*)k.inv, p.dW);
-      if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-    }
-  }
-  if (c.dX) {
-    hipLaunchKernelGGL(k_lin_sum, dim3(sum_grid(c.N, c.D)), dim3(256), 0, st, (const float*)(ws + s.xpart), c.N * c.D,
-                       s.x_slots, (int64_t)0, c.N, c.D, (const float*)k.inv, OutArgs{c.dX, c.lddx, c.dx_type, 0});
+    // the runs of dW summed, and those of dX behind the last piece
+    SumArgs w{}, x{};
+    if (c.dW && p.w_slots > 1) w = SumArgs{p.wpart, p.cols * c.D, v0, v1 - v0, p.w_slots, c.D, p.dW};
+    if (c.dX && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.x_slots, c.D, OutArgs{c.dX, c.lddx, c.dx_type, 0}};
+    const unsigned wb = w.rows ? sum_grid(w.rows, c.D) : 0, xb = x.rows ? sum_grid(x.rows, c.D) : 0;
+    if (wb + xb == 0) continue;
+    hipLaunchKernelGGL(k_lin_sum, dim3(wb + xb), dim3(256), 0, st, w, x, (int)wb, (const float*)k.inv);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   }
   return ELMO_OK_;

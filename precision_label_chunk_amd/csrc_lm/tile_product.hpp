@@ -73,6 +73,14 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
+// Sixteen bytes a lane from `buf` at byte offset `off` to LDS at `to` + 16 lane (zeros past the buffer's end).
+// In assembly, for the compiler's own form makes every transposing LDS read behind it wait for all copies (the
+// loop over K-major operands took 1.08 us a stage, and 0.8 without these waits). No register receives
+// anything; wait_copies() counts the copies. Five wait states: an SGPR of `buf` may come from a vector instruction.
+__device__ __forceinline__ void copy16(__amdgpu_buffer_rsrc_t buf, int off, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(buf) : "memory", "m0");
+}
+
 // One operand's copies: ROWS of m or n per stage, THREADS threads.
 template <bool KM, int ROWS, int THREADS, int BYTES>
 struct StageCopy {
@@ -81,36 +89,41 @@ struct StageCopy {
   static constexpr int PER_ROW = ROWS * BYTES / 16;        // K-major: pieces per row of k
   int off;                                                 // byte offset of the thread's first piece
   int step;                                                // and of the next one from it
-  Operand o;
-  __device__ __forceinline__ void start(const Operand& op, int tid) {
-    o = op;
-    const int ld = (int)op.ld;
+  const char* at;                                          // the stage to be copied next
+  int64_t left, ld;                                        // K-major: its valid rows of k and those behind it
+  int cols, bytes;
+  __device__ __forceinline__ void start(const Operand& o, int tid) {
+    at = o.at;
+    ld = o.ld;
     if constexpr (KM) {
       const int k = tid / PER_ROW, c = (tid % PER_ROW) ^ km_swizzle(k);
-      off = k * ld + c * 16;
-      step = THREADS / PER_ROW * ld;
+      off = k * (int)ld + c * 16;
+      step = THREADS / PER_ROW * (int)ld;
+      left = o.rows;
+      cols = o.cols;
     } else {
       const int r = tid / 4, c = (tid % 4) ^ kc_swizzle(r);
-      off = r * ld + c * 16;
-      step = THREADS / 4 * ld;
+      off = r * (int)ld + c * 16;
+      step = THREADS / 4 * (int)ld;
+      const int rows = o.rows < ROWS ? (int)o.rows : ROWS;
+      bytes = rows > 0 ? (rows - 1) * (int)ld + STAGE_K : 0;
     }
   }
-  // the copies of stage s into the LDS bytes at `to` (a wave's part of each starts at wave * 1024)
-  __device__ __forceinline__ void copy(int s, char* to, int wave, bool live) const {
-    const char* base = o.at;
-    int64_t bytes;
+  // the copies of the next stage into the LDS bytes from `to` on (a wave's part of each starts at wave * 1024)
+  __device__ __forceinline__ void copy(uint32_t to, bool live) {
     if constexpr (KM) {
-      const int64_t left = o.rows - (int64_t)s * KROWS;
-      base += (int64_t)s * KROWS * o.ld;
-      bytes = left > 0 ? ((left < KROWS ? left : KROWS) - 1) * o.ld + o.cols : 0;
-    } else {
-      base += (int64_t)s * STAGE_K;
-      bytes = o.rows > 0 ? ((o.rows < ROWS ? o.rows : ROWS) - 1) * o.ld + STAGE_K : 0;
+      const int rows = left < KROWS ? (int)left : KROWS;
+      bytes = rows > 0 ? (rows - 1) * (int)ld + cols : 0;
     }
-    const auto buf = buffer_rsrc(base, (int)bytes & (live ? -1 : 0));
+    const auto buf = buffer_rsrc(at, live ? bytes : 0);
 #pragma unroll
-    for (int i = 0; i < COPIES; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (lds_char_t*)(to + i * THREADS * 16 + wave * 1024), 16, off + i * step, 0, 0, 0);
+    for (int i = 0; i < COPIES; ++i) copy16(buf, off + i * step, to + i * THREADS * 16);
+    if constexpr (KM) {
+      at += KROWS * ld;
+      left -= KROWS;
+    } else {
+      at += STAGE_K;
+    }
   }
 };
 
@@ -206,6 +219,7 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
   constexpr int COPIES = decltype(ca)::COPIES + decltype(cb)::COPIES;
   int lu = first, ls = 0, lstages;                         // the unit and stage to be copied next
   int fill = 0;                                            // and its buffer
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_char_t*)lds + wave * 1024;
   {
     const TileUnit t = job.unit(lu);
     ca.start(t.a, tid);
@@ -213,9 +227,9 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
     lstages = t.stages;
   }
   auto fetch = [&]() __attribute__((always_inline)) {
-    char* to = lds + fill * BUF;
-    ca.copy(ls, to, wave, lu < end);                       // (past the last unit: copies of nothing, for the count)
-    cb.copy(ls, to + A_BYTES, wave, lu < end);
+    const uint32_t to = lds0 + fill * BUF;
+    ca.copy(to, lu < end);                                 // (past the last unit: copies of nothing, for the count)
+    cb.copy(to + A_BYTES, lu < end);
     fill = fill + 1 == NBUF ? 0 : fill + 1;
     if (++ls == lstages) {
       ls = 0;
