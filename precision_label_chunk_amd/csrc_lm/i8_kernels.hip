@@ -276,20 +276,121 @@ __global__ __launch_bounds__(256) void k_i8_join(I8Args a) {
   }
 }
 
-// Up to 32 rows: weights straight from memory to the matrix cores. A wave takes 16 labels x all rows, 64 bytes
-// of K per product; KS waves of a block share a tile's K where there are few tiles.
+// Up to 32 rows: weights straight from memory to the matrix cores, 64 bytes of K per product, LT tiles of 16 labels a
+// wave against all rows.
 __device__ __forceinline__ i32x4_t mul_i8_16(i32x4_t a, i32x4_t b, i32x4_t c) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
+__device__ __forceinline__ void lds_barrier() {            // (loads to registers stay on their way)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Many labels: a block's 4 waves share the rows in LDS, PANEL features at a time, and its 128 labels leave through
+// LDS, 256 or 512 bytes of a row at a time. 3M labels x 768: 1 row 386 us (6.0 TB/s), 16 rows with FP32 results 490
+// (5.1; with the rows read from the caches and results in 64-byte pieces 615); 32 rows x 1M, 16-bit results 165 (277).
+constexpr int ROWS_LT = 2;
+template <typename E, int NT>
+__global__ __launch_bounds__(256) void k_i8_rows(I8Args a) {
+  constexpr int LT = ROWS_LT, LABELS = 64 * LT, PANEL = 1024, XP = PANEL + 16, ROWS = 16 * NT, AHEAD = 8 / LT;
+  typedef typename E::raw raw;
+  constexpr int PITCH = LABELS + 16 / (int)sizeof(raw);    // of the results (and XP of the rows): 16 bytes apart in banks
+  constexpr int BYTES = ROWS * XP > ROWS * PITCH * (int)sizeof(raw) ? ROWS * XP : ROWS * PITCH * (int)sizeof(raw);
+  __shared__ __attribute__((aligned(16))) char lds[BYTES];
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t l0 = (int64_t)blockIdx.x * LABELS;
+  const char* w[LT];
+  i32x4_t acc[LT][NT];
+#pragma unroll
+  for (int i = 0; i < LT; ++i) {                           // labels past the last are the last one again; not stored
+    const int64_t row = l0 + (wave * LT + i) * 16 + (lane & 15);
+    w[i] = a.W + (row < a.L ? row : a.L - 1) * a.D + 16 * (lane >> 4);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  }
+  const char* xs = lds + (lane & 15) * XP + 16 * (lane >> 4);
+  for (int d0 = 0; d0 < a.D; d0 += PANEL) {
+    const int width = a.D - d0 < PANEL ? a.D - d0 : PANEL, pieces = width / 16;
+    if (d0 > 0) lds_barrier();
+    for (int p = tid; p < ROWS * pieces; p += 256) {
+      const int r = p / pieces, c = p % pieces * 16;       // (rows past the last: zeros)
+      *(i32x4_t*)(lds + r * XP + c) = r < a.N ? *(const i32x4_t*)(a.X + (int64_t)r * a.D + d0 + c) : i32x4_t{0, 0, 0, 0};
+    }
+    auto load = [&](int s, auto count, i32x4_t (&f)[LT][AHEAD]) __attribute__((always_inline)) {
+      constexpr int C = count;
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+#pragma unroll
+        for (int i = 0; i < LT; ++i) f[i][k] = *(const i32x4_t*)(w[i] + d0 + (s + k) * 64);
+    };
+    auto mul = [&](int s, auto count, i32x4_t (&f)[LT][AHEAD]) __attribute__((always_inline)) {
+      constexpr int C = count;
+#pragma unroll
+      for (int k = 0; k < C; ++k)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const i32x4_t x = *(const i32x4_t*)(xs + j * 16 * XP + (s + k) * 64);
+#pragma unroll
+          for (int i = 0; i < LT; ++i) acc[i][j] = mul_i8_16(f[i][k], x, acc[i][j]);
+        }
+    };
+    const int steps = width / 64;
+    int s = 0;
+    i32x4_t f[LT][AHEAD];
+    constexpr std::integral_constant<int, AHEAD> many{};
+    constexpr std::integral_constant<int, 1> one{};
+    if (steps >= AHEAD) load(0, many, f);
+    lds_barrier();
+    for (; s + 2 * AHEAD <= steps; s += AHEAD) {           // the next ones are on their way while these are used
+      i32x4_t g[LT][AHEAD];
+      load(s + AHEAD, many, g);
+      mul(s, many, f);
+#pragma unroll
+      for (int i = 0; i < LT; ++i)
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) f[i][k] = g[i][k];
+    }
+    if (steps >= AHEAD) {
+      mul(s, many, f);
+      s += AHEAD;
+    }
+    for (; s < steps; ++s) {
+      load(s, one, f);
+      mul(s, one, f);
+    }
+  }
+  lds_barrier();
+#pragma unroll
+  for (int i = 0; i < LT; ++i) {
+    const int c = (wave * LT + i) * 16 + 4 * (lane >> 4);  // the lane's first of four labels in the block
+    const f32x4_t t = scales4(a.sw, l0 + c, a.L);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int r = 16 * j + (lane & 15);
+      const float f = r < a.N ? a.sx[r] : 0.0f;
+      float y[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = (float)acc[i][j][k] * f * t[k];
+      store_results<E>((raw*)lds + r * PITCH + c, 4, y);
+    }
+  }
+  lds_barrier();
+  constexpr int PIECES = LABELS / E::VEC;                  // of 16 bytes in a row
+#pragma unroll
+  for (int p = tid; p < ROWS * PIECES; p += 256) {
+    const int r = p / PIECES, c = p % PIECES * E::VEC;
+    if (r < a.N && l0 + c < a.L)
+      store_piece<E>((raw*)a.Y + r * a.ldy + l0 + c, a.L - l0 - c, *(const i32x4_t*)((raw*)lds + r * PITCH + c));
+  }
+}
+
+// Few labels: a block's KS waves share the K of one tile.
 template <typename E, int NT, int KS>
-__global__ __launch_bounds__(KS > 4 ? 64 * KS : 256) void k_i8_rows(I8Args a) {
-  constexpr int WAVES = KS > 4 ? KS : 4, TILES = WAVES / KS;
-  __shared__ i32x4_t sums[KS > 1 ? WAVES : 1][NT][64];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  const int64_t tile = (int64_t)blockIdx.x * TILES + wave / KS;
-  const int64_t v0 = tile * 16;
-  const int ks = wave % KS, steps = a.D / 64, s0 = (int)((int64_t)steps * ks / KS), s1 = (int)((int64_t)steps * (ks + 1) / KS);
-  // rows past the last read the last one again; their results are not stored
+__global__ __launch_bounds__(64 * KS) void k_i8_rows_split(I8Args a) {
+  __shared__ i32x4_t sums[KS][NT][64];
+  const int lane = (int)threadIdx.x & 63, ks = (int)threadIdx.x >> 6;
+  const int64_t v0 = (int64_t)blockIdx.x * 16;
+  const int steps = a.D / 64, s0 = steps * ks / KS, s1 = steps * (ks + 1) / KS;
+  // rows past the last are the last one again; their results are not stored
   const int64_t row = v0 + (lane & 15) < a.L ? v0 + (lane & 15) : a.L - 1;
   const char* w = a.W + row * a.D + 16 * (lane >> 4);
   const char* x[NT];
@@ -300,34 +401,34 @@ __global__ __launch_bounds__(KS > 4 ? 64 * KS : 256) void k_i8_rows(I8Args a) {
     x[j] = a.X + (n < a.N ? n : a.N - 1) * a.D + 16 * (lane >> 4);
     acc[j] = i32x4_t{0, 0, 0, 0};
   }
-  constexpr int AHEAD = 8 / NT;                            // products whose operands are on their way together
   auto steps_of = [&](int s, auto count) __attribute__((always_inline)) {
-    constexpr int C = count;
+    constexpr int C = count;                               // products whose operands are on their way together
     i32x4_t fw[C], fx[NT][C];
 #pragma unroll
     for (int k = 0; k < C; ++k) {
-      fw[k] = *(const i32x4_t*)(w + (int64_t)(s + k) * 64);
+      fw[k] = *(const i32x4_t*)(w + (s + k) * 64);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fx[j][k] = *(const i32x4_t*)(x[j] + (int64_t)(s + k) * 64);
+      for (int j = 0; j < NT; ++j) fx[j][k] = *(const i32x4_t*)(x[j] + (s + k) * 64);
     }
 #pragma unroll
     for (int k = 0; k < C; ++k)
 #pragma unroll
       for (int j = 0; j < NT; ++j) acc[j] = mul_i8_16(fw[k], fx[j][k], acc[j]);
   };
+  constexpr int AHEAD = 8 / NT;
   int s = s0;
   for (; s + AHEAD <= s1; s += AHEAD) steps_of(s, std::integral_constant<int, AHEAD>{});
-  for (; s < s1; ++s) steps_of(s, std::integral_constant<int, 1>{});
-  if constexpr (KS > 1) {
+  if (AHEAD > 4 && s + 4 <= s1) { steps_of(s, std::integral_constant<int, 4>{}); s += 4; }
+  if (s + 2 <= s1) { steps_of(s, std::integral_constant<int, 2>{}); s += 2; }
+  if (s < s1) steps_of(s, std::integral_constant<int, 1>{});
 #pragma unroll
-    for (int j = 0; j < NT; ++j) sums[wave][j][lane] = acc[j];
-    __syncthreads();
-    if (ks != 0) return;
+  for (int j = 0; j < NT; ++j) sums[ks][j][lane] = acc[j];
+  __syncthreads();
+  if (ks != 0) return;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll 5
-      for (int k = 1; k < KS; ++k) acc[j] += sums[wave + k][j][lane];
-  }
+    for (int k = 1; k < KS; ++k) acc[j] += sums[k][j][lane];
   const int64_t v = v0 + 4 * (lane >> 4);
   if (v >= a.L) return;
   const f32x4_t t = scales4(a.sw, v, a.L);
@@ -369,16 +470,23 @@ template <typename E>
 static int matmul_as(I8Args& a, hipStream_t st) {
   if (a.N <= I8_ROWS) {
     const int64_t tiles = ceil_div(a.L, 16), cus = device_cus();
-    // waves that share a tile: until there are 8 for every compute unit
-    const int ks = tiles >= 8 * cus ? 1 : tiles >= 2 * cus ? 4 : 16;
-    const unsigned grid = (unsigned)(ks == 1 ? ceil_div(tiles, 4) : tiles);
-#define ELMO_I8_ROWS(NT, KS) hipLaunchKernelGGL((k_i8_rows<E, NT, KS>), dim3(grid), dim3(KS > 4 ? 64 * KS : 256), 0, st, a)
-    if (a.N <= 16) {
-      if (ks == 1) ELMO_I8_ROWS(1, 1); else if (ks == 4) ELMO_I8_ROWS(1, 4); else ELMO_I8_ROWS(1, 16);
+    // Rows shared by a block: for labels that fill the device several times over, fewer of them where the rows fit
+    // one panel (131,072 labels, 16 rows x 768: 24 us against 30 split; 1 row x 4096: 113 against 90)
+    if (tiles >= 64 * cus || (tiles >= 16 * cus && a.D <= 1024)) {
+      const dim3 grid((unsigned)ceil_div(a.L, 64 * ROWS_LT));
+      if (a.N <= 16) hipLaunchKernelGGL((k_i8_rows<E, 1>), grid, dim3(256), 0, st, a);
+      else hipLaunchKernelGGL((k_i8_rows<E, 2>), grid, dim3(256), 0, st, a);
     } else {
-      if (ks == 1) ELMO_I8_ROWS(2, 1); else if (ks == 4) ELMO_I8_ROWS(2, 4); else ELMO_I8_ROWS(2, 16);
+      const dim3 grid((unsigned)tiles);
+#define ELMO_I8_SPLIT(NT, KS) hipLaunchKernelGGL((k_i8_rows_split<E, NT, KS>), grid, dim3(64 * KS), 0, st, a)
+      const bool few = tiles < 2 * cus;                    // (then 16 waves a tile fill it sooner than 4)
+      if (a.N <= 16) {
+        if (few) ELMO_I8_SPLIT(1, 16); else ELMO_I8_SPLIT(1, 4);
+      } else {
+        if (few) ELMO_I8_SPLIT(2, 16); else ELMO_I8_SPLIT(2, 4);
+      }
+#undef ELMO_I8_SPLIT
     }
-#undef ELMO_I8_ROWS
     return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
   }
   const int64_t units = (int64_t)a.row_tiles * a.label_tiles * a.slots, cus = device_cus();
