@@ -350,8 +350,8 @@ int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int6
  *   G[n, v] = p_v (dlse - sum_j dlogp_j) + sum_{j : ids_j = v} dlogp_j;  dX = G W;  dW = G^T X.
  * row_max and log_sum are elmo_linear_logprobs' outputs for the same X and W. The vocabulary goes in pieces
  * of `chunk` labels (rounded up to a multiple of 256; 0: the library's choice, about 2^26 / N): a piece's logits
- * are computed again and G held in the workspace in X's type, the one rounding below 32 bits, relative to
- * each element; sums are binary32. A label given more than once receives the sum of its gradients, a negative
+ * are computed again and G held in the workspace in X's type (for N <= 128 as the sum of two such numbers), the one
+ * rounding below 32 bits, relative to each element; sums are binary32. A label given more than once receives the sum of its gradients, a negative
  * id none. A row of nothing but -inf logits has G = 0; an id >= V makes G NaN in the whole row.
  *   dX       [N, D] of type `dx_type` (any), dW [V, D] of type `dw_type`, 16-byte aligned rows at pitches lddx,
  *            lddw; either may be NULL. accumulate: dW is added to, in binary32, and rounded once.
@@ -372,7 +372,8 @@ int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_
  *   X [N, D], W [L, D] int8 (any of -128 .. 127), row-major without gaps, 16-byte aligned; D % 64 == 0,
  *   64 <= D <= ELMO_MAX_I8_D. x_scales [N], w_scales [L] FP32. Y [N, L] of element type `ytype`, row n at Y + n ldy,
  *   any pitch and element alignment. 1 <= L < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). A NaN scale stays
- *   in its row or column.
+ *   in its row or column. The workspace holds the sums of runs of K where there are few results; its size is 0 where none is
+ *   needed (it may be NULL then), and for unsupported shapes.
  * elmo_i8_quantize makes such rows from x [N, D] (element type `type`, 16-byte aligned rows at pitch ldx):
  *   scale = max_k |x[k]| / 127, code = 127 x / max|x| to the nearest whole number, halves to the even one, of the
  *   exact quotient. A zero row has scale 0 and codes 0; a row with a NaN or an infinity has scale NaN and

@@ -639,15 +639,22 @@ def i8_matmul(X, x_scales, W, w_scales, out_dtype=torch.bfloat16, out=None, work
     _like("w_scales", w_scales, (L,), torch.float32, dev)
     if out is None:
         out = X.new_empty((N, L), dtype=out_dtype)
+        ldy = L
     elif tuple(out.shape) != (N, L) or out.device != dev:
         raise ValueError("out must be [N, L] on X's device")
-    e, ldy = _etype(out), _rows("out", out)[2]
+    else:
+        ldy = _rows("out", out)[2]
+    e = _etype(out)
     if L == 0:
         return out
-    workspace = _scratch(workspace, lib().elmo_i8_matmul_workspace_bytes(N, L, D) if N else 0, X)
-    _chk("elmo_i8_matmul", lib().elmo_i8_matmul(X.data_ptr(), x_scales.data_ptr(), W.data_ptr(), w_scales.data_ptr(), N, L, D,
-                                                out.data_ptr(), e, ldy, workspace.data_ptr(), workspace.numel(),
-                                                _stream_of(dev)))
+    k = lib()
+    need = k.elmo_i8_matmul_workspace_bytes(N, L, D)
+    if need or workspace is not None:
+        workspace = _scratch(workspace, need, X)
+    rc = k.elmo_i8_matmul(X.data_ptr(), x_scales.data_ptr(), W.data_ptr(), w_scales.data_ptr(), N, L, D, out.data_ptr(), e, ldy,
+                          _at(workspace), 0 if workspace is None else workspace.numel(), _stream_of(dev))
+    if rc:
+        raise ElmoError("elmo_i8_matmul", rc)
     return out
 
 

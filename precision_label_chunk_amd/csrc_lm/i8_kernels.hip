@@ -462,7 +462,7 @@ I8Layout i8_layout(int64_t N, int64_t L, int D) {
       s.slots = (int)ceil_div(all, s.per);
     }
   }
-  s.total = s.slots > 1 ? (size_t)s.slots * N * s.L4 * 4 : 256;
+  s.total = s.slots > 1 ? (size_t)s.slots * N * s.L4 * 4 : 0;
   return s;
 }
 

@@ -10,7 +10,9 @@
 // rounding below 32 bits: half a unit of its type per element, of its own size (c p of a label that was
 // not given, c p + g of one that was, added before it is rounded, so that a label of probability near 1
 // keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
-// a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38.
+// a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows, which leave
+// half of a tile empty, G is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average
+// their roundings, and a second product of the empty half costs nothing.
 #include "lm_kernels.hpp"
 #include "tile_product.hpp"
 
@@ -287,8 +289,18 @@ __device__ __forceinline__ int pack16(float lo, float hi) {
   }
 }
 
+// what rounding to 16 bits leaves of two values
+template <class Mul>
+__device__ __forceinline__ int rest16(float lo, float hi) {
+  const int w = pack16<Mul>(lo, hi);
+  float f[8];
+  std::conditional_t<std::is_same_v<Mul, MulF16>, ElemF16, ElemBF16>::widen(i32x4_t{w, 0, 0, 0}, f);
+  return pack16<Mul>(lo - f[0], hi - f[1]);
+}
+
 struct GradArgs {
   LogitTiles t;
+  int planes;                                              // 2: G as two numbers
   const int32_t* ids; int M;
   const float2* coef; const float* up;
   char* G; int64_t ldg;                                    // [N] rows of the piece's labels; bytes
@@ -351,6 +363,11 @@ struct GradJob : GradArgs {
       put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
         if (r0 + row < t.N) *(i32x4_t*)(G + (r0 + row) * ldg + 2 * col0 + 16 * c) = x;
       });
+      if (planes == 1) continue;
+      pieces16(acc, j, v, [](float lo, float hi) { return rest16<Mul>(lo, hi); });
+      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+        if (r0 + row < t.N) *(i32x4_t*)(G + (t.N + r0 + row) * ldg + 2 * col0 + 16 * c) = x;
+      });
     }
     return n0 + 64 <= t.N;
   }
@@ -372,6 +389,7 @@ struct ProductArgs {
   const char* W; int64_t ldw;
   const char* G; int64_t ldg;
   int64_t N, v0, v1, cols;                                 // cols: the piece's labels, a multiple of 256
+  int planes;
   int D, d_tiles, row_tiles;
   const float* inv;
   // dW: the tokens in w_slots runs of w_per; one run goes to the result, several to `wpart`
@@ -451,7 +469,10 @@ struct WeightJob : ProductArgs {
     const int64_t t0 = slot * w_per, left = N - t0, rows = left < w_per ? left : w_per;
     const int d0 = dt * TILE_M, v = vt * LIN_TN;
     const int dc = D - d0 < TILE_M ? D - d0 : TILE_M;
-    return {{X + t0 * ldx + 2 * d0, ldx, rows, 2 * dc}, {G + t0 * ldg + 2 * (int64_t)v, ldg, rows, 2 * LIN_TN}, (int)((rows + 31) / 32)};
+    // (two planes come with one run: X's rows with the first, then again with the second)
+    const int stages = (int)((rows + 31) / 32);
+    const char *x = X + t0 * ldx + 2 * d0, *g = G + t0 * ldg + 2 * (int64_t)v;
+    return {{x, ldx, rows, 2 * dc, stages, x}, {g, ldg, rows, 2 * LIN_TN, stages, g + N * ldg}, planes * stages};
   }
   __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int dt, vt, slot;
@@ -476,12 +497,13 @@ struct FeatureJob : ProductArgs {
     const int64_t c0 = slot * x_per, n = (int64_t)nt * LIN_TN;
     const int64_t left = cols - c0, len = left < x_per ? left : x_per;
     const int d0 = dt * TILE_M, dc = D - d0 < TILE_M ? D - d0 : TILE_M;
-    return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, N - n, 0}, (int)(len / 32)};
+    return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, planes * N - n, 0}, (int)(len / 32)};
   }
   __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
     int dt, nt, slot;
     place(u, dt, nt, slot);
-    return store_tile(OutArgs{xpart + (int64_t)slot * N * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * LIN_TN + 64 * wn, N,
+    const int64_t rows = planes * N;
+    return store_tile(OutArgs{xpart + slot * rows * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * LIN_TN + 64 * wn, rows,
                dt * TILE_M + 128 * wm, D, lane, lds);
   }
 };
@@ -632,7 +654,8 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   int64_t most = chunk > 0 ? ceil_div(chunk, TILE_M) : (int64_t(1) << 27) / N / TILE_M;
   most = most < 1 ? 1 : (most > whole ? whole : most);
   if (most > MAX_PIECE / TILE_M) most = MAX_PIECE / TILE_M;
-  const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most);
+  s.planes = 2 * N <= LIN_TN ? 2 : 1;
+  const int64_t wst = s.planes * ceil_div(N, 32), fewest = ceil_div(whole, most);
   const double rd = (double)N * D * 4e-6 / 5.0;            // us for dX's size in FP32 to memory
   double least = 0.0;
   const int64_t last = chunk > 0 || fewest == 1 ? fewest : fewest + 4;
@@ -640,7 +663,7 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
     const int64_t tiles = chunk > 0 ? most : ceil_div(whole, pieces), used = ceil_div(whole, tiles);
     const double logits = (double)ceil_div(row_tiles * tiles, cus) * (6.0 + D / 32) + 4.0;
     for (int64_t ws = 1; ws <= 16; ws *= 2) {
-      if (ws > 1 && (!need_dw || ws * 2 > wst || tiles * dt * ws > 2 * cus)) break;
+      if (ws > 1 && (!need_dw || s.planes > 1 || ws * 2 > wst || tiles * dt * ws > 2 * cus)) break;
       for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
         if (xs > 1 && (!need_dx || xs * 2 > tiles * 8 || row_tiles * dt * xs > 2 * cus)) break;
         int h, l;
@@ -656,15 +679,15 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   }
   s.x_per = ceil_div(s.piece / 32, s.x_slots) * 32;
   s.x_slots = (int)ceil_div(s.piece, s.x_per);
-  s.w_per = ceil_div(wst, s.w_slots) * 32;
+  s.w_per = ceil_div(ceil_div(N, 32), s.w_slots) * 32;
   s.w_slots = (int)ceil_div(N, s.w_per);
   size_t at = 0;
   s.most = at; at += up256(256 * 8);
   s.inv = at; at += 256;
   s.coef = at; at += up256((size_t)N * 8);
   s.up = at; at += up256((size_t)N * (M > 0 ? M : 1) * 4);
-  s.G = at; at += up256((size_t)N * s.piece * 2);
-  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * N * D * 4);
+  s.G = at; at += up256((size_t)s.planes * N * s.piece * 2);
+  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * s.planes * N * D * 4);
   s.wpart = at; if (need_dw && s.w_slots > 1) at += up256((size_t)s.w_slots * s.piece * D * 4);
   s.total = at;
   return s;
@@ -686,12 +709,12 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     const int64_t v1 = v0 + s.piece < c.V ? v0 + s.piece : c.V;
     GradArgs g{};
     g.t = tiles_of(c.X, c.ldx, c.W, c.ldw, c.N, v0, v1, c.D);
-    g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.G = ws + s.G; g.ldg = 2 * s.piece;
+    g.planes = s.planes; g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.G = ws + s.G; g.ldg = 2 * s.piece;
     hipLaunchKernelGGL(k_lin_grad_logits<Mul>, dim3(blocks_for((int64_t)g.t.row_tiles * g.t.label_tiles)), dim3(LIN_THREADS), 0, st, g);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
     ProductArgs p{};
     p.X = (const char*)c.X; p.ldx = 2 * c.ldx; p.W = (const char*)c.W; p.ldw = 2 * c.ldw; p.G = ws + s.G; p.ldg = 2 * s.piece;
-    p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, TILE_M); p.inv = k.inv;
+    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, TILE_M); p.inv = k.inv;
     p.cols = ceil_div(v1 - v0, TILE_M) * TILE_M;
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
@@ -705,7 +728,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
       p.x_heavy = 0;
       p.x_light = 1;
     } else {
-      products_time(p.cols / TILE_M, ceil_div(c.N, 32), p.row_tiles, p.d_tiles, p.w_slots, p.x_slots, s.piece < c.V, c.dW != nullptr,
+      products_time(p.cols / TILE_M, s.planes * ceil_div(c.N, 32), p.row_tiles, p.d_tiles, p.w_slots, p.x_slots, s.piece < c.V, c.dW != nullptr,
                     c.dX != nullptr, &p.x_heavy, &p.x_light);
     }
     hipLaunchKernelGGL(k_lin_products<Mul>, dim3(grid), dim3(LIN_THREADS), 0, st, p);
@@ -713,7 +736,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     // the runs of dW summed, and those of dX behind the last piece
     SumArgs w{}, x{};
     if (c.dW && p.w_slots > 1) w = SumArgs{p.wpart, p.cols * c.D, v0, v1 - v0, p.w_slots, c.D, p.dW};
-    if (c.dX && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.x_slots, c.D, OutArgs{c.dX, c.lddx, c.dx_type, 0}};
+    if (c.dX && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.planes * s.x_slots, c.D, OutArgs{c.dX, c.lddx, c.dx_type, 0}};
     const unsigned wb = w.rows ? sum_grid(w.rows, c.D) : 0, xb = x.rows ? sum_grid(x.rows, c.D) : 0;
     if (wb + xb == 0) continue;
     hipLaunchKernelGGL(k_lin_sum, dim3(wb + xb), dim3(256), 0, st, w, x, (int)wb, (const float*)k.inv);

@@ -245,9 +245,8 @@ int elmo_i8_matmul(const int8_t* X, const float* x_scales, const int8_t* W, cons
   if (!X || !W || !x_scales || !w_scales || !Y || !aligned16(X) || !aligned16(W) || !aligned_to(x_scales, 4) ||
       !aligned_to(w_scales, 4) || !aligned_to(Y, type_bytes(ytype)))
     return ELMO_EINVAL;
-  if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
   const elmo::I8Layout s = elmo::i8_layout(N, L, D);
-  if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
+  if (s.total > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < s.total)) return ELMO_EWORKSPACE;
   return elmo::run_i8_matmul(X, x_scales, W, w_scales, N, L, D, Y, ytype, ldy, s, workspace, (hipStream_t)stream);
 }
 

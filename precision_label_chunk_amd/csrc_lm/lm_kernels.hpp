@@ -44,6 +44,7 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
 struct LinearGradLayout {
   int64_t piece, x_per, w_per;                             // labels per piece; labels / tokens per run
   int x_slots, w_slots;                                    // runs
+  int planes;                                              // 16-bit numbers whose sum holds an element of G
   size_t most, inv, coef, up, G, xpart, wpart, total;
 };
 struct LinearGradCall {

@@ -55,8 +55,9 @@ struct MulI8 {
 // One operand of a tile: where its first stage starts, and how far it reaches. K-contiguous: `rows` valid
 // rows (of m or n) at pitch `ld` bytes. K-major: `rows` valid rows of k, of which `cols` bytes belong to
 // the tile and the matrix. What lies outside reads as zero, or as other elements of the matrix where it
-// reaches only sums that nobody uses.
-struct Operand { const char* at; int64_t ld; int64_t rows; int cols; };
+// reaches only sums that nobody uses. A K-major operand may go on behind `turn` stages at `second`, with the same
+// rows and columns.
+struct Operand { const char* at; int64_t ld; int64_t rows; int cols; int turn = 0; const char* second = nullptr; };
 struct TileUnit { Operand a, b; int stages; };
 
 constexpr int TILE_M = 256, STAGE_K = 64;                  // rows of A per tile; bytes of K per stage
@@ -92,6 +93,7 @@ struct StageCopy {
   const char* at;                                          // the stage to be copied next
   int64_t left, ld;                                        // K-major: its valid rows of k and those behind it
   int cols, bytes;
+  int turn; const char* second; int64_t rows;              // K-major: stages up to the second part, its place
   __device__ __forceinline__ void start(const Operand& o, int tid) {
     at = o.at;
     ld = o.ld;
@@ -99,21 +101,23 @@ struct StageCopy {
       const int k = tid / PER_ROW, c = (tid % PER_ROW) ^ km_swizzle(k);
       off = k * (int)ld + c * 16;
       step = THREADS / PER_ROW * (int)ld;
-      left = o.rows;
+      left = rows = o.rows;
       cols = o.cols;
+      turn = o.turn;
+      second = o.second;
     } else {
       const int r = tid / 4, c = (tid % 4) ^ kc_swizzle(r);
       off = r * (int)ld + c * 16;
       step = THREADS / 4 * (int)ld;
-      const int rows = o.rows < ROWS ? (int)o.rows : ROWS;
-      bytes = rows > 0 ? (rows - 1) * (int)ld + STAGE_K : 0;
+      const int n = o.rows < ROWS ? (int)o.rows : ROWS;
+      bytes = n > 0 ? (n - 1) * (int)ld + STAGE_K : 0;
     }
   }
   // the copies of the next stage into the LDS bytes from `to` on (a wave's part of each starts at wave * 1024)
   __device__ __forceinline__ void copy(uint32_t to, bool live) {
     if constexpr (KM) {
-      const int rows = left < KROWS ? (int)left : KROWS;
-      bytes = rows > 0 ? (rows - 1) * (int)ld + cols : 0;
+      const int n = left < KROWS ? (int)left : KROWS;
+      bytes = n > 0 ? (n - 1) * (int)ld + cols : 0;
     }
     const auto buf = buffer_rsrc(at, live ? bytes : 0);
 #pragma unroll
@@ -121,6 +125,10 @@ struct StageCopy {
     if constexpr (KM) {
       at += KROWS * ld;
       left -= KROWS;
+      if (--turn == 0) {
+        at = second;
+        left = rows;
+      }
     } else {
       at += STAGE_K;
     }

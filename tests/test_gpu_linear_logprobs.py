@@ -7,7 +7,8 @@ parts of 64 and a tree, at most c = 64 + V / 8192 + 24 additions deep; each term
 exponent and the exponential's 2 u (as for the operator on given logits: weighted by the terms the mean of |y| is at
 most log2 V + 2), so log s is off by R = (c + 3 (log2 V + 3) + 8) u + 2 E.
 Gradient: G = c p + g carries p's R + (3 |y| + 8) u + 2 E relative and a few roundings of c and g (8 u of |c| p +
-sum |g|), then half a unit h of its own type; dX and dW are binary32 sums of exact products of it, off by at most
+sum |g|), then half a unit h of its own type (h^2 up to 128 rows, where a second number of the type holds what the first
+leaves); dX and dW are binary32 sums of exact products of it, off by at most
 K u sum |G W|, and round once to their type: half a unit relative, and for FP16 results at least 2^-25, half the
 spacing 2^-24 of its numbers below 2^-14."""
 import math
@@ -99,7 +100,7 @@ def _gradients(X, W, ids, up, dlse):
         on = torch.zeros_like(G)
         on.scatter_(1, i[:, j:j + 1].clamp(min=0), g[:, j:j + 1])
         G, A = G + on, A + on.abs()
-    h = HALF[X.dtype]
+    h = HALF[X.dtype] ** (2 if N <= 128 else 1)
     off = h * G.abs() + (rough + 8 * U * A) * (1 + h)
     if X.dtype == HF:                        # below its normal numbers FP16 is off by 2^-25 of the scaled value
         off = off + 2.0**-25 * 2.0**-13 * 2 * big.max()
