@@ -337,10 +337,10 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
  * -inf, log_sum 0 and its labels' log probabilities -inf; a NaN or +inf logit makes log_sum and logp of its
  * row NaN (row_max skips NaN). Results repeat bit for bit on one device.
  * D % 32 == 0, 32 <= D <= ELMO_MAX_LINEAR_D; 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). The workspace
- * takes 8 bytes for 128 logits.
+ * takes 8 bytes for 128 logits (for 32 where there are few).
  */
 #define ELMO_MAX_LINEAR_D 65536
-size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int M);
+size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int D, int M);
 int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
                          const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, void* workspace,
                          size_t workspace_bytes, void* stream);

@@ -97,7 +97,7 @@ def lib():
         L.elmo_ckpt8_weight_grad_workspace_bytes.restype = sz
         L.elmo_ckpt8_weight_grad.argtypes = [P, i64, P, P, i64, i32, i32, P, i32, P, sz, P]
         L.elmo_ckpt8_weight_grad.restype = i32
-        L.elmo_linear_logprobs_workspace_bytes.argtypes = [i64, i64, i32]
+        L.elmo_linear_logprobs_workspace_bytes.argtypes = [i64, i64, i32, i32]
         L.elmo_linear_logprobs_workspace_bytes.restype = sz
         L.elmo_linear_logprobs.argtypes = [P, P, i32, i64, i64, i32, i64, i64, P, i32, P, P, P, P, sz, P]
         L.elmo_linear_logprobs.restype = i32
@@ -566,7 +566,7 @@ def linear_logprobs(X, W, ids=None, workspace=None) -> LinearLogProbs:
     e, N, V, D, M, ldx, ldw = _linear(X, W, ids)
     logp = X.new_empty((N, M), dtype=torch.float32)
     row_max, log_sum = X.new_empty((2, N), dtype=torch.float32).unbind(0)
-    need = lib().elmo_linear_logprobs_workspace_bytes(N, V, M) if N else 0
+    need = lib().elmo_linear_logprobs_workspace_bytes(N, V, D, M) if N else 0
     workspace = _scratch(workspace, need, X)
     _chk("elmo_linear_logprobs", lib().elmo_linear_logprobs(
         X.data_ptr(), W.data_ptr(), e, N, V, D, ldx, ldw, _at(ids) if M else None, M, _at(logp) if M else None,

@@ -4,12 +4,9 @@
 // y[n, v] = sx[n] sw[v] sum_k x[n, k] w[v, k]: the sum is exact (D <= 65536 products of at most 2^14 stay
 // within 2^30), so its split along K and its order change nothing; what rounds is its conversion, the two
 // scales and the result.
-#include "lm_kernels.hpp"
-#include "tile_product.hpp"
+#include "tile_shapes.hpp"
 
 namespace elmo {
-
-static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---- quantisation ----------------------------------------------------------------------------------
 // q = the whole number nearest to 127 x / top (halves to even), scale = top / 127. The quotient comes from
@@ -176,9 +173,9 @@ __device__ __forceinline__ f32x4_t scales4(const float* sw, int64_t v, int64_t L
   return s;
 }
 
-constexpr int I8_WN = 4, I8_NBUF = 3, I8_THREADS = 128 * I8_WN, I8_TN = 64 * I8_WN, I8_GROUP = 8;
+constexpr int I8_GROUP = 8;
 
-template <typename E, bool PARTS>
+template <typename E, bool PARTS, class S>
 struct I8Job : I8Args {
   __device__ __forceinline__ void place(int u, int& lt, int& nt, int& slot) const {
     const int tiles = row_tiles * label_tiles;
@@ -192,24 +189,24 @@ struct I8Job : I8Args {
   __device__ __forceinline__ TileUnit unit(int u) const {
     int lt, nt, slot;
     place(u, lt, nt, slot);
-    const int64_t l = (int64_t)lt * TILE_M, n = (int64_t)nt * I8_TN;
+    const int64_t l = (int64_t)lt * S::M, n = (int64_t)nt * S::N;
     const int s0 = slot * per, all = D / STAGE_K, len = all - s0 < per ? all - s0 : per;
     return {{W + l * D + s0 * STAGE_K, D, L - l, 0}, {X + n * D + s0 * STAGE_K, D, N - n, 0}, len};
   }
-  static constexpr int STORES = PARTS || E::VEC == 4 ? 32 : 16;
-  __device__ __forceinline__ bool finish(int u, i32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
+  static constexpr int STORES = S::NF * S::PIECES / (PARTS || E::VEC == 4 ? 1 : 2);
+  __device__ __forceinline__ bool finish(int u, i32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int lt, nt, slot;
     place(u, lt, nt, slot);
-    const int64_t v0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * I8_TN + 64 * wn;
+    const int64_t v0 = (int64_t)lt * S::M + S::WM_ROWS * wm, n0 = (int64_t)nt * S::N + S::WN_ROWS * wn;
     const int64_t left = L - v0;                           // (scales past the last label read as zero)
-    const auto scales = buffer_rsrc(PARTS ? nullptr : sw + v0, PARTS ? 0 : 4 * (int)(left < 0 ? 0 : left < 128 ? left : 128));
+    const auto scales = buffer_rsrc(PARTS ? nullptr : sw + v0, PARTS ? 0 : 4 * (int)(left < 0 ? 0 : left < S::WM_ROWS ? left : S::WM_ROWS));
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NF; ++j) {
       const int64_t r0 = n0 + 32 * j;
       if constexpr (!PARTS) {                              // the results take the sums' place
         const float s = r0 + (lane & 31) < N ? sx[r0 + (lane & 31)] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < S::MF; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const i32x4_t t = buffer_load16(scales, 16 * (8 * i + 2 * q + (lane >> 5)));
@@ -220,43 +217,38 @@ struct I8Job : I8Args {
       if constexpr (PARTS || E::VEC == 4) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          i32x4_t v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const i32x16_t& a = acc[2 * h + k / 4][j];
-            const int q = 4 * (k % 4);
-            v[k] = i32x4_t{a[q], a[q + 1], a[q + 2], a[q + 3]};
-          }
-          put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
-            const int64_t n = r0 + row, l = v0 + 64 * h + 4 * c;
+          i32x4_t v[2 * S::MF];
+          pieces32<S::MF>(j, h, v, [&](int i, int jj, int r) { return (int)acc[i][jj][r]; });
+          put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
+            const int64_t n = r0 + row, l = v0 + 16 * S::MF * h + 4 * c;
             if (n >= N || l >= L) return;
             if constexpr (PARTS) *(i32x4_t*)(part + ((int64_t)slot * N + n) * L4 + l) = x;
             else store_piece<E>((typename E::raw*)Y + n * ldy + l, L - l, x);
           });
         }
       } else {
-        i32x4_t v[8];
-        pieces16(acc, j, v, [](int lo, int hi) {
+        i32x4_t v[2 * S::MF];
+        pieces16<S::MF>(acc, j, v, [](int lo, int hi) {
           const float z[8] = {u2f((uint32_t)lo), u2f((uint32_t)hi), 0, 0, 0, 0, 0, 0};
           return E::narrow(z)[0];
         });
-        put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+        put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
           const int64_t n = r0 + row, l = v0 + 8 * c;
           if (n < N && l < L) store_piece<E>((typename E::raw*)Y + n * ldy + l, L - l, x);
         });
       }
     }
-    return n0 + 64 <= N && left >= 128;
+    return n0 + S::WN_ROWS <= N && left >= S::WM_ROWS;
   }
 };
 
-template <typename E, bool PARTS>
-__global__ __launch_bounds__(I8_THREADS, 2) void k_i8_tiles(I8Args a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<I8_WN, I8_NBUF, true>()];
-  I8Job<E, PARTS> job;
+template <typename E, bool PARTS, class S>
+__global__ __launch_bounds__(S::THREADS, S::WAVES) void k_i8_tiles(I8Args a) {
+  __shared__ __attribute__((aligned(1024))) char lds[S::lds(true)];
+  I8Job<E, PARTS, S> job;
   (I8Args&)job = a;
   const UnitRange r = xcd_units(a.label_tiles * a.row_tiles * a.slots);
-  tile_stream<MulI8, false, false, I8_WN, I8_NBUF>(job, r.first, r.step, r.end, lds);
+  tile_stream<MulI8, false, false, S>(job, r.first, r.step, r.end, lds);
 }
 
 // the runs' sums joined, scaled and rounded
@@ -447,27 +439,38 @@ __global__ __launch_bounds__(64 * KS) void k_i8_rows_split(I8Args a) {
 
 constexpr int I8_ROWS = 32;                                // rows that the streaming kernel takes
 
+// The tile shape and the runs of K by the time they are expected to take; a run keeps 4 stages.
 I8Layout i8_layout(int64_t N, int64_t L, int D) {
   I8Layout s{};
   s.slots = 1;
   s.per = D / STAGE_K;
   s.L4 = ceil_div(L, 4) * 4;
   if (N > I8_ROWS) {
-    // fewer tiles than compute units: runs of K, as long as one keeps 8 stages
-    const int64_t tiles = ceil_div(L, TILE_M) * ceil_div(N, I8_TN), cus = device_cus(), all = D / STAGE_K;
-    int64_t k = cus / tiles;
-    if (k > all / 8) k = all / 8;
-    if (k > 1) {
-      s.per = (int)ceil_div(all, k);
-      s.slots = (int)ceil_div(all, s.per);
+    const int64_t all = D / STAGE_K;
+    const int cus = device_cus();
+    double least = 0.0;
+    for (int k = 0; k < SHAPE_COUNT; ++k) {
+      const ShapeCost& c = SHAPES[k];
+      const int64_t tiles = ceil_div(L, c.size) * ceil_div(N, c.size);
+      for (int64_t slots = 1; slots <= 64; slots *= 2) {
+        if (slots > 1 && (slots * 4 > all || tiles * slots > 2 * (int64_t)cus * c.blocks)) break;
+        double us = units_time(c, tiles * slots, ceil_div(all, slots), cus);
+        if (slots > 1) us += 3.0 + (double)(2 * slots) * N * L * 4e-6 / 5.0;
+        if (least == 0.0 || us < least) {
+          least = us;
+          s.shape = k;
+          s.per = (int)ceil_div(all, slots);
+        }
+      }
     }
+    s.slots = (int)ceil_div(all, s.per);
   }
   s.total = s.slots > 1 ? (size_t)s.slots * N * s.L4 * 4 : 0;
   return s;
 }
 
 template <typename E>
-static int matmul_as(I8Args& a, hipStream_t st) {
+static int matmul_as(I8Args& a, int shape, hipStream_t st) {
   if (a.N <= I8_ROWS) {
     const int64_t tiles = ceil_div(a.L, 16), cus = device_cus();
     // Rows shared by a block: for labels that fill the device several times over, fewer of them where the rows fit
@@ -489,15 +492,15 @@ static int matmul_as(I8Args& a, hipStream_t st) {
     }
     return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
   }
-  const int64_t units = (int64_t)a.row_tiles * a.label_tiles * a.slots, cus = device_cus();
-  const dim3 grid((unsigned)(units < cus ? units : cus));
-  if (a.slots == 1) {
-    hipLaunchKernelGGL((k_i8_tiles<E, false>), grid, dim3(I8_THREADS), 0, st, a);
-    return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
-  }
-  hipLaunchKernelGGL((k_i8_tiles<ElemF32, true>), grid, dim3(I8_THREADS), 0, st, a);
+  const dim3 grid(blocks_for(shape, (int64_t)a.row_tiles * a.label_tiles * a.slots, device_cus()));
+  with_shape(shape, [&](auto tiles) {
+    typedef decltype(tiles) S;
+    if (a.slots == 1) hipLaunchKernelGGL((k_i8_tiles<E, false, S>), grid, dim3(S::THREADS), 0, st, a);
+    else hipLaunchKernelGGL((k_i8_tiles<ElemF32, true, S>), grid, dim3(S::THREADS), 0, st, a);
+  });
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-  const int64_t want = ceil_div(a.N * (a.L4 / 4), 256), cap = 16 * cus;
+  if (a.slots == 1) return ELMO_OK_;
+  const int64_t want = ceil_div(a.N * (a.L4 / 4), 256), cap = 16 * (int64_t)device_cus();
   hipLaunchKernelGGL(k_i8_join<E>, dim3((unsigned)(want < cap ? want : cap)), dim3(256), 0, st, a);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
@@ -506,11 +509,11 @@ int run_i8_matmul(const int8_t* X, const float* sx, const int8_t* W, const float
                   int ytype, int64_t ldy, const I8Layout& s, void* workspace, hipStream_t st) {
   I8Args a{};
   a.X = (const char*)X; a.W = (const char*)W; a.sx = sx; a.sw = sw; a.Y = Y; a.ldy = ldy; a.N = N; a.L = L; a.D = D;
-  a.row_tiles = (int)ceil_div(N, I8_TN); a.label_tiles = (int)ceil_div(L, TILE_M); a.slots = s.slots; a.per = s.per;
+  a.row_tiles = (int)ceil_div(N, SHAPES[s.shape].size); a.label_tiles = (int)ceil_div(L, SHAPES[s.shape].size); a.slots = s.slots; a.per = s.per;
   a.part = (int*)workspace; a.L4 = s.L4;
-  if (ytype == T_F32_) return matmul_as<ElemF32>(a, st);
-  if (ytype == T_BF16_) return matmul_as<ElemBF16>(a, st);
-  return matmul_as<ElemF16>(a, st);
+  if (ytype == T_F32_) return matmul_as<ElemF32>(a, s.shape, st);
+  if (ytype == T_BF16_) return matmul_as<ElemBF16>(a, s.shape, st);
+  return matmul_as<ElemF16>(a, s.shape, st);
 }
 
 }  // namespace elmo

@@ -1,25 +1,22 @@
 // Log probabilities of given labels straight from features and weights, and the gradient: softmax cross
 // entropy of a linear head whose logits are never kept.
 //
-// Forward: Z = X W^T tile by tile (256 labels x 256 rows); each wave reduces its 128 labels x 64 rows to a
-// maximum and a sum of e^(z - max) per row, 8 bytes for 128 logits, and picks the given labels' logits
-// out. A second kernel joins the parts of a row.
+// Forward: Z = X W^T tile by tile (256 labels x 256 rows, or less); each wave reduces its labels to a maximum and a
+// sum of e^(z - max) per row (8 bytes for 128 logits) and picks the given labels' logits out. A second kernel joins the parts of a row.
 //
 // Backward, a piece of the vocabulary at a time: the piece's logits again, as G = c_n p + (given labels'
 // gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch. G is the one
 // rounding below 32 bits: half a unit of its type per element, of its own size (c p of a label that was
 // not given, c p + g of one that was, added before it is rounded, so that a label of probability near 1
 // keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
-// a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows, which leave
-// half of a tile empty, G is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average
-// their roundings, and a second product of the empty half costs nothing.
-#include "lm_kernels.hpp"
-#include "tile_product.hpp"
+// a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows G
+// is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average their roundings, and
+// memory bounds such products.
+#include "tile_shapes.hpp"
 
 namespace elmo {
 
 constexpr float L2E = 1.44269502162933349609375f;          // FP32(log2 e)
-constexpr int LIN_WN = 4, LIN_NBUF = 3, LIN_THREADS = 128 * LIN_WN, LIN_TN = 64 * LIN_WN;
 constexpr int COEF_THREADS = 1024;
 constexpr int GROUP = 8;                                   // label tiles that are taken together over the rows
 
@@ -35,58 +32,63 @@ struct LogitTiles {
     nt = r / wide;
     lt = g * GROUP + r % wide;
   }
+  template <class S>
   __device__ __forceinline__ TileUnit unit(int u) const {
     int lt, nt;
     place(u, lt, nt);
-    const int64_t l = v0 + (int64_t)lt * TILE_M, n = (int64_t)nt * LIN_TN;
+    const int64_t l = v0 + (int64_t)lt * S::M, n = (int64_t)nt * S::N;
     return {{W + l * ldw, ldw, v1 - l, 0}, {X + n * ldx, ldx, N - n, 0}, stages};
   }
 };
 
-// where a wave's tile of labels from l0 on has a given label: 32 i + 8 (r / 4) + r % 4 of the lane that
+// where a wave's ROWS labels from l0 on have a given label: 32 i + 8 (r / 4) + r % 4 of the lane that
 // holds it, else negative
+template <int ROWS>
 __device__ __forceinline__ int given_place(int id, int64_t l0, int64_t v1, int half) {
   const int64_t at = (int64_t)id - l0;
-  if (at < 0 || at >= 128 || id >= v1 || (((int)at >> 2) & 1) != half) return -1;
+  if (at < 0 || at >= ROWS || id >= v1 || (((int)at >> 2) & 1) != half) return -1;
   return (int)at - 4 * half;
 }
 
 struct StatArgs {
   LogitTiles t;
   const int32_t* ids; int M;
-  float2* part;                                            // [2 label tiles][N]: maximum, sum
+  float2* part;                                            // [parts of 32 MF labels][N]: maximum, sum
   float* given;                                            // [N][M]: logits of the given labels
 };
 
+template <class S>
 struct StatJob : StatArgs {
-  static constexpr int STORES = 2;
-  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
-  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
+  static constexpr int STORES = S::NF;
+  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit<S>(u); }
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int lt, nt;
     t.place(u, lt, nt);
-    const int64_t l0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
+    const int64_t l0 = (int64_t)lt * S::M + S::WM_ROWS * wm, n0 = (int64_t)nt * S::N + S::WN_ROWS * wn;
     const int half = lane >> 5;
     const int64_t left = t.v1 - l0;                        // (wave-uniform)
-    int64_t n[2];
-    int first[2];
+    int64_t n[S::NF];
+    int first[S::NF];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NF; ++j) {
       n[j] = n0 + 32 * j + (lane & 31);
       first[j] = M > 0 && n[j] < t.N ? ids[n[j] * M] : -1;
     }
-    if (left < 128) {
+    if (left < S::WM_ROWS) {
       const int mine = (int)(left < -128 ? -128 : left) - 4 * half;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::MF; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (32 * i + 8 * (r / 4) + r % 4 >= mine) acc[i][0][r] = acc[i][1][r] = -__builtin_inff();
+          if (32 * i + 8 * (r / 4) + r % 4 >= mine) 
+#pragma unroll
+            for (int j = 0; j < S::NF; ++j) acc[i][j][r] = -__builtin_inff();
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NF; ++j) {
       float top = -__builtin_inff();
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::MF; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -95,7 +97,7 @@ struct StatJob : StatArgs {
       const float b = ref * L2E, rest = __builtin_fmaf(ref, L2E, -b);
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < S::MF; ++i) {
         float s = 0.0f;
 #pragma unroll
         for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -b));
@@ -106,12 +108,12 @@ struct StatJob : StatArgs {
       if (half == 0 && n[j] < t.N) part[((int64_t)lt * 2 + wm) * t.N + n[j]] = make_float2(top, sum);
       for (int g = 0; g < M; ++g) {
         const int id = g == 0 ? first[j] : (n[j] < t.N ? ids[n[j] * M + g] : -1);
-        const int at = given_place(id, l0, t.v1, half);
+        const int at = given_place<S::WM_ROWS>(id, l0, t.v1, half);
         const bool hit = at >= 0;
         if (__any(hit)) {
           float z = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < S::MF; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
               if (at == 32 * i + 8 * (r / 4) + r % 4) z = acc[i][j][r];
@@ -119,25 +121,26 @@ struct StatJob : StatArgs {
         }
       }
     }
-    return n0 + 64 <= t.N;
+    return n0 + S::WN_ROWS <= t.N;
   }
 };
 
-template <class Mul>
-__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_stats(StatArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, false>()];
-  StatJob job;
+template <class Mul, class S>
+__global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_stats(StatArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[S::lds(false)];
+  StatJob<S> job;
   (StatArgs&)job = a;
   const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
-  tile_stream<Mul, false, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+  tile_stream<Mul, false, false, S>(job, r.first, r.step, r.end, lds);
 }
 
-// The parts of 16 rows joined: 16 rows x 64 runs of parts per block, then the runs in the order of a tree.
-__global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t parts, int64_t N, int64_t V, const int32_t* ids,
+// The parts of `wide` rows (a power of two up to 16) joined by a block: 1024 / wide runs of parts a row, then the runs in
+// the order of a tree.
+__global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t parts, int64_t N, int64_t V, int wide, const int32_t* ids,
                                                    int M, const float* given, float* logp, float* row_max, float* log_sum) {
-  __shared__ float tops[64][16], sums[64][16];
-  const int x = (int)threadIdx.x & 15, y = (int)threadIdx.x >> 4;
-  const int64_t n = (int64_t)blockIdx.x * 16 + x;
+  __shared__ float2 joined[1024];
+  const int tid = (int)threadIdx.x, x = tid & (wide - 1), y = tid / wide, runs = 1024 / wide;
+  const int64_t n = (int64_t)blockIdx.x * wide + x;
   float top = -__builtin_inff(), sum = 0.0f;
   auto add = [&](float m, float s) {
     const float hi = fmaxf(top, m);
@@ -146,33 +149,31 @@ __global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t p
     top = hi;
   };
   if (n < N) {
-#pragma unroll 4
-    for (int64_t p = y; p < parts; p += 64) {
+#pragma unroll 8
+    for (int64_t p = y; p < parts; p += runs) {
       const float2 v = part[p * N + n];
       add(v.x, v.y);
     }
   }
-  tops[y][x] = top;
-  sums[y][x] = sum;
-  for (int k = 32; k > 0; k >>= 1) {
+  joined[tid] = make_float2(top, sum);
+  for (int k = 512; k >= wide; k >>= 1) {
     __syncthreads();
-    if (y < k) {
-      add(tops[y + k][x], sums[y + k][x]);
-      tops[y][x] = top;
-      sums[y][x] = sum;
+    if (tid < k) {
+      add(joined[tid + k].x, joined[tid + k].y);
+      joined[tid] = make_float2(top, sum);
     }
   }
   __syncthreads();
   if (n >= N) return;
-  top = tops[0][x];
-  sum = sums[0][x];
+  top = joined[x].x;
+  sum = joined[x].y;
   const bool empty = top == -__builtin_inff() && sum == 0.0f;
   const float logs = empty ? 0.0f : logf(sum);
   if (y == 0) {
     row_max[n] = top;
     log_sum[n] = logs;
   }
-  for (int g = y; g < M; g += 64) {
+  for (int g = y; g < M; g += runs) {
     const int id = ids[n * M + g];
     float v = 0.0f;
     if (id >= V) v = __builtin_nanf("");
@@ -306,80 +307,82 @@ struct GradArgs {
   char* G; int64_t ldg;                                    // [N] rows of the piece's labels; bytes
 };
 
-template <class Mul>
+template <class Mul, class S>
 struct GradJob : GradArgs {
-  static constexpr int STORES = 16;
-  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit(u); }
-  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
+  static constexpr int STORES = S::NF * S::PIECES / 2;
+  __device__ __forceinline__ TileUnit unit(int u) const { return t.unit<S>(u); }
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int lt, nt;
     t.place(u, lt, nt);
-    const int64_t col0 = (int64_t)lt * TILE_M + 128 * wm, n0 = (int64_t)nt * LIN_TN + 64 * wn;
+    const int64_t col0 = (int64_t)lt * S::M + S::WM_ROWS * wm, n0 = (int64_t)nt * S::N + S::WN_ROWS * wn;
     const int half = lane >> 5;
     const int64_t l0 = t.v0 + col0, left = t.v1 - l0;      // (wave-uniform)
-    int64_t n[2];
-    float2 cf[2];
-    int first[2];
+    int64_t n[S::NF];
+    float2 cf[S::NF];
+    int first[S::NF];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NF; ++j) {
       n[j] = n0 + 32 * j + (lane & 31);
       const bool in = n[j] < t.N;
       cf[j] = in ? coef[n[j]] : make_float2(0.0f, 0.0f);
       first[j] = M > 0 && in ? ids[n[j] * M] : -1;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < S::NF; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::MF; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           acc[i][j][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -cf[j].x)) * cf[j].y;
       for (int g = 0; g < M; ++g) {
         const int id = g == 0 ? first[j] : (n[j] < t.N ? ids[n[j] * M + g] : -1);
-        const int at = given_place(id, l0, t.v1, half);
+        const int at = given_place<S::WM_ROWS>(id, l0, t.v1, half);
         const bool hit = at >= 0;
         if (__any(hit)) {
           const float d = hit ? up[n[j] * M + g] : 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < S::MF; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
               acc[i][j][r] += at == 32 * i + 8 * (r / 4) + r % 4 ? d : 0.0f;
         }
       }
     }
-    if (left < 128) {                                      // labels past the last: no share in dX
+    if (left < S::WM_ROWS) {                                      // labels past the last: no share in dX
       const int mine = (int)(left < -128 ? -128 : left) - 4 * half;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < S::MF; ++i)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (32 * i + 8 * (r / 4) + r % 4 >= mine) acc[i][0][r] = acc[i][1][r] = 0.0f;
+          if (32 * i + 8 * (r / 4) + r % 4 >= mine) 
+#pragma unroll
+            for (int j = 0; j < S::NF; ++j) acc[i][j][r] = 0.0f;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      i32x4_t v[8];
-      pieces16(acc, j, v, [](float lo, float hi) { return pack16<Mul>(lo, hi); });
+    for (int j = 0; j < S::NF; ++j) {
+      i32x4_t v[2 * S::MF];
+      pieces16<S::MF>(acc, j, v, [](float lo, float hi) { return pack16<Mul>(lo, hi); });
       const int64_t r0 = n0 + 32 * j;
-      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+      put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
         if (r0 + row < t.N) *(i32x4_t*)(G + (r0 + row) * ldg + 2 * col0 + 16 * c) = x;
       });
       if (planes == 1) continue;
-      pieces16(acc, j, v, [](float lo, float hi) { return rest16<Mul>(lo, hi); });
-      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+      pieces16<S::MF>(acc, j, v, [](float lo, float hi) { return rest16<Mul>(lo, hi); });
+      put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
         if (r0 + row < t.N) *(i32x4_t*)(G + (t.N + r0 + row) * ldg + 2 * col0 + 16 * c) = x;
       });
     }
-    return n0 + 64 <= t.N;
+    return n0 + S::WN_ROWS <= t.N;
   }
 };
 
-template <class Mul>
-__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_grad_logits(GradArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, true>()];
-  GradJob<Mul> job;
+template <class Mul, class S>
+__global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_grad_logits(GradArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[S::lds(true)];
+  GradJob<Mul, S> job;
   (GradArgs&)job = a;
   const UnitRange r = xcd_units(a.t.label_tiles * a.t.row_tiles);
-  tile_stream<Mul, false, false, LIN_WN, LIN_NBUF>(job, r.first, r.step, r.end, lds);
+  tile_stream<Mul, false, false, S>(job, r.first, r.step, r.end, lds);
 }
 
 // dW = G^T X: rows of the result are labels (n of the tile), its columns features (m)
@@ -420,44 +423,41 @@ __device__ __forceinline__ void store4(const OutArgs& o, int64_t row, int64_t co
   }
 }
 
-// A wave's 64 rows x 128 columns of a result in rows: tile row r of the result is row r0 + r, present below `rows`; the
+// A wave's part of a result in rows: tile row r of the result is row r0 + r, present below `rows`; the
 // columns start at c0, present below `cols` (a multiple of 8). Scaled by f, in o's type, added to or not. Returns whether all of it is
-// present (then it took 16 stores at least).
-__device__ __forceinline__ bool store_tile(const OutArgs& o, f32x16_t (&acc)[4][2], float f, int64_t r0, int64_t rows, int c0, int cols,
+// present (then it took a store per piece of 16-bit results at least).
+template <class S>
+__device__ __forceinline__ bool store_tile(const OutArgs& o, f32x16_t (&acc)[S::MF][S::NF], float f, int64_t r0, int64_t rows, int c0, int cols,
                                            int lane, char* lds) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < S::NF; ++j) {
     const int64_t rj = r0 + 32 * j;
     if (o.type == T_F32_ || o.accumulate) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        i32x4_t v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const f32x16_t& s = acc[2 * h + k / 4][j];
-          const int q = 4 * (k % 4);
-          v[k] = i32x4_t{(int)f2u(s[q] * f), (int)f2u(s[q + 1] * f), (int)f2u(s[q + 2] * f), (int)f2u(s[q + 3] * f)};
-        }
-        put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
-          const int col = c0 + 64 * h + 4 * c;
+        i32x4_t v[2 * S::MF];
+        pieces32<S::MF>(j, h, v, [&](int i, int jj, int r) { return (int)f2u(acc[i][jj][r] * f); });
+        put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
+          const int col = c0 + 16 * S::MF * h + 4 * c;
           if (rj + row < rows && col < cols) store4(o, rj + row, col, __builtin_bit_cast(f32x4_t, x));
         });
       }
     } else {
-      i32x4_t v[8];
-      if (o.type == T_BF16_) pieces16(acc, j, v, [f](float lo, float hi) { return pack16<MulBF16>(lo * f, hi * f); });
-      else pieces16(acc, j, v, [f](float lo, float hi) { return pack16<MulF16>(lo * f, hi * f); });
-      put_rows(lds, lane, v, [&](int row, int c, i32x4_t x) {
+      i32x4_t v[2 * S::MF];
+      if (o.type == T_BF16_) pieces16<S::MF>(acc, j, v, [f](float lo, float hi) { return pack16<MulBF16>(lo * f, hi * f); });
+      else pieces16<S::MF>(acc, j, v, [f](float lo, float hi) { return pack16<MulF16>(lo * f, hi * f); });
+      put_rows<S::PIECES>(lds, lane, v, [&](int row, int c, i32x4_t x) {
         const int col = c0 + 8 * c;
         if (rj + row < rows && col < cols) *(i32x4_t*)((uint16_t*)o.out + (rj + row) * o.ld + col) = x;
       });
     }
   }
-  return r0 + 64 <= rows && c0 + 128 <= cols;
+  return r0 + S::WN_ROWS <= rows && c0 + S::WM_ROWS <= cols;
 }
 
+template <class S>
 struct WeightJob : ProductArgs {
-  static constexpr int STORES = 16;
+  static constexpr int STORES = S::NF * S::PIECES / 2;
   __device__ __forceinline__ void place(int u, int& dt, int& vt, int& slot) const {
     dt = u % d_tiles;
     slot = u / d_tiles % w_slots;
@@ -467,25 +467,26 @@ struct WeightJob : ProductArgs {
     int dt, vt, slot;
     place(u, dt, vt, slot);
     const int64_t t0 = slot * w_per, left = N - t0, rows = left < w_per ? left : w_per;
-    const int d0 = dt * TILE_M, v = vt * LIN_TN;
-    const int dc = D - d0 < TILE_M ? D - d0 : TILE_M;
+    const int d0 = dt * S::M, v = vt * S::N;
+    const int dc = D - d0 < S::M ? D - d0 : S::M;
     // (two planes come with one run: X's rows with the first, then again with the second)
     const int stages = (int)((rows + 31) / 32);
     const char *x = X + t0 * ldx + 2 * d0, *g = G + t0 * ldg + 2 * (int64_t)v;
-    return {{x, ldx, rows, 2 * dc, stages, x}, {g, ldg, rows, 2 * LIN_TN, stages, g + N * ldg}, planes * stages};
+    return {{x, ldx, rows, 2 * dc, stages, x}, {g, ldg, rows, 2 * S::N, stages, g + N * ldg}, planes * stages};
   }
-  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int dt, vt, slot;
     place(u, dt, vt, slot);
-    const int64_t c = (int64_t)vt * LIN_TN + 64 * wn;
-    const int d = dt * TILE_M + 128 * wm;
-    if (w_slots > 1) return store_tile(OutArgs{wpart + (int64_t)slot * cols * D, D, T_F32_, 0}, acc, 1.0f, c, cols, d, D, lane, lds);
-    return store_tile(dW, acc, *inv, v0 + c, v1, d, D, lane, lds);
+    const int64_t c = (int64_t)vt * S::N + S::WN_ROWS * wn;
+    const int d = dt * S::M + S::WM_ROWS * wm;
+    if (w_slots > 1) return store_tile<S>(OutArgs{wpart + (int64_t)slot * cols * D, D, T_F32_, 0}, acc, 1.0f, c, cols, d, D, lane, lds);
+    return store_tile<S>(dW, acc, *inv, v0 + c, v1, d, D, lane, lds);
   }
 };
 
+template <class S>
 struct FeatureJob : ProductArgs {
-  static constexpr int STORES = 16;
+  static constexpr int STORES = S::NF * S::PIECES / 2;
   __device__ __forceinline__ void place(int u, int& dt, int& nt, int& slot) const {
     dt = u % d_tiles;
     nt = u / d_tiles % row_tiles;
@@ -494,49 +495,50 @@ struct FeatureJob : ProductArgs {
   __device__ __forceinline__ TileUnit unit(int u) const {
     int dt, nt, slot;
     place(u, dt, nt, slot);
-    const int64_t c0 = slot * x_per, n = (int64_t)nt * LIN_TN;
+    const int64_t c0 = slot * x_per, n = (int64_t)nt * S::N;
     const int64_t left = cols - c0, len = left < x_per ? left : x_per;
-    const int d0 = dt * TILE_M, dc = D - d0 < TILE_M ? D - d0 : TILE_M;
+    const int d0 = dt * S::M, dc = D - d0 < S::M ? D - d0 : S::M;
     return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, planes * N - n, 0}, (int)(len / 32)};
   }
-  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[4][2], int wm, int wn, int lane, char* lds) const {
+  __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int dt, nt, slot;
     place(u, dt, nt, slot);
     const int64_t rows = planes * N;
-    return store_tile(OutArgs{xpart + slot * rows * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * LIN_TN + 64 * wn, rows,
-               dt * TILE_M + 128 * wm, D, lane, lds);
+    return store_tile<S>(OutArgs{xpart + slot * rows * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * S::N + S::WN_ROWS * wn, rows,
+               dt * S::M + S::WM_ROWS * wm, D, lane, lds);
   }
 };
 
 // A block takes the units of dW in turn with the others (the first w_units % blocks take one more), then a
 // run of units of dX, x_heavy or x_light of them, so that both kinds of block end together. Blocks of
 // an XCD have neighbouring numbers here.
-template <class Mul>
-__global__ __launch_bounds__(LIN_THREADS, 2) void k_lin_products(ProductArgs a) {
-  __shared__ __attribute__((aligned(1024))) char lds[tile_lds<LIN_WN, LIN_NBUF, true>()];
+template <class Mul, class S>
+__global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_products(ProductArgs a) {
+  __shared__ __attribute__((aligned(1024))) char lds[S::lds(true)];
   const int blocks = (int)gridDim.x, per = blocks / 8;
   const int b = blocks % 8 == 0 ? ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3) : (int)blockIdx.x;
   {
-    WeightJob job;
+    WeightJob<S> job;
     (ProductArgs&)job = a;
-    tile_stream<Mul, true, true, LIN_WN, LIN_NBUF>(job, b, blocks, a.w_units, lds);
+    tile_stream<Mul, true, true, S>(job, b, blocks, a.w_units, lds);
   }
   {
-    FeatureJob job;
+    FeatureJob<S> job;
     (ProductArgs&)job = a;
     const int heavy = a.w_units % blocks;
     const int first = b < heavy ? b * a.x_heavy : heavy * a.x_heavy + (b - heavy) * a.x_light;
     const int end = first + (b < heavy ? a.x_heavy : a.x_light);
-    tile_stream<Mul, true, false, LIN_WN, LIN_NBUF>(job, first, 1, end < a.x_units ? end : a.x_units, lds);
+    tile_stream<Mul, true, false, S>(job, first, 1, end < a.x_units ? end : a.x_units, lds);
   }
 }
 
 // Rows [r0, r0 + rows) of a result from the partial sums of `slots` runs, `stride` floats apart. Thread (x, y) of a block of
-// 64 x 4 sums the runs y, y + 4, .. of vector x; the four sums are added in the order of y. Two results share a
+// 64 x G sums the runs y, y + G, .. of vector x; the G sums are added in the order of y. Two results share a
 // launch: the first `blocks` blocks take the first.
 struct SumArgs { const float* part; int64_t stride, r0, rows; int slots, D; OutArgs o; };
-__global__ __launch_bounds__(256) void k_lin_sum(SumArgs a, SumArgs b, int blocks, const float* inv) {
-  __shared__ f32x4_t sums[4][64];
+template <int G>
+__global__ __launch_bounds__(64 * G) void k_lin_sum(SumArgs a, SumArgs b, int blocks, const float* inv) {
+  __shared__ f32x4_t sums[G][64];
   const int x = (int)threadIdx.x & 63, y = (int)threadIdx.x >> 6;
   const float f = *inv;
   const bool second = (int)blockIdx.x >= blocks;
@@ -548,14 +550,13 @@ __global__ __launch_bounds__(256) void k_lin_sum(SumArgs a, SumArgs b, int block
     f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
     if (i < n4) {
 #pragma unroll 8
-      for (int k = y; k < s.slots; k += 4) v += *(const f32x4_t*)(s.part + k * s.stride + i * 4);
+      for (int k = y; k < s.slots; k += G) v += *(const f32x4_t*)(s.part + k * s.stride + i * 4);
     }
     sums[y][x] = v;
     __syncthreads();
     if (y == 0 && i < n4) {
-      v += sums[1][x];
-      v += sums[2][x];
-      v += sums[3][x];
+#pragma unroll
+      for (int g = 1; g < G; ++g) v += sums[g][x];
       store4(s.o, s.r0 + i / d4, i % d4 * 4, v * f);
     }
     __syncthreads();
@@ -563,31 +564,41 @@ __global__ __launch_bounds__(256) void k_lin_sum(SumArgs a, SumArgs b, int block
 }
 
 // ---- launchers -------------------------------------------------------------------------------------
-static unsigned blocks_for(int64_t units) {
-  const int64_t cus = device_cus();
-  return (unsigned)(units < cus ? units : cus);
-}
-static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 static unsigned sum_grid(int64_t rows, int D) {
   const int64_t want = ceil_div(rows * (D / 4), 64), cap = 32 * (int64_t)device_cus();
   return (unsigned)(want < cap ? want : cap);
 }
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
-LinearLayout linear_layout(int64_t N, int64_t V, int M) {
+// The shape that takes N x V logits soonest.
+static int logits_shape(int64_t N, int64_t V, int D, int cus, double* us) {
+  int best = 0;
+  for (int k = 0; k < SHAPE_COUNT; ++k) {
+    const int m = SHAPES[k].size;
+    const double t = units_time(SHAPES[k], ceil_div(N, m) * ceil_div(V, m), D / 32, cus) + (double)N * V / m * 32e-6 / 5.0;   // (and the join)
+    if (k == 0 || t < *us) {
+      best = k;
+      *us = t;
+    }
+  }
+  return best;
+}
+LinearLayout linear_layout(int64_t N, int64_t V, int D, int M) {
   LinearLayout s{};
-  s.parts = 2 * ceil_div(V, TILE_M);
+  double us;
+  s.shape = logits_shape(N, V, D, device_cus(), &us);
+  s.parts = 2 * ceil_div(V, SHAPES[s.shape].size);
   s.part = 0;
   s.given = up256((size_t)s.parts * N * 8);
   s.total = s.given + up256((size_t)N * (M > 0 ? M : 1) * 4);
   return s;
 }
 
-static LogitTiles tiles_of(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t N, int64_t v0, int64_t v1, int D) {
+static LogitTiles tiles_of(int shape, const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t N, int64_t v0, int64_t v1, int D) {
   LogitTiles t{};
   t.X = (const char*)X; t.W = (const char*)W; t.ldx = 2 * ldx; t.ldw = 2 * ldw;
   t.N = N; t.v0 = v0; t.v1 = v1; t.stages = D / 32;
-  t.row_tiles = (int)ceil_div(N, LIN_TN); t.label_tiles = (int)ceil_div(v1 - v0, TILE_M);
+  t.row_tiles = (int)ceil_div(N, SHAPES[shape].size); t.label_tiles = (int)ceil_div(v1 - v0, SHAPES[shape].size);
   return t;
 }
 
@@ -596,33 +607,37 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
                         void* workspace, hipStream_t st) {
   char* ws = (char*)workspace;
   StatArgs a{};
-  a.t = tiles_of(X, ldx, W, ldw, N, 0, V, D);
+  a.t = tiles_of(s.shape, X, ldx, W, ldw, N, 0, V, D);
   a.ids = ids; a.M = M; a.part = (float2*)(ws + s.part); a.given = (float*)(ws + s.given);
-  const unsigned grid = blocks_for((int64_t)a.t.row_tiles * a.t.label_tiles);
-  if (type == T_BF16_) hipLaunchKernelGGL(k_lin_stats<MulBF16>, dim3(grid), dim3(LIN_THREADS), 0, st, a);
-  else hipLaunchKernelGGL(k_lin_stats<MulF16>, dim3(grid), dim3(LIN_THREADS), 0, st, a);
+  const unsigned grid = blocks_for(s.shape, (int64_t)a.t.row_tiles * a.t.label_tiles, device_cus());
+  with_shape(s.shape, [&](auto shape) {
+    typedef decltype(shape) S;
+    if (type == T_BF16_) hipLaunchKernelGGL((k_lin_stats<MulBF16, S>), dim3(grid), dim3(S::THREADS), 0, st, a);
+    else hipLaunchKernelGGL((k_lin_stats<MulF16, S>), dim3(grid), dim3(S::THREADS), 0, st, a);
+  });
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-  hipLaunchKernelGGL(k_lin_join, dim3((unsigned)ceil_div(N, 16)), dim3(1024), 0, st, a.part, s.parts, N, V, ids, M, a.given, logp,
+  int wide = 1;                                            // (few rows: more blocks, and more runs of parts in each)
+  while (wide * 64 < N && wide < 16) wide *= 2;
+  hipLaunchKernelGGL(k_lin_join, dim3((unsigned)ceil_div(N, wide)), dim3(1024), 0, st, a.part, s.parts, N, V, wide, ids, M, a.given, logp,
                      row_max, log_sum);
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
 
-// How one piece's products are spread over the device: the time (us) of a launch whose dX is cut into x_slots
-// runs and dW into w_slots, by what a stage (1 us with every compute unit at work), a unit's start and its
-// results take; and how many units of dX a block takes that has one unit of dW more than the others
-// (heavy) or not (light).
-static double products_time(int64_t tiles, int64_t wst, int64_t row_tiles, int64_t dt, int64_t w_slots, int64_t x_slots, bool add,
-                            bool dw, bool dx, int* heavy, int* light) {
-  const int cus = device_cus();
-  const double tw = 3.0 + (double)ceil_div(wst, w_slots), tx = (add ? 10.0 : 4.0) + (double)ceil_div(tiles * 8, x_slots);
-  const int64_t uw = dw ? tiles * dt * w_slots : 0, ux = dx ? row_tiles * dt * x_slots : 0;
-  const int rem = (int)(uw % cus);
-  const double low = (double)(uw / cus) * tw, top = rem > 0 ? low + tw : low;
+// How one piece's products are spread over the device: the time (us) of a launch with dX in x_units units of x_stages
+// stages and dW in w_units of w_stages, and how many units of dX a block takes that has one unit of dW more than the
+// others (heavy) or not (light). add: dX's sums are added to those of the pieces before.
+static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stages, int64_t x_units, int64_t x_stages, bool add,
+                            int cus, int* heavy, int* light) {
+  const int64_t blocks = (int64_t)cus * c.blocks;
+  const double stage = 1.25 * stage_time(c, w_units + x_units, cus);  // (K-major)
+  const double tw = c.ends + (double)w_stages * stage, tx = c.ends + (add ? 6.0 : 0.0) + (double)x_stages * stage;
+  const int64_t rem = w_units % blocks;
+  const double low = (double)(w_units / blocks) * tw, top = rem > 0 ? low + tw : low;
   *heavy = *light = 0;
-  if (ux == 0) return top;
+  if (x_units == 0) return top;
   // the blocks end after m units of dX, counted from the end of dW's units of either kind: no earlier than the
   // work shared out evenly, and soon after that
-  const double even = ((double)uw * tw + (double)ux * tx) / cus, from = even > top ? even : top;
+  const double even = ((double)w_units * tw + (double)x_units * tx) / (double)blocks, from = even > top ? even : top;
   double best = 0.0;
   for (int k = 0; k < (rem > 0 ? 2 : 1); ++k) {
     const double start = k ? top : low;
@@ -631,7 +646,7 @@ static double products_time(int64_t tiles, int64_t wst, int64_t row_tiles, int64
       if (best > 0.0 && T >= best) break;
       if (T < top) continue;
       const double h = rem > 0 ? (double)(int64_t)((T - top) / tx + 1e-6) : 0.0, l = (double)(int64_t)((T - low) / tx + 1e-6);
-      if (rem * h + (cus - rem) * l >= (double)ux) {
+      if ((double)rem * h + (double)(blocks - rem) * l >= (double)x_units) {
         best = T;
         *heavy = (int)h;
         *light = (int)l;
@@ -642,52 +657,61 @@ static double products_time(int64_t tiles, int64_t wst, int64_t row_tiles, int64
   return best;
 }
 
-// The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache) and the runs,
-// by the time they are expected to take: more pieces fill the device's last round better or worse, runs fill it
-// with less in each, but are summed apart (dX by adding to memory, dW by another launch). 4096 rows x 131,072
-// labels x 768: equal pieces and one run per round of blocks took 324 us a piece, runs alone 25% less.
+// The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache), the shapes of its
+// tiles and the runs, by the time they are expected to take: more pieces fill the device's last round better or
+// worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch). 4096 rows
+// x 131,072 labels x 768: equal pieces with one run per round of blocks took 4.3 ms in all, these 3.4.
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
+constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
   LinearGradLayout s{};
-  const int64_t cus = device_cus(), dt = ceil_div(D, TILE_M), row_tiles = ceil_div(N, LIN_TN);
-  const int64_t whole = ceil_div(V, TILE_M);               // label tiles
-  int64_t most = chunk > 0 ? ceil_div(chunk, TILE_M) : (int64_t(1) << 27) / N / TILE_M;
+  const int cus = device_cus();
+  const int64_t whole = ceil_div(V, 256);   // pieces are multiples of 256 labels
+  int64_t most = chunk > 0 ? ceil_div(chunk, 256) : (int64_t(1) << 27) / N / 256;
   most = most < 1 ? 1 : (most > whole ? whole : most);
-  if (most > MAX_PIECE / TILE_M) most = MAX_PIECE / TILE_M;
-  s.planes = 2 * N <= LIN_TN ? 2 : 1;
-  const int64_t wst = s.planes * ceil_div(N, 32), fewest = ceil_div(whole, most);
-  const double rd = (double)N * D * 4e-6 / 5.0;            // us for dX's size in FP32 to memory
+  if (most > MAX_PIECE / 256) most = MAX_PIECE / 256;
+  s.planes = N <= TWO_PLANES ? 2 : 1;
+  const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most), x_rows = s.planes * N;
+  const double rd = (double)x_rows * D * 4e-6 / 5.0;       // us for dX's partial sums to memory
   double least = 0.0;
   const int64_t last = chunk > 0 || fewest == 1 ? fewest : fewest + 4;
   for (int64_t pieces = fewest; pieces <= last && pieces <= whole; ++pieces) {
-    const int64_t tiles = chunk > 0 ? most : ceil_div(whole, pieces), used = ceil_div(whole, tiles);
-    const double logits = (double)ceil_div(row_tiles * tiles, cus) * (6.0 + D / 32) + 4.0;
-    for (int64_t ws = 1; ws <= 16; ws *= 2) {
-      if (ws > 1 && (!need_dw || s.planes > 1 || ws * 2 > wst || tiles * dt * ws > 2 * cus)) break;
-      for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64}) {
-        if (xs > 1 && (!need_dx || xs * 2 > tiles * 8 || row_tiles * dt * xs > 2 * cus)) break;
-        int h, l;
-        double us = products_time(tiles, wst, row_tiles, dt, ws, xs, used > 1, need_dw, need_dx, &h, &l) + logits + 4.0;
-        if (ws > 1) us += 2.0 + (double)(ws + 1) * tiles * TILE_M * D * 4e-6 / 5.0;
-        us = us * (double)used + (double)xs * rd;
-        if (least == 0.0 || us < least) {
-          least = us;
-          s.piece = tiles * TILE_M; s.x_slots = (int)xs; s.w_slots = (int)ws;
+    const int64_t labels = (chunk > 0 ? most : ceil_div(whole, pieces)) * 256, used = ceil_div(V, labels);
+    const int64_t n = labels < V ? labels : V, xst = ceil_div(n, 32);
+    double logits;
+    const int ls = logits_shape(N, n, D, cus, &logits);
+    for (int k = 0; k < SHAPE_COUNT; ++k) {
+      const ShapeCost& c = SHAPES[k];
+      const int64_t dt = ceil_div(D, c.size), wt = need_dw ? ceil_div(n, c.size) * dt : 0, xt = need_dx ? ceil_div(x_rows, c.size) * dt : 0;
+      const int64_t most_units = 2 * (int64_t)cus * c.blocks;
+      if (k > 0 && N >= 1024 && n >= 16384) break;         // (the large shape's)
+      for (int64_t ws = 1; ws <= 16; ws *= 2) {
+        if (ws > 1 && (!need_dw || s.planes > 1 || ws * 2 > wst || wt * ws > most_units)) break;
+        for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512}) {
+          if (xs > 1 && (!need_dx || xs * 4 > xst || xt * xs > most_units)) break;
+          int h, l;
+          double us = products_time(c, wt * ws, s.planes * ceil_div(wst, ws), xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + logits + 8.0;
+          if (ws > 1) us += 2.0 + (double)(ws + 1) * n * D * 4e-6 / 5.0;
+          us = us * (double)used + (double)xs * (rd + 0.02);   // (and a run's share of its sum)
+          if (least == 0.0 || us < least) {
+            least = us;
+            s.piece = labels; s.x_slots = (int)xs; s.w_slots = (int)ws; s.logits = ls; s.shape = k;
+          }
         }
       }
     }
   }
-  s.x_per = ceil_div(s.piece / 32, s.x_slots) * 32;
-  s.x_slots = (int)ceil_div(s.piece, s.x_per);
-  s.w_per = ceil_div(ceil_div(N, 32), s.w_slots) * 32;
+  s.x_per = ceil_div(ceil_div(s.piece < V ? s.piece : V, 32), s.x_slots) * 32;
+  s.x_slots = (int)ceil_div(s.piece < V ? s.piece : V, s.x_per);
+  s.w_per = ceil_div(wst, s.w_slots) * 32;
   s.w_slots = (int)ceil_div(N, s.w_per);
   size_t at = 0;
   s.most = at; at += up256(256 * 8);
   s.inv = at; at += 256;
   s.coef = at; at += up256((size_t)N * 8);
   s.up = at; at += up256((size_t)N * (M > 0 ? M : 1) * 4);
-  s.G = at; at += up256((size_t)s.planes * N * s.piece * 2);
-  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * s.planes * N * D * 4);
+  s.G = at; at += up256((size_t)x_rows * s.piece * 2);
+  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * x_rows * D * 4);
   s.wpart = at; if (need_dw && s.w_slots > 1) at += up256((size_t)s.w_slots * s.piece * D * 4);
   s.total = at;
   return s;
@@ -705,33 +729,36 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   hipLaunchKernelGGL(k_lin_coef, dim3((unsigned)ceil_div(c.N, COEF_THREADS)), dim3(COEF_THREADS), 0, st, k);
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+  const int cus = device_cus();
   for (int64_t v0 = 0; v0 < c.V; v0 += s.piece) {
     const int64_t v1 = v0 + s.piece < c.V ? v0 + s.piece : c.V;
     GradArgs g{};
-    g.t = tiles_of(c.X, c.ldx, c.W, c.ldw, c.N, v0, v1, c.D);
+    g.t = tiles_of(s.logits, c.X, c.ldx, c.W, c.ldw, c.N, v0, v1, c.D);
     g.planes = s.planes; g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.G = ws + s.G; g.ldg = 2 * s.piece;
-    hipLaunchKernelGGL(k_lin_grad_logits<Mul>, dim3(blocks_for((int64_t)g.t.row_tiles * g.t.label_tiles)), dim3(LIN_THREADS), 0, st, g);
+    with_shape(s.logits, [&](auto shape) {
+      typedef decltype(shape) S;
+      const unsigned grid = blocks_for(s.logits, (int64_t)g.t.row_tiles * g.t.label_tiles, cus);
+      hipLaunchKernelGGL((k_lin_grad_logits<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, g);
+    });
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+    const ShapeCost& cost = SHAPES[s.shape];
     ProductArgs p{};
     p.X = (const char*)c.X; p.ldx = 2 * c.ldx; p.W = (const char*)c.W; p.ldw = 2 * c.ldw; p.G = ws + s.G; p.ldg = 2 * s.piece;
-    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, TILE_M); p.inv = k.inv;
-    p.cols = ceil_div(v1 - v0, TILE_M) * TILE_M;
+    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, cost.size); p.inv = k.inv;
+    p.cols = ceil_div(v1 - v0, 32) * 32;                   // (G is zero behind the last label, up to its tile's end)
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
     p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0; p.xpart = (float*)(ws + s.xpart);
-    p.row_tiles = (int)ceil_div(c.N, LIN_TN);
-    p.w_units = c.dW ? (int)(p.cols / LIN_TN) * p.d_tiles * p.w_slots : 0;
+    p.row_tiles = (int)ceil_div(s.planes * c.N, cost.size);
+    p.w_units = c.dW ? (int)ceil_div(v1 - v0, cost.size) * p.d_tiles * p.w_slots : 0;
     p.x_units = c.dX ? p.row_tiles * p.d_tiles * p.x_slots : 0;
-    const int64_t cus = device_cus();
-    const unsigned grid = blocks_for((int64_t)p.w_units + p.x_units);
-    if (grid < cus) {                                      // a unit for each block
-      p.x_heavy = 0;
-      p.x_light = 1;
-    } else {
-      products_time(p.cols / TILE_M, s.planes * ceil_div(c.N, 32), p.row_tiles, p.d_tiles, p.w_slots, p.x_slots, s.piece < c.V, c.dW != nullptr,
-                    c.dX != nullptr, &p.x_heavy, &p.x_light);
-    }
-    hipLaunchKernelGGL(k_lin_products<Mul>, dim3(grid), dim3(LIN_THREADS), 0, st, p);
+    const unsigned grid = blocks_for(s.shape, (int64_t)p.w_units + p.x_units, cus);
+    if ((int64_t)p.w_units + p.x_units <= grid) p.x_light = 1;   // a unit for each block
+    else products_time(cost, p.w_units, s.planes * ceil_div(s.w_per, 32), p.x_units, ceil_div(s.x_per, 32), s.piece < c.V, cus, &p.x_heavy, &p.x_light);
+    with_shape(s.shape, [&](auto shape) {
+      typedef decltype(shape) S;
+      hipLaunchKernelGGL((k_lin_products<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, p);
+    });
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
     // the runs of dW summed, and those of dX behind the last piece
     SumArgs w{}, x{};
@@ -739,7 +766,8 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     if (c.dX && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.planes * s.x_slots, c.D, OutArgs{c.dX, c.lddx, c.dx_type, 0}};
     const unsigned wb = w.rows ? sum_grid(w.rows, c.D) : 0, xb = x.rows ? sum_grid(x.rows, c.D) : 0;
     if (wb + xb == 0) continue;
-    hipLaunchKernelGGL(k_lin_sum, dim3(wb + xb), dim3(256), 0, st, w, x, (int)wb, (const float*)k.inv);
+    if (w.slots > 32 || x.slots > 32) hipLaunchKernelGGL(k_lin_sum<16>, dim3(wb + xb), dim3(1024), 0, st, w, x, (int)wb, (const float*)k.inv);
+    else hipLaunchKernelGGL(k_lin_sum<4>, dim3(wb + xb), dim3(256), 0, st, w, x, (int)wb, (const float*)k.inv);
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   }
   return ELMO_OK_;

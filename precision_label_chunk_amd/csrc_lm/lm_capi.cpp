@@ -39,14 +39,14 @@ int check_linear(int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw
   if (N < 0 || N >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (D < 32 || D % 32 != 0 || D > ELMO_MAX_LINEAR_D || M < 0 || M > ELMO_MAX_GIVEN) return ELMO_ESHAPE;
   if (ldx < D || ldw < D || ldx > MAX_LINEAR_LD || ldw > MAX_LINEAR_LD) return ELMO_ESHAPE;
-  if (((N + 255) / 256) * ((V + 255) / 256) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (((N + 63) / 64) * ((V + 63) / 64) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   return ELMO_OK;
 }
 
 int check_i8(int64_t N, int64_t L, int D) {
   if (N < 0 || N >= (int64_t(1) << 31) || L < 1 || L >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (D < 64 || D % 64 != 0 || D > ELMO_MAX_I8_D) return ELMO_ESHAPE;
-  if (((N + 255) / 256) * ((L + 255) / 256) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (((N + 63) / 64) * ((L + 63) / 64) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   return ELMO_OK;
 }
 
@@ -165,9 +165,9 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
   return elmo::run_ckpt8_wgrad(dY, ldy, codes, scales, T, O, D, dW, accumulate, s, workspace, (hipStream_t)stream);
 }
 
-size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int M) {
-  if (N < 1 || check_linear(ELMO_T_BF16, N, V, 32, 32, 32, M) != ELMO_OK) return 0;
-  return elmo::linear_layout(N, V, M).total;
+size_t elmo_linear_logprobs_workspace_bytes(int64_t N, int64_t V, int D, int M) {
+  if (N < 1 || check_linear(ELMO_T_BF16, N, V, D, D, D, M) != ELMO_OK) return 0;
+  return elmo::linear_layout(N, V, D, M).total;
 }
 
 int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
@@ -181,7 +181,7 @@ int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int6
   for (const void* p : {(const void*)ids, (const void*)logp, (const void*)row_max, (const void*)log_sum})
     if (!aligned_to(p, 4)) return ELMO_EINVAL;
   if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
-  const elmo::LinearLayout s = elmo::linear_layout(N, V, M);
+  const elmo::LinearLayout s = elmo::linear_layout(N, V, D, M);
   if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
   return elmo::run_linear_logprobs(X, W, type, N, V, D, ldx, ldw, ids, M, logp, row_max, log_sum, s, workspace,
                                    (hipStream_t)stream);

@@ -36,14 +36,16 @@ int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uin
                     float* dW, int accumulate, const WgradLayout& s, void* workspace, hipStream_t st);
 
 // log probabilities of given labels from features and weights, and the gradients of both
-struct LinearLayout { int64_t parts; size_t part, given, total; };
-LinearLayout linear_layout(int64_t N, int64_t V, int M);
+// (shapes: the numbers of their tile shapes)
+struct LinearLayout { int shape; int64_t parts; size_t part, given, total; };
+LinearLayout linear_layout(int64_t N, int64_t V, int D, int M);
 int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw,
                         const int32_t* ids, int M, float* logp, float* row_max, float* log_sum, const LinearLayout& s,
                         void* workspace, hipStream_t st);
 struct LinearGradLayout {
   int64_t piece, x_per, w_per;                             // labels per piece; labels / tokens per run
   int x_slots, w_slots;                                    // runs
+  int logits, shape;                                       // tile shapes of the logits and of the products
   int planes;                                              // 16-bit numbers whose sum holds an element of G
   size_t most, inv, coef, up, G, xpart, wpart, total;
 };
@@ -59,7 +61,7 @@ int run_zero_rows(void* out, int type, int64_t rows, int D, int64_t ld, hipStrea
 int run_linear_logprobs_grad(const LinearGradCall& c, const LinearGradLayout& s, void* workspace, hipStream_t st);
 
 // rows in 8-bit integers with a scale each, and products of such rows
-struct I8Layout { int slots, per; int64_t L4; size_t total; };
+struct I8Layout { int shape, slots, per; int64_t L4; size_t total; };
 int run_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st);
 I8Layout i8_layout(int64_t N, int64_t L, int D);
 int run_i8_matmul(const int8_t* X, const float* sx, const int8_t* W, const float* sw, int64_t N, int64_t L, int D, void* Y,

@@ -1,20 +1,18 @@
 // Matrix products in tiles, C[m, n] = sum_k A[m, k] B[n, k], for kernels that do something of their
 // own with the sums of a tile (softmax statistics, a gradient, scales) instead of storing them.
 //
-// A block of 2 x WN waves computes 256 x 64 WN tiles, a wave 128 x 64 of it in 4 x 2 sums of 32 x 32
-// (128 registers). The depth goes in stages of 64 bytes of K per row (32 elements of 16 bits, 64 of 8),
-// copied from memory to LDS without passing registers, NBUF - 1 stages ahead, one barrier a stage (NBUF = 3: 4 and
-// 5 are no faster, 96 KiB leave room for results on their way out). The
-// stages of a block's tiles follow each other without a break: the first stages of the next tile are on
-// their way while the sums of the last one are used.
+// A block of 2 x WN waves computes tiles of 64 MF x 32 NF WN, a wave 32 MF x 32 NF of it in sums of 32 x 32. The depth goes
+// in stages of 64 bytes of K per row (32 elements of 16 bits, 64 of 8), copied from memory to LDS without
+// passing registers, NBUF - 1 stages ahead, one barrier a stage. The stages of a block's tiles follow each other
+// without a break: the first stages of the next tile are on their way while the sums of the last one are used.
 //
 // An operand is K-contiguous (rows of m or n, its elements of a row along K) or K-major (rows of k, 16-bit
-// elements along m or n, read from LDS by the transposing reads). Both are 16 KiB of LDS per 256 rows
+// elements along m or n, read from LDS by the transposing reads). Both take 64 bytes of LDS per row of m or n
 // and stage. The copies write 16 bytes a lane in lane order, so what a lane fetches is permuted instead:
 //   K-contiguous  row r's four 16-byte pieces at p = c ^ f(r), f(r) = (r >> 1 & 3) ^ (r >> 3 & 1): the 8
 //                 rows that a read serves at once touch all 32 banks once, any 16 rows all 64 once
-//   K-major       row k's 16-byte piece c at c ^ 2 X(k & 3), X = 0, 2, 5, 7: the same for the 4 rows x
-//                 32 (64) bytes of a transposing read
+//   K-major       row k's 16-byte piece c at c ^ 2 X(k & 3), X = 0, 2, 5, 7 (rows of 128 bytes: 0, 1, 2, 3): the same
+//                 for the 4 rows x 32 (64) bytes of a transposing read
 #pragma once
 #include "elem_types.hpp"
 
@@ -60,13 +58,29 @@ struct MulI8 {
 struct Operand { const char* at; int64_t ld; int64_t rows; int cols; int turn = 0; const char* second = nullptr; };
 struct TileUnit { Operand a, b; int stages; };
 
-constexpr int TILE_M = 256, STAGE_K = 64;                  // rows of A per tile; bytes of K per stage
+constexpr int STAGE_K = 64;                                // bytes of K per stage
 
-template <int WN> constexpr int tile_n() { return 64 * WN; }
-template <int WN, int NBUF, bool PUT> constexpr int tile_lds() { return NBUF * (TILE_M + 64 * WN) * STAGE_K + (PUT ? 2 * WN * 8192 : 0); }
+// The tile shapes. Large: 128 x 64 a wave, the fewest LDS reads per product, one block per compute unit (NBUF = 3:
+// 4 and 5 are no faster, and 96 KiB leave room for results on their way out). Medium and small: less is left
+// empty by few rows, more blocks share a compute unit, and a stage alone takes less time.
+template <int MF_, int NF_, int WN_, int NBUF_, int BLOCKS_>
+struct TileShape {
+  static constexpr int MF = MF_, NF = NF_, WN = WN_, NBUF = NBUF_;
+  static constexpr int BLOCKS = BLOCKS_;                   // per compute unit
+  static constexpr int M = 64 * MF, N = 32 * NF * WN, THREADS = 128 * WN, WM_ROWS = 32 * MF, WN_ROWS = 32 * NF;
+  static constexpr int WAVES = BLOCKS * THREADS / 256;     // per SIMD
+  static constexpr int PIECES = 4 * MF;                    // 16-byte pieces of a wave's row of 16-bit results
+  static constexpr int PUT = 32 * PIECES * 16;             // LDS bytes of a wave for results on their way out
+  static constexpr int BUF = (M + N) * STAGE_K;
+  static constexpr int lds(bool put) { return NBUF * BUF + (put ? 2 * WN * PUT : 0); }
+};
+typedef TileShape<4, 2, 4, 3, 1> LargeTiles;               // 256 x 256
+typedef TileShape<2, 2, 2, 3, 2> MediumTiles;              // 128 x 128
+typedef TileShape<1, 1, 2, 4, 4> SmallTiles;               // 64 x 64
 
 __device__ __forceinline__ int kc_swizzle(int row) { return ((row >> 1) & 3) ^ ((row >> 3) & 1); }
-__device__ __forceinline__ int km_swizzle(int k) { const int r = k & 3; return 2 * (2 * r | (r >> 1)); }
+template <int ROWS>
+__device__ __forceinline__ int km_swizzle(int k) { const int r = k & 3; return ROWS == 64 ? 2 * r : 2 * (2 * r | (r >> 1)); }
 
 // every wave of the block has all but its last N vector memory operations and all its LDS reads behind it
 template <int N>
@@ -98,7 +112,7 @@ struct StageCopy {
     at = o.at;
     ld = o.ld;
     if constexpr (KM) {
-      const int k = tid / PER_ROW, c = (tid % PER_ROW) ^ km_swizzle(k);
+      const int k = tid / PER_ROW, c = (tid % PER_ROW) ^ km_swizzle<ROWS>(k);
       off = k * (int)ld + c * 16;
       step = THREADS / PER_ROW * (int)ld;
       left = rows = o.rows;
@@ -146,7 +160,7 @@ struct StageRead {
       const int g = lane >> 4, j = lane & 15, k = 8 * (g >> 1) + (j >> 2);
       const int col = first + 16 * (g & 1) + 4 * (j & 3);
 #pragma unroll
-      for (int f = 0; f < F; ++f) at[f] = k * (ROWS * 2) + (((col + 32 * f) >> 3) ^ km_swizzle(k)) * 16 + (col & 7) * 2;
+      for (int f = 0; f < F; ++f) at[f] = k * (ROWS * 2) + (((col + 32 * f) >> 3) ^ km_swizzle<ROWS>(k)) * 16 + (col & 7) * 2;
     } else {
       const int r = first + (lane & 31);
       at[0] = r * STAGE_K + ((lane >> 5) ^ kc_swizzle(r)) * 16;
@@ -166,32 +180,30 @@ struct StageRead {
   }
 };
 
-// A wave's results, on their way to memory in rows: 32 rows of 16 pieces of 16 bytes, of which a lane holds
-// pieces 2 k + lane / 32 (k = 0 .. 7) of row lane % 32. They go through 8 KiB of LDS of the wave's own, so
-// that 16 lanes write 256 bytes of a row: put(row, piece, value) 8 times. Straight from the sums a store reaches
-// 32 rows with 16 or 32 bytes in each, and a 256 x 256 tile of 16-bit results took 20 us to write, of 16-bit
-// gradient codes 4.
-template <class F>
-__device__ __forceinline__ void put_rows(char* lds, int lane, const i32x4_t (&v)[8], F&& put) {
+// A wave's results, on their way to memory in rows: 32 rows of P pieces of 16 bytes, of which a lane holds pieces
+// 2 k + lane / 32 of row lane % 32. They go through LDS of the wave's own, so that P lanes write a row's 16 P
+// bytes: put(row, piece, value). Straight from the sums a store reaches 32 rows with 16 or 32 bytes in each, and a
+// 256 x 256 tile of 16-bit results took 20 us to write.
+template <int P, class F>
+__device__ __forceinline__ void put_rows(char* lds, int lane, const i32x4_t (&v)[P / 2], F&& put) {
   asm volatile("" : "+v"(lane));                           // (no address is held across the products)
   const int r = lane & 31;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) *(i32x4_t*)(lds + r * 256 + (((2 * k + (lane >> 5)) ^ (r & 15)) * 16)) = v[k];
+  for (int k = 0; k < P / 2; ++k) *(i32x4_t*)(lds + r * (16 * P) + (((2 * k + (lane >> 5)) ^ (r & (P - 1))) * 16)) = v[k];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int row = 4 * k + (lane >> 4), c = lane & 15;
-    put(row, c, *(const i32x4_t*)(lds + row * 256 + ((c ^ (row & 15)) * 16)));
+  for (int k = 0; k < P / 2; ++k) {
+    const int row = (64 / P) * k + lane / P, c = lane % P;
+    put(row, c, *(const i32x4_t*)(lds + row * (16 * P) + ((c ^ (row & (P - 1))) * 16)));
   }
   sched_fence();                                           // (the next rows' values are not formed ahead: registers)
 }
-constexpr int PUT_BYTES = 8192;                            // of LDS per wave
 
-// 128 rows of m of one column as 16-bit pieces for put_rows: a lane has 4 of every 8, and swaps with the lane of
-// the other half, so that each holds 8. pack(lo, hi) rounds two sums.
-template <class Acc, class Pack>
-__device__ __forceinline__ void pieces16(const Acc& acc, int j, i32x4_t (&v)[8], Pack&& pack) {
+// A wave's rows of m of one column as 16-bit pieces for put_rows: a lane has 4 of every 8, and swaps with the lane
+// of the other half, so that each holds 8. pack(lo, hi) rounds two sums.
+template <int MF, class Acc, class Pack>
+__device__ __forceinline__ void pieces16(const Acc& acc, int j, i32x4_t (&v)[2 * MF], Pack&& pack) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
       int lo[2], hi[2];
@@ -206,24 +218,32 @@ __device__ __forceinline__ void pieces16(const Acc& acc, int j, i32x4_t (&v)[8],
       v[2 * i + q / 2] = i32x4_t{lo[0], lo[1], hi[0], hi[1]};
     }
 }
+// and half h of them (16 MF rows of m) as 32-bit pieces, 4 rows of m in each: word(i, j, r) gives a sum's bits
+template <int MF, class Word>
+__device__ __forceinline__ void pieces32(int j, int h, i32x4_t (&v)[2 * MF], Word&& word) {
+#pragma unroll
+  for (int k = 0; k < 2 * MF; ++k) {
+    const int t = 2 * MF * h + k, i = t / 4, q = 4 * (t % 4);
+    v[k] = i32x4_t{word(i, j, q), word(i, j, q + 1), word(i, j, q + 2), word(i, j, q + 3)};
+  }
+}
 
 // The products of the units first, first + step, .. below `end`; job.unit(u) describes a unit,
-// job.finish(u, acc, wm, wn, lane, lds) uses its sums (lds: PUT_BYTES of the wave's own behind the buffers, if the
-// block has them): acc[i][j][r] of wave (wm, wn) is row
-// m = 128 wm + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 and column n = 64 wn + 32 j + lane % 32 of the tile.
-// It returns whether the wave has issued at least
-// Job::STORES stores (the same for all its lanes). Every unit has at least one stage. All threads of the block call it.
-template <class Mul, bool AKM, bool BKM, int WN, int NBUF, class Job>
+// job.finish(u, acc, wm, wn, lane, lds) uses its sums (lds: S::PUT bytes of the wave's own behind the buffers, if the
+// block has them): acc[i][j][r] of wave (wm, wn) is row m = S::WM_ROWS wm + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 and
+// column n = S::WN_ROWS wn + 32 j + lane % 32 of the tile. It returns whether the wave has issued at least Job::STORES
+// stores (the same for all its lanes). Every unit has at least one stage. All threads of the block call it.
+template <class Mul, bool AKM, bool BKM, class S, class Job>
 __device__ __forceinline__ void tile_stream(const Job& job, int first, int step, int end, char* lds) {
-  constexpr int THREADS = 128 * WN, A_BYTES = TILE_M * STAGE_K, BUF = A_BYTES + 64 * WN * STAGE_K;
+  constexpr int THREADS = S::THREADS, NBUF = S::NBUF, WN = S::WN, A_BYTES = S::M * STAGE_K, BUF = S::BUF;
   typedef typename Mul::frag frag;
   const int tid = (int)threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   if (first >= end) return;
 
-  StageCopy<AKM, TILE_M, THREADS, Mul::BYTES> ca;
-  StageCopy<BKM, 64 * WN, THREADS, Mul::BYTES> cb;
+  StageCopy<AKM, S::M, THREADS, Mul::BYTES> ca;
+  StageCopy<BKM, S::N, THREADS, Mul::BYTES> cb;
   constexpr int COPIES = decltype(ca)::COPIES + decltype(cb)::COPIES;
   int lu = first, ls = 0, lstages;                         // the unit and stage to be copied next
   int fill = 0;                                            // and its buffer
@@ -251,17 +271,17 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
     }
   };
 
-  StageRead<AKM, TILE_M, 4, Mul> ra;
-  StageRead<BKM, 64 * WN, 2, Mul> rb;
-  ra.start(128 * wm, lane);
-  rb.start(64 * wn, lane);
-  frag fa[2][4], fb[2][2];
-  typename Mul::acc acc[4][2];
+  StageRead<AKM, S::M, S::MF, Mul> ra;
+  StageRead<BKM, S::N, S::NF, Mul> rb;
+  ra.start(S::WM_ROWS * wm, lane);
+  rb.start(S::WN_ROWS * wn, lane);
+  frag fa[2][S::MF], fb[2][S::NF];
+  typename Mul::acc acc[S::MF][S::NF];
   auto products = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < S::MF; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = Mul::mul(fa[h][i], fb[h][j], acc[i][j]);
+      for (int j = 0; j < S::NF; ++j) acc[i][j] = Mul::mul(fa[h][i], fb[h][j], acc[i][j]);
   };
   auto frags = [&](const char* from, int h) __attribute__((always_inline)) {
     rb.read(from + A_BYTES, h, fb[h]);
@@ -290,9 +310,9 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
   for (int u = first; u < end; u += step) {
     const int stages = job.unit(u).stages;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < S::MF; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < S::NF; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
     stage(false, stored);
@@ -300,7 +320,7 @@ __device__ __forceinline__ void tile_stream(const Job& job, int first, int step,
     for (; s < NBUF - 1 && s < stages; ++s) stage(true, stored);
     for (; s < stages; ++s) stage(true, false);
     products(1);
-    stored = job.finish(u, acc, wm, wn, lane, lds + NBUF * BUF + wave * PUT_BYTES);
+    stored = job.finish(u, acc, wm, wn, lane, lds + NBUF * BUF + wave * S::PUT);
   }
   wait_copies<0>();                                        // no copy is on its way when the block's LDS is given back
 }
