@@ -479,8 +479,9 @@ struct WeightJob : ProductArgs {
     place(u, dt, vt, slot);
     const int64_t c = (int64_t)vt * S::N + S::WN_ROWS * wn;
     const int d = dt * S::M + S::WM_ROWS * wm;
-    if (w_slots > 1) return store_tile<S>(OutArgs{wpart + (int64_t)slot * cols * D, D, T_F32_, 0}, acc, 1.0f, c, cols, d, D, lane, lds);
-    return store_tile<S>(dW, acc, *inv, v0 + c, v1, d, D, lane, lds);
+    const bool split = w_slots > 1;                        // (one call: the code of one)
+    const OutArgs o = split ? OutArgs{wpart + (int64_t)slot * cols * D, D, T_F32_, 0} : dW;
+    return store_tile<S>(o, acc, split ? 1.0f : *inv, split ? c : v0 + c, split ? cols : v1, d, D, lane, lds);
   }
 };
 
