@@ -510,9 +510,11 @@ struct FeatureJob : ProductArgs {
   }
 };
 
-// A block takes the units of dW in turn with the others (the first w_units % blocks take one more), then a
-// run of units of dX, x_heavy or x_light of them, so that both kinds of block end together. Blocks of
-// an XCD have neighbouring numbers here.
+// A block takes the units of dW in turn with the others (the first w_units % blocks, the heavy ones, take one more),
+// then x_light or x_heavy units of dX, so that both kinds of block end together: the light blocks go ahead by as
+// many rounds as they have more. In a round neighbouring blocks have neighbouring units, which read the same
+// rows of G (several units of a block in a row let each of them read G from memory again: 1.15 times longer).
+// Blocks of an XCD have neighbouring numbers here.
 template <class Mul, class S>
 __global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_products(ProductArgs a) {
   __shared__ __attribute__((aligned(1024))) char lds[S::lds(true)];
@@ -523,13 +525,14 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_products(ProductAr
     (ProductArgs&)job = a;
     tile_stream<Mul, true, true, S>(job, b, blocks, a.w_units, lds);
   }
-  {
-    FeatureJob<S> job;
-    (ProductArgs&)job = a;
-    const int heavy = a.w_units % blocks;
-    const int first = b < heavy ? b * a.x_heavy : heavy * a.x_heavy + (b - heavy) * a.x_light;
-    const int end = first + (b < heavy ? a.x_heavy : a.x_light);
-    tile_stream<Mul, true, false, S>(job, first, 1, end < a.x_units ? end : a.x_units, lds);
+  FeatureJob<S> job;
+  (ProductArgs&)job = a;
+  const int heavy = a.w_units % blocks, light = blocks - heavy;
+  int ahead = (a.x_light - a.x_heavy) * light;
+  if (ahead > a.x_units) ahead = a.x_units;
+  for (int round = b < heavy ? 1 : 0; round < 2; ++round) {
+    const int first = round ? ahead + b : b - heavy, step = round ? blocks : light;
+    tile_stream<Mul, true, false, S>(job, first, step, round ? a.x_units : ahead, lds);
   }
 }
 
@@ -626,12 +629,13 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
 
 // How one piece's products are spread over the device: the time (us) of a launch with dX in x_units units of x_stages
 // stages and dW in w_units of w_stages, and how many units of dX a block takes that has one unit of dW more than the
-// others (heavy) or not (light). add: dX's sums are added to those of the pieces before.
+// others (heavy) or not (light). add: dX's sums are added to those of the pieces before (20 us for 256 x 256). Within 5%
+// of the times of 4096 x 131,072 x 768 in pieces of 16,384 to 131,072 labels and 4 to 8 runs.
 static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stages, int64_t x_units, int64_t x_stages, bool add,
                             int cus, int* heavy, int* light) {
   const int64_t blocks = (int64_t)cus * c.blocks;
-  const double stage = 1.25 * stage_time(c, w_units + x_units, cus);  // (K-major)
-  const double tw = c.ends + (double)w_stages * stage, tx = c.ends + (add ? 6.0 : 0.0) + (double)x_stages * stage;
+  const double stage = 1.1 * stage_time(c, w_units + x_units, cus);   // (K-major)
+  const double tw = c.ends + (double)w_stages * stage, tx = c.ends + (add ? 20.0 * c.size * c.size / 65536.0 : 0.0) + (double)x_stages * stage;
   const int64_t rem = w_units % blocks;
   const double low = (double)(w_units / blocks) * tw, top = rem > 0 ? low + tw : low;
   *heavy = *light = 0;
@@ -660,8 +664,7 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 
 // The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache), the shapes of its
 // tiles and the runs, by the time they are expected to take: more pieces fill the device's last round better or
-// worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch). 4096 rows
-// x 131,072 labels x 768: equal pieces with one run per round of blocks took 4.3 ms in all, these 3.4.
+// worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
