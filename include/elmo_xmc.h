@@ -336,7 +336,8 @@ int elmo_ckpt8_weight_grad(const void* dY, int64_t ldy, const uint8_t* codes, co
  * Products of exact operands, binary32 sums; logits below 2^126 in magnitude. A row of nothing but -inf logits has row_max
  * -inf, log_sum 0 and its labels' log probabilities -inf; a NaN or +inf logit makes log_sum and logp of its
  * row NaN (row_max skips NaN). Results repeat bit for bit on one device.
- * D % 32 == 0, 32 <= D <= ELMO_MAX_LINEAR_D; 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). The workspace
+ * D % 32 == 0, 32 <= D <= ELMO_MAX_LINEAR_D; 1 <= V < 2^31, 0 <= N < 2^31 (N = 0: nothing is done), fewer than 2^30 tiles of
+ * 64 x 64 logits (ELMO_ESHAPE). The workspace
  * takes 8 bytes for 128 logits (for 32 where there are few).
  */
 #define ELMO_MAX_LINEAR_D 65536
@@ -371,7 +372,8 @@ int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_
  * binary32, multiplied by x_scales[n], then by w_scales[v], and rounded to `ytype`.
  *   X [N, D], W [L, D] int8 (any of -128 .. 127), row-major without gaps, 16-byte aligned; D % 64 == 0,
  *   64 <= D <= ELMO_MAX_I8_D. x_scales [N], w_scales [L] FP32. Y [N, L] of element type `ytype`, row n at Y + n ldy,
- *   any pitch and element alignment. 1 <= L < 2^31, 0 <= N < 2^31 (N = 0: nothing is done). A NaN scale stays
+ *   any pitch and element alignment. 1 <= L < 2^31, 0 <= N < 2^31 (N = 0: nothing is done), fewer than 2^30
+ *   tiles of 64 x 64 results. A NaN scale stays
  *   in its row or column. The workspace holds the sums of runs of K where there are few results; its size is 0 where none is
  *   needed (it may be NULL then), and for unsupported shapes.
  * elmo_i8_quantize makes such rows from x [N, D] (element type `type`, 16-byte aligned rows at pitch ldx):

@@ -664,11 +664,12 @@ def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
     a whole number, or a CUDA int64 tensor of one element that is read when the work runs (for recorded graphs). out = x
     or out = residual writes over it. See elmo_dropout in elmo_xmc.h."""
     e = _etype(x)
-    D, ld, matrix = x.shape[-1], 0, x.dim() == 2
+    matrix = x.dim() == 2
     if matrix:
         T, D, ld = _rows("x", x)
     elif x.dim() == 1 and x.is_cuda and x.is_contiguous():
-        T, ld = 1, D
+        T, D = 1, x.shape[0]
+        ld = D
     else:
         raise ValueError("x must be a 2-D CUDA tensor, or a contiguous 1-D one")
 

@@ -684,6 +684,7 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   LinearGradLayout s{};
   const int cus = device_cus();
   const int64_t whole = ceil_div(V, 256);   // pieces are multiples of 256 labels
+  if (chunk > V) chunk = V;
   int64_t most = chunk > 0 ? ceil_div(chunk, 256) : (int64_t(1) << 27) / N / 256;
   most = most < 1 ? 1 : (most > whole ? whole : most);
   if (most > MAX_PIECE / 256) most = MAX_PIECE / 256;

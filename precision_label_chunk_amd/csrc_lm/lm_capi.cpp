@@ -39,14 +39,14 @@ int check_linear(int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw
   if (N < 0 || N >= (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (D < 32 || D % 32 != 0 || D > ELMO_MAX_LINEAR_D || M < 0 || M > ELMO_MAX_GIVEN) return ELMO_ESHAPE;
   if (ldx < D || ldw < D || ldx > MAX_LINEAR_LD || ldw > MAX_LINEAR_LD) return ELMO_ESHAPE;
-  if (((N + 63) / 64) * ((V + 63) / 64) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (((N + 63) / 64) * ((V + 63) / 64) >= (int64_t(1) << 30)) return ELMO_ESHAPE;   // (tiles are counted in 31 bits)
   return ELMO_OK;
 }
 
 int check_i8(int64_t N, int64_t L, int D) {
   if (N < 0 || N >= (int64_t(1) << 31) || L < 1 || L >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (D < 64 || D % 64 != 0 || D > ELMO_MAX_I8_D) return ELMO_ESHAPE;
-  if (((N + 63) / 64) * ((L + 63) / 64) >= (int64_t(1) << 31)) return ELMO_ESHAPE;
+  if (((N + 63) / 64) * ((L + 63) / 64) >= (int64_t(1) << 30)) return ELMO_ESHAPE;
   return ELMO_OK;
 }
 

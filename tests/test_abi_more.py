@@ -26,7 +26,8 @@ def test_linear_logprobs(L):
     for t in (0, 3, -1):
         assert call(t=t) == -3, t
     for bad in (dict(N=-1), dict(N=2**31), dict(V=0), dict(V=2**31), dict(D=0), dict(D=48), dict(D=65568, ldx=65568, ldw=65568), dict(ldx=63),
-                dict(ldw=32), dict(ldx=1 << 22), dict(ldw=1 << 22), dict(M=65), dict(M=-1), dict(N=2**31 - 1, V=2**31 - 1)):
+                dict(ldw=32), dict(ldx=1 << 22), dict(ldw=1 << 22), dict(M=65), dict(M=-1), dict(N=2**31 - 1, V=2**31 - 1),
+                dict(N=1 << 21, V=1 << 21)):
         assert call(**bad) == -2, bad
     for bad in (dict(X=None), dict(W=None), dict(ids=None), dict(logp=None), dict(m=None), dict(s=None), dict(X=Q), dict(W=Q), dict(ldx=68),
                 dict(ldw=68), dict(ids=ODD), dict(logp=Q), dict(m=ODD), dict(s=ODD)):
@@ -59,6 +60,7 @@ def test_linear_logprobs_backward(L):
     assert f(0, 100, 64, 1, 0, 1, 1) == 0 and f(2, 100, 64, 1, -1, 1, 1) == 0 and f(2, 100, 40, 1, 0, 1, 1) == 0
     # a piece of 2^27 gradient codes at most, partial sums beside it; less with smaller pieces
     assert f(16384, 1 << 20, 768, 1, 0, 1, 1) < 2 * 2**27 + 64 * 16384 * 768 * 4
+    assert f(5, 100, 64, 1, 2**63 - 1, 1, 1) == f(5, 100, 64, 1, 100, 1, 1)
     assert f(16384, 1 << 20, 768, 1, 1024, 1, 1) < f(16384, 1 << 20, 768, 1, 0, 1, 1)
 
 
