@@ -2,7 +2,9 @@
 // entropy of a linear head whose logits are never kept.
 //
 // Forward: Z = X W^T tile by tile (256 labels x 256 rows, or less); each wave reduces its labels to a maximum and a
-// sum of e^(z - max) per row (8 bytes for 128 logits) and picks the given labels' logits out. A second kernel joins the parts of a row.
+// sum of e^(z - max) per row (8 bytes for 128 logits) and picks the given labels' logits out. 4,096 x 131,072 x 768:
+// 760 us, 1.08 PFLOP/s (the library's product alone 720); a tile of 24 stages takes 19 us and its exponentials, at a
+// quarter of the vector rate, 5. One row: 32 us, 6.3 TB/s of weights. A second kernel joins the parts of a row.
 //
 // Backward, a piece of the vocabulary at a time: the piece's logits again, as G = c_n p + (given labels'
 // gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch. G is the one
@@ -11,7 +13,7 @@
 // keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
 // a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows G
 // is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average their roundings, and
-// memory bounds such products.
+// memory bounds such products. 4,096 x 131,072 x 768: 2.4 ms, 1.0 PFLOP/s over the three products.
 #include "tile_shapes.hpp"
 
 namespace elmo {
@@ -677,7 +679,9 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 
 // The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache), the shapes of its
 // tiles and the runs, by the time they are expected to take: more pieces fill the device's last round better or
-// worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch).
+// worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch). Both
+// products share a launch, or each has its own with its own shape (few rows: dW in the large shape, dX in the
+// medium one take 98 + 71 us at 2 x 365,721 x 576, one launch in the medium shape 227).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
@@ -698,26 +702,40 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
     const int64_t n = labels < V ? labels : V, xst = ceil_div(n, 32);
     double logits;
     const int ls = logits_shape(N, n, D, cus, &logits);
+    // each product by itself in its best shape and runs, and both in one launch of one shape
+    struct Best { double us = 0.0; int shape = 0, slots = 1; } bw, bx;
+    auto take = [&](double us, int w_shape, int x_shape, int64_t ws, int64_t xs) {
+      us = (us + logits + 8.0) * (double)used;
+      if (least > 0.0 && us >= least) return;
+      least = us;
+      s.piece = labels; s.x_slots = (int)xs; s.w_slots = (int)ws; s.logits = ls; s.w_shape = w_shape; s.x_shape = x_shape;
+    };
     for (int k = 0; k < SHAPE_COUNT; ++k) {
       const ShapeCost& c = SHAPES[k];
       const int64_t dt = ceil_div(D, c.size), wt = need_dw ? ceil_div(n, c.size) * dt : 0, xt = need_dx ? ceil_div(x_rows, c.size) * dt : 0;
       const int64_t most_units = 2 * (int64_t)cus * c.blocks;
       if (k > 0 && N >= 1024 && n >= 16384) break;         // (the large shape's)
+      int h, l;
       for (int64_t ws = 1; ws <= 16; ws *= 2) {
         if (ws > 1 && (!need_dw || s.planes > 1 || ws * 2 > wst || wt * ws > most_units)) break;
+        const double sum_w = ws > 1 ? 2.0 + (double)(ws + 1) * n * D * 4e-6 / 5.0 : 0.0;
+        const int64_t w_stages = s.planes * ceil_div(wst, ws);
+        if (need_dw) {
+          const double us = products_time(c, wt * ws, w_stages, 0, 0, false, cus, &h, &l) + sum_w;
+          if (bw.us == 0.0 || us < bw.us) bw = Best{us, k, (int)ws};
+        }
         for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512}) {
           if (xs > 1 && (!need_dx || xs * 4 > xst || xt * xs > most_units)) break;
-          int h, l;
-          double us = products_time(c, wt * ws, s.planes * ceil_div(wst, ws), xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + logits + 8.0;
-          if (ws > 1) us += 2.0 + (double)(ws + 1) * n * D * 4e-6 / 5.0;
-          us = us * (double)used + (double)xs * (rd + 0.02);   // (and a run's share of its sum)
-          if (least == 0.0 || us < least) {
-            least = us;
-            s.piece = labels; s.x_slots = (int)xs; s.w_slots = (int)ws; s.logits = ls; s.shape = k;
+          const double sum_x = (double)xs * (rd + 0.02) / (double)used;      // (and a run's share of its sum)
+          if (need_dx && ws == 1) {
+            const double us = products_time(c, 0, 0, xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + sum_x;
+            if (bx.us == 0.0 || us < bx.us) bx = Best{us, k, (int)xs};
           }
+          take(products_time(c, wt * ws, w_stages, xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + sum_w + sum_x, k, k, ws, xs);
         }
       }
     }
+    if (need_dw && need_dx && bw.shape != bx.shape) take(bw.us + bx.us + 4.0, bw.shape, bx.shape, bw.slots, bx.slots);
   }
   s.x_per = ceil_div(ceil_div(s.piece < V ? s.piece : V, 32), s.x_slots) * 32;
   s.x_slots = (int)ceil_div(s.piece < V ? s.piece : V, s.x_per);
@@ -759,25 +777,34 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
       hipLaunchKernelGGL((k_lin_grad_logits<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, g);
     });
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
-    const ShapeCost& cost = SHAPES[s.shape];
     ProductArgs p{};
     p.X = (const char*)c.X; p.ldx = 2 * c.ldx; p.W = (const char*)c.W; p.ldw = 2 * c.ldw; p.G = ws + s.G; p.ldg = 2 * s.piece;
-    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.d_tiles = (int)ceil_div(c.D, cost.size); p.inv = k.inv;
+    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.inv = k.inv;
     p.cols = ceil_div(v1 - v0, 32) * 32;                   // (G is zero behind the last label, up to its tile's end)
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
     p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0; p.xpart = (float*)(ws + s.xpart);
-    p.row_tiles = (int)ceil_div(s.planes * c.N, cost.size);
-    p.w_units = c.dW ? (int)ceil_div(v1 - v0, cost.size) * p.d_tiles * p.w_slots : 0;
-    p.x_units = c.dX ? p.row_tiles * p.d_tiles * p.x_slots : 0;
-    const unsigned grid = blocks_for(s.shape, (int64_t)p.w_units + p.x_units, cus);
-    if ((int64_t)p.w_units + p.x_units <= grid) p.x_light = 1;   // a unit for each block
-    else products_time(cost, p.w_units, s.planes * ceil_div(s.w_per, 32), p.x_units, ceil_div(s.x_per, 32), s.piece < c.V, cus, &p.x_heavy, &p.x_light);
-    with_shape(s.shape, [&](auto shape) {
-      typedef decltype(shape) S;
-      hipLaunchKernelGGL((k_lin_products<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, p);
-    });
-    if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
+    auto launch = [&](int number, bool dw, bool dx) {
+      const ShapeCost& cost = SHAPES[number];
+      ProductArgs q = p;
+      q.d_tiles = (int)ceil_div(c.D, cost.size);
+      q.row_tiles = (int)ceil_div(s.planes * c.N, cost.size);
+      q.w_units = dw ? (int)ceil_div(v1 - v0, cost.size) * q.d_tiles * q.w_slots : 0;
+      q.x_units = dx ? q.row_tiles * q.d_tiles * q.x_slots : 0;
+      const unsigned grid = blocks_for(number, (int64_t)q.w_units + q.x_units, cus);
+      if ((int64_t)q.w_units + q.x_units <= grid) q.x_light = 1;   // a unit for each block
+      else products_time(cost, q.w_units, s.planes * ceil_div(s.w_per, 32), q.x_units, ceil_div(s.x_per, 32), s.piece < c.V, cus, &q.x_heavy, &q.x_light);
+      with_shape(number, [&](auto shape) {
+        typedef decltype(shape) S;
+        hipLaunchKernelGGL((k_lin_products<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, q);
+      });
+      return hipGetLastError() == hipSuccess;
+    };
+    if (c.dW && c.dX && s.w_shape != s.x_shape) {
+      if (!launch(s.w_shape, true, false) || !launch(s.x_shape, false, true)) return ELMO_EHIP_;
+    } else if (!launch(c.dW ? s.w_shape : s.x_shape, c.dW != nullptr, c.dX != nullptr)) {
+      return ELMO_EHIP_;
+    }
     // the runs of dW summed, and those of dX behind the last piece
     SumArgs w{}, x{};
     if (c.dW && p.w_slots > 1) w = SumArgs{p.wpart, p.cols * c.D, v0, v1 - v0, p.w_slots, c.D, p.dW};

@@ -45,7 +45,7 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
 struct LinearGradLayout {
   int64_t piece, x_per, w_per;                             // labels per piece; labels / tokens per run
   int x_slots, w_slots;                                    // runs
-  int logits, shape;                                       // tile shapes of the logits and of the products
+  int logits, w_shape, x_shape;                            // tile shapes of the logits, of dW and of dX
   int planes;                                              // 16-bit numbers whose sum holds an element of G
   size_t most, inv, coef, up, G, xpart, wpart, total;
 };
