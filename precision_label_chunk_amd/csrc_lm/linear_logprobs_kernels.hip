@@ -3,17 +3,16 @@
 //
 // Forward: Z = X W^T tile by tile (256 labels x 256 rows, or less); each wave reduces its labels to a maximum and a
 // sum of e^(z - max) per row (8 bytes for 128 logits) and picks the given labels' logits out. 4,096 x 131,072 x 768:
-// 760 us, 1.08 PFLOP/s (the library's product alone 720); a tile of 24 stages takes 19 us and its exponentials, at a
-// quarter of the vector rate, 5. One row: 32 us, 6.3 TB/s of weights. A second kernel joins the parts of a row.
+// 720 us, 1,145 TFLOP/s (the library's product alone 700). One row of 131,072 x 768: 40 us, 5.0 TB/s of weights. A second kernel joins the parts of a row.
 //
 // Backward, a piece of the vocabulary at a time: the piece's logits again, as G = c_n p + (given labels'
-// gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch. G is the one
+// gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch or two. G is the one
 // rounding below 32 bits: half a unit of its type per element, of its own size (c p of a label that was
 // not given, c p + g of one that was, added before it is rounded, so that a label of probability near 1
 // keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
 // a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows G
 // is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average their roundings, and
-// memory bounds such products. 4,096 x 131,072 x 768: 2.4 ms, 1.0 PFLOP/s over the three products.
+// memory bounds such products. 4,096 x 131,072 x 768: 2.5 ms, 980 TFLOP/s over the three products.
 #include "tile_shapes.hpp"
 
 namespace elmo {
@@ -680,8 +679,9 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 // The piece (the caller's, or at most 2^27 gradient codes: 256 MiB, about the last-level cache), the shapes of its
 // tiles and the runs, by the time they are expected to take: more pieces fill the device's last round better or
 // worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch). Both
-// products share a launch, or each has its own with its own shape (few rows: dW in the large shape, dX in the
-// medium one take 98 + 71 us at 2 x 365,721 x 576, one launch in the medium shape 227).
+// products share a launch, or each has its own with its own shape (few rows, where memory bounds them: dW in the large
+// shape, dX in the medium one take 156 us at 2 x 365,721 x 576, one launch 217; 93 and 139 at 64 x 131,072 x 768). dX goes
+// first: the gradient codes' pass has just read W (behind dW: 210 and 133 us).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
@@ -801,7 +801,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
       return hipGetLastError() == hipSuccess;
     };
     if (c.dW && c.dX && s.w_shape != s.x_shape) {
-      if (!launch(s.w_shape, true, false) || !launch(s.x_shape, false, true)) return ELMO_EHIP_;
+      if (!launch(s.x_shape, false, true) || !launch(s.w_shape, true, false)) return ELMO_EHIP_;
     } else if (!launch(c.dW ? s.w_shape : s.x_shape, c.dW != nullptr, c.dX != nullptr)) {
       return ELMO_EHIP_;
     }
