@@ -266,12 +266,12 @@ __global__ __launch_bounds__(COEF_THREADS) void k_lin_coef(CoefArgs a) {
   }
   v = block_max(v, s);
   // unit: what becomes 1 (the largest given gradient, or else the bound); FP16: times the power of two
-  // that brings the bound into [2^14, 2^15)
+  // that brings the bound into [2^14, 2^15), as far as its inverse is finite
   float unit = v.x > 0.0f ? v.x : v.y;
   unit = fminf(fmaxf(unit, 1e-30f), 1e30f);
   if (a.f16) {
     const float ratio = fmaxf(v.y / unit, 1e-30f);
-    unit = ldexpf(unit, __builtin_amdgcn_frexp_expf(ratio) - 15);
+    unit = fmaxf(ldexpf(unit, __builtin_amdgcn_frexp_expf(ratio) - 15), 1.17549435e-38f);   // (2^-126)
   }
   const float scale = 1.0f / unit;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = unit;
