@@ -103,12 +103,15 @@ __global__ __launch_bounds__(256) void k_i8_quantize(const typename E::raw* x, i
 
 template <typename E>
 static void quantize_as(const void* x, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st) {
-  const typename E::raw* p = (const typename E::raw*)x;
   // a wave holds 2048 features of a row in registers, a block 8192
-  if (D <= 2048)
-    hipLaunchKernelGGL((k_i8_quantize<E, 64>), dim3((unsigned)ceil_div(N, 4)), dim3(256), 0, st, p, N, D, ldx, codes, scales);
-  else
-    hipLaunchKernelGGL((k_i8_quantize<E, 256>), dim3((unsigned)N), dim3(256), 0, st, p, N, D, ldx, codes, scales);
+  const int64_t rows = D <= 2048 ? 4 : 1, most = MAX_THREADS / 256 * rows;
+  for (int64_t n0 = 0; n0 < N; n0 += most) {
+    const int64_t n = N - n0 < most ? N - n0 : most;
+    const typename E::raw* p = (const typename E::raw*)x + n0 * ldx;
+    const dim3 grid((unsigned)ceil_div(n, rows));
+    if (rows == 4) hipLaunchKernelGGL((k_i8_quantize<E, 64>), grid, dim3(256), 0, st, p, n, D, ldx, codes + n0 * D, scales + n0);
+    else hipLaunchKernelGGL((k_i8_quantize<E, 256>), grid, dim3(256), 0, st, p, n, D, ldx, codes + n0 * D, scales + n0);
+  }
 }
 
 int run_i8_quantize(const void* x, int type, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales, hipStream_t st) {
@@ -476,9 +479,14 @@ static int matmul_as(I8Args& a, int shape, hipStream_t st) {
     // Rows shared by a block: for labels that fill the device several times over, fewer of them where the rows fit
     // one panel (131,072 labels, 16 rows x 768: 24 us against 30 split; 1 row x 4096: 113 against 90)
     if (tiles >= 64 * cus || (tiles >= 16 * cus && a.D <= 1024)) {
-      const dim3 grid((unsigned)ceil_div(a.L, 64 * ROWS_LT));
-      if (a.N <= 16) hipLaunchKernelGGL((k_i8_rows<E, 1>), grid, dim3(256), 0, st, a);
-      else hipLaunchKernelGGL((k_i8_rows<E, 2>), grid, dim3(256), 0, st, a);
+      const int64_t most = MAX_THREADS / 256 * (64 * ROWS_LT);
+      for (int64_t l0 = 0; l0 < a.L; l0 += most) {
+        I8Args b = a;
+        b.W += l0 * a.D; b.sw += l0; b.Y = (typename E::raw*)a.Y + l0; b.L = a.L - l0 < most ? a.L - l0 : most;
+        const dim3 grid((unsigned)ceil_div(b.L, 64 * ROWS_LT));
+        if (a.N <= 16) hipLaunchKernelGGL((k_i8_rows<E, 1>), grid, dim3(256), 0, st, b);
+        else hipLaunchKernelGGL((k_i8_rows<E, 2>), grid, dim3(256), 0, st, b);
+      }
     } else {
       const dim3 grid((unsigned)tiles);
 #define ELMO_I8_SPLIT(NT, KS) hipLaunchKernelGGL((k_i8_rows_split<E, NT, KS>), grid, dim3(64 * KS), 0, st, a)

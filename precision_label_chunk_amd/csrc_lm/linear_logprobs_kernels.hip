@@ -149,13 +149,13 @@ __global__ __launch_bounds__(S::THREADS, S::WAVES) void k_lin_stats(StatArgs a) 
   tile_stream<Mul, false, false, S>(job, r.first, r.step, r.end, lds);
 }
 
-// The parts of `wide` rows (a power of two up to 16) joined by a block: 1024 / wide runs of parts a row, then the runs in
+// The parts of `wide` rows from n0 on (a power of two up to 16) joined by a block: 1024 / wide runs of parts a row, then the runs in
 // the order of a tree.
-__global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t parts, int64_t N, int64_t V, int wide, const int32_t* ids,
+__global__ __launch_bounds__(1024) void k_lin_join(const float2* part, int64_t parts, int64_t n0, int64_t N, int64_t V, int wide, const int32_t* ids,
                                                    int M, const float* given, float* logp, float* row_max, float* log_sum) {
   __shared__ float2 joined[1024];
   const int tid = (int)threadIdx.x, x = tid & (wide - 1), y = tid / wide, runs = 1024 / wide;
-  const int64_t n = (int64_t)blockIdx.x * wide + x;
+  const int64_t n = n0 + (int64_t)blockIdx.x * wide + x;
   float top = -__builtin_inff(), sum = 0.0f;
   auto add = [&](float m, float s) {
     const float hi = fmaxf(top, m);
@@ -636,8 +636,12 @@ int run_linear_logprobs(const void* X, const void* W, int type, int64_t N, int64
   if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
   int wide = 1;                                            // (few rows: more blocks, and more runs of parts in each)
   while (wide * 64 < N && wide < 16) wide *= 2;
-  hipLaunchKernelGGL(k_lin_join, dim3((unsigned)ceil_div(N, wide)), dim3(1024), 0, st, a.part, s.parts, N, V, wide, ids, M, a.given, logp,
-                     row_max, log_sum);
+  const int64_t most = MAX_THREADS / 1024;                 // blocks
+  for (int64_t n0 = 0; n0 < N; n0 += most * wide) {
+    const int64_t blocks = ceil_div(N - n0, wide);
+    hipLaunchKernelGGL(k_lin_join, dim3((unsigned)(blocks < most ? blocks : most)), dim3(1024), 0, st, a.part, s.parts, n0, N, V, wide, ids,
+                       M, a.given, logp, row_max, log_sum);
+  }
   return hipGetLastError() == hipSuccess ? ELMO_OK_ : ELMO_EHIP_;
 }
 

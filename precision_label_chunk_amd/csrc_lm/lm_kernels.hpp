@@ -35,6 +35,9 @@ WgradLayout wgrad_layout(int64_t T, int O, int D);
 int run_ckpt8_wgrad(const void* dY, int64_t ldy, const uint8_t* codes, const uint8_t* scales, int64_t T, int O, int D,
                     float* dW, int accumulate, const WgradLayout& s, void* workspace, hipStream_t st);
 
+// threads of one launch: a grid of 2^32 or more is cut short without an error
+constexpr int64_t MAX_THREADS = int64_t(1) << 31;
+
 // log probabilities of given labels from features and weights, and the gradients of both
 // (shapes: the numbers of their tile shapes)
 struct LinearLayout { int shape; int64_t parts; size_t part, given, total; };
