@@ -412,9 +412,10 @@ struct ProductArgs {
   // dW: the tokens in w_slots runs of w_per; one run goes to the result, several to `wpart`
   int w_units, w_slots; int64_t w_per;
   float* wpart; OutArgs dW;
-  // dX: the piece's labels in x_slots runs of x_per, each added to its partial sum
+  // dX: the piece's labels in x_slots runs of x_per, each added to its partial sum; or (xpart NULL) one run over all
+  // labels, which goes to the result
   int x_units, x_slots, x_heavy, x_light, first; int64_t x_per;
-  float* xpart;
+  float* xpart; OutArgs dX;
 };
 
 __device__ __forceinline__ void store4(const OutArgs& o, int64_t row, int64_t col, f32x4_t v) {
@@ -519,8 +520,8 @@ struct FeatureJob : ProductArgs {
     int dt, nt, slot;
     place(u, dt, nt, slot);
     const int64_t rows = planes * N;
-    return store_tile<S>(OutArgs{xpart + slot * rows * D, D, T_F32_, !first}, acc, 1.0f, (int64_t)nt * S::N + S::WN_ROWS * wn, rows,
-               dt * S::M + S::WM_ROWS * wm, D, lane, lds);
+    const OutArgs o = xpart ? OutArgs{xpart + slot * rows * D, D, T_F32_, !first} : dX;
+    return store_tile<S>(o, acc, xpart ? 1.0f : *inv, (int64_t)nt * S::N + S::WN_ROWS * wn, rows, dt * S::M + S::WM_ROWS * wm, D, lane, lds);
   }
 };
 
@@ -730,7 +731,7 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
         }
         for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512}) {
           if (xs > 1 && (!need_dx || xs * 4 > xst || xt * xs > most_units)) break;
-          const double sum_x = (double)xs * (rd + 0.02) / (double)used;      // (and a run's share of its sum)
+          const double sum_x = s.planes == 1 && used == 1 && xs == 1 ? 0.0 : 5.0 + (double)xs * (rd + 0.02) / (double)used;   // (the sum of the runs: a launch more)
           if (need_dx && ws == 1) {
             const double us = products_time(c, 0, 0, xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + sum_x;
             if (bx.us == 0.0 || us < bx.us) bx = Best{us, k, (int)xs};
@@ -745,13 +746,14 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   s.x_slots = (int)ceil_div(s.piece < V ? s.piece : V, s.x_per);
   s.w_per = ceil_div(wst, s.w_slots) * 32;
   s.w_slots = (int)ceil_div(N, s.w_per);
+  s.sum_x = s.planes > 1 || s.x_slots > 1 || s.piece < V;
   size_t at = 0;
   s.most = at; at += up256(256 * 8);
   s.inv = at; at += 256;
   s.coef = at; at += up256((size_t)N * 8);
   s.up = at; at += up256((size_t)N * (M > 0 ? M : 1) * 4);
   s.G = at; at += up256((size_t)x_rows * s.piece * 2);
-  s.xpart = at; if (need_dx) at += up256((size_t)s.x_slots * x_rows * D * 4);
+  s.xpart = at; if (need_dx && s.sum_x) at += up256((size_t)s.x_slots * x_rows * D * 4);
   s.wpart = at; if (need_dw && s.w_slots > 1) at += up256((size_t)s.w_slots * s.piece * D * 4);
   s.total = at;
   return s;
@@ -787,7 +789,8 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     p.cols = ceil_div(v1 - v0, 32) * 32;                   // (G is zero behind the last label, up to its tile's end)
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
-    p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0; p.xpart = (float*)(ws + s.xpart);
+    p.x_per = s.x_per; p.x_slots = (int)ceil_div(p.cols, s.x_per); p.first = v0 == 0;
+    p.xpart = s.sum_x ? (float*)(ws + s.xpart) : nullptr; p.dX = OutArgs{c.dX, c.lddx, c.dx_type, 0};
     auto launch = [&](int number, bool dw, bool dx) {
       const ShapeCost& cost = SHAPES[number];
       ProductArgs q = p;
@@ -812,7 +815,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     // the runs of dW summed, and those of dX behind the last piece
     SumArgs w{}, x{};
     if (c.dW && p.w_slots > 1) w = SumArgs{p.wpart, p.cols * c.D, v0, v1 - v0, p.w_slots, c.D, p.dW};
-    if (c.dX && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.planes * s.x_slots, c.D, OutArgs{c.dX, c.lddx, c.dx_type, 0}};
+    if (c.dX && s.sum_x && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.planes * s.x_slots, c.D, p.dX};
     const unsigned wb = w.rows ? sum_grid(w.rows, c.D) : 0, xb = x.rows ? sum_grid(x.rows, c.D) : 0;
     if (wb + xb == 0) continue;
     if (w.slots > 32 || x.slots > 32) hipLaunchKernelGGL(k_lin_sum<16>, dim3(wb + xb), dim3(1024), 0, st, w, x, (int)wb, (const float*)k.inv);

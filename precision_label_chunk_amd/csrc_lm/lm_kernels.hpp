@@ -50,6 +50,7 @@ struct LinearGradLayout {
   int x_slots, w_slots;                                    // runs
   int logits, w_shape, x_shape;                            // tile shapes of the logits, of dW and of dX
   int planes;                                              // 16-bit numbers whose sum holds an element of G
+  bool sum_x;                                              // dX is the sum of several runs, pieces or planes
   size_t most, inv, coef, up, G, xpart, wpart, total;
 };
 struct LinearGradCall {

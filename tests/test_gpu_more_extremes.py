@@ -1,4 +1,4 @@
-"""Gradients from features for upstream gradients of zero and at the ends of binary32's range.
+"""Gradients from features for upstream gradients of zero and at the ends of binary32's range, and where dX needs no sum.
 
 Tolerances of the gradients: those of the tests of ordinary sizes. FP16 holds G scaled by a power of two of at most 2^126, so
 that each element is off by a further 2^-25 2^-126 at most, half the spacing of FP16's smallest numbers."""
@@ -38,3 +38,17 @@ def test_upstream_at_the_ends_of_the_range(elmo, dtype, scale):  # noqa: F811
             tX, tW = tX + 2.0**-151 * W.cpu().double().abs().sum(0), tW + 2.0**-151 * X.cpu().double().abs().sum(0)
         _near(dx, dX, tX + HALF[F32] * (dX.abs() + tX) + LEAST[F32], "dX")
         _near(dw, dW, tW + 2 * HALF[F32] * (dW.abs() + tW) + 2 * LEAST[F32], "dW")
+
+
+@pytest.mark.parametrize("out", [F32, BF, HF])
+@pytest.mark.parametrize("N,V,D", [(129, 31, 32), (200, 500, 512), (701, 1116, 1216), (4096, 4096, 4096)])
+def test_dx_of_one_run(elmo, N, V, D, out):  # noqa: F811
+    """Few labels for the rows: dX comes from one run over them, straight to its place, in rows of a wider buffer."""
+    X, W, ids, up, dlse = _case(N, V, D, 1, BF, seed=N)
+    r = elmo.linear_logprobs(X, W, ids)
+    buf = torch.full((N + 1, D + 16), 7.0, device="cuda", dtype=out)
+    dx, dw = elmo.linear_logprobs_backward(X, W, ids, r, up, dlse=dlse, dx=buf[:N, :D])
+    dX, dW, tX, tW = _gradients(X, W, ids, up, dlse)
+    _near(dx, dX, tX + HALF[out] * (dX.abs() + tX) + LEAST[out], "dX")
+    _near(dw, dW, tW + 2 * HALF[BF] * (dW.abs() + tW) + 2 * LEAST[BF], "dW")
+    assert bool((buf[:N, D:] == 7.0).all()) and bool((buf[N] == 7.0).all())
