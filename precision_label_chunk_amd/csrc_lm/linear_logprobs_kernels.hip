@@ -3,7 +3,8 @@
 //
 // Forward: Z = X W^T tile by tile (256 labels x 256 rows, or less); each wave reduces its labels to a maximum and a
 // sum of e^(z - max) per row (8 bytes for 128 logits) and picks the given labels' logits out. 4,096 x 131,072 x 768:
-// 720 us, 1,145 TFLOP/s (the library's product alone 700). One row of 131,072 x 768: 40 us, 5.0 TB/s of weights. A second kernel joins the parts of a row.
+// 720 us, 1,145 TFLOP/s (the library's product alone 700). One row of 131,072 x 768: 40 us, 5.0 TB/s of weights. A
+// second kernel joins the parts of a row.
 //
 // Backward, a piece of the vocabulary at a time: the piece's logits again, as G = c_n p + (given labels'
 // gradients) in 16 bits in the workspace, then dX += G W and dW = G^T X in one launch or two. G is the one
@@ -686,7 +687,8 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 // worse, runs fill it with less in each, but are summed apart (dX by adding to memory, dW by another launch). Both
 // products share a launch, or each has its own with its own shape (few rows, where memory bounds them: dW in the large
 // shape, dX in the medium one take 156 us at 2 x 365,721 x 576, one launch 217; 93 and 139 at 64 x 131,072 x 768). dX goes
-// first: the gradient codes' pass has just read W (behind dW: 210 and 133 us).
+// first: the gradient codes' pass has just read W (behind dW: 210 and 133 us). One run over all labels in one plane
+// needs no sum of dX and no launch for it (512 x 1,000 x 256, loss and gradient: 43 us against 46.5).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {

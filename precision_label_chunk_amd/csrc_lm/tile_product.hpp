@@ -17,8 +17,9 @@
 //
 // What bounds it: at 4,096 x 16,384 x 4,096 the matrix cores are busy 67 to 73% of the cycles and the card lowers its
 // clock to 1.5 GHz for it: logits with their softmax 1,243 TFLOP/s (the library's product alone: 1,533), 8-bit integers
-// at 16,384 x 4,096 x 4,096 2,190 TOP/s (2,180 to 2,230). LDS is in use a quarter of the time. Two blocks of 128 x 256 per compute unit, four waves of 128 x 128, more stages ahead, wave
-// priorities and fixed orders of reads and products were built and are as fast or slower (down to 0.6 of the rate).
+// at 16,384 x 4,096 x 4,096 2,190 TOP/s (2,180 to 2,230). LDS is in use a quarter of the time. Two blocks of 128 x 256
+// per compute unit, four waves of 128 x 128, more stages ahead, wave priorities and fixed orders of reads and
+// products were built and are as fast or slower (down to 0.6 of the rate).
 #pragma once
 #include "elem_types.hpp"
 
