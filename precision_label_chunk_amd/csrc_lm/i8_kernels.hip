@@ -442,6 +442,19 @@ __global__ __launch_bounds__(64 * KS) void k_i8_rows_split(I8Args a) {
 
 constexpr int I8_ROWS = 32;                                // rows that the streaming kernel takes
 
+// The time of a stage by the blocks that share a compute unit (small tiles: 0.14 us alone, 0.22 and 0.5 with two and
+// four). By the device's share, as for 16-bit products, 133 x 8,935 x 4,352 takes 25.3 us and 512 x 4,096 x 4,096 24.2;
+// by this 19.8 and 20.8 (but gradients of 333 x 32,003 x 1,024 in 16 bits 148 instead of 143).
+static const ShapeCost I8_SHAPES[SHAPE_COUNT] = {{LargeTiles::M, LargeTiles::BLOCKS, 5.5, 0.5, 0.8},
+                                                 {MediumTiles::M, MediumTiles::BLOCKS, 3.5, 0.2, 0.58},
+                                                 {SmallTiles::M, SmallTiles::BLOCKS, 2.5, 0.15, 0.52}};
+static double i8_stage_time(const ShapeCost& c, int64_t units, int cus) {
+  const int64_t each = ceil_div(units, cus);
+  const double part = c.full / c.blocks, shared = part * (double)(each < c.blocks ? each : c.blocks);
+  if (each > 1) return c.alone > shared ? c.alone : shared;
+  return part > c.alone ? c.alone + (part - c.alone) * (double)units / cus : c.alone;
+}
+
 // The tile shape and the runs of K by the time they are expected to take; a run keeps 4 stages.
 I8Layout i8_layout(int64_t N, int64_t L, int D) {
   I8Layout s{};
@@ -453,11 +466,11 @@ I8Layout i8_layout(int64_t N, int64_t L, int D) {
     const int cus = device_cus();
     double least = 0.0;
     for (int k = 0; k < SHAPE_COUNT; ++k) {
-      const ShapeCost& c = SHAPES[k];
+      const ShapeCost& c = I8_SHAPES[k];
       const int64_t tiles = ceil_div(L, c.size) * ceil_div(N, c.size);
       for (int64_t slots = 1; slots <= 64; slots *= 2) {
         if (slots > 1 && (slots * 4 > all || tiles * slots > 2 * (int64_t)cus * c.blocks)) break;
-        double us = units_time(c, tiles * slots, ceil_div(all, slots), cus);
+        double us = units_time(c, tiles * slots, ceil_div(all, slots), i8_stage_time(c, tiles * slots, cus), cus);
         if (slots > 1) us += 3.0 + (double)(2 * slots) * N * L * 4e-6 / 5.0;
         if (least == 0.0 || us < least) {
           least = us;

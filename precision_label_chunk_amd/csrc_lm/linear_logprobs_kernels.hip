@@ -595,7 +595,8 @@ static int logits_shape(int64_t N, int64_t V, int D, int cus, double* us) {
   int best = 0;
   for (int k = 0; k < SHAPE_COUNT; ++k) {
     const int m = SHAPES[k].size;
-    const double t = units_time(SHAPES[k], ceil_div(N, m) * ceil_div(V, m), D / 32, cus) + (double)N * V / m * 32e-6 / 5.0;   // (and the join)
+    const int64_t units = ceil_div(N, m) * ceil_div(V, m);
+    const double t = units_time(SHAPES[k], units, D / 32, stage_time(SHAPES[k], units, cus), cus) + (double)N * V / m * 32e-6 / 5.0;   // (and the join)
     if (k == 0 || t < *us) {
       best = k;
       *us = t;

@@ -21,10 +21,10 @@ static inline double stage_time(const ShapeCost& c, int64_t units, int cus) {
   const double most = (double)cus * c.blocks, share = (double)units / most;
   return c.alone + (c.full - c.alone) * (share < 1.0 ? share : 1.0);
 }
-static inline double units_time(const ShapeCost& c, int64_t units, int64_t stages, int cus) {
+static inline double units_time(const ShapeCost& c, int64_t units, int64_t stages, double stage, int cus) {
   // (a last round that is not full ends sooner: the clock rises)
   const double blocks = (double)cus * c.blocks, rounds = (double)units / blocks, whole = (double)ceil_div(units, (int64_t)cus * c.blocks);
-  return (rounds < 1.0 ? 1.0 : 0.5 * (rounds + whole)) * (c.ends + (double)stages * stage_time(c, units, cus));
+  return (rounds < 1.0 ? 1.0 : 0.5 * (rounds + whole)) * (c.ends + (double)stages * stage);
 }
 static inline unsigned blocks_for(int shape, int64_t units, int cus) {
   const int64_t most = (int64_t)cus * SHAPES[shape].blocks;
