@@ -357,7 +357,7 @@ int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int6
  *   dX       [N, D] of type `dx_type` (any), dW [V, D] of type `dw_type`, 16-byte aligned rows at pitches lddx,
  *            lddw; either may be NULL. accumulate: dW is added to, in binary32, and rounded once.
  * Neither overlaps another argument (dW is written while W is read). In FP16 an element of G is also off by up to 2^-39
- * of the largest |dlse| + 2 sum |dlogp| of a row.
+ * of the largest |dlse| + 2 sum |dlogp| of a row. Probabilities below 2^-126 count as 0.
  * N = 0 leaves dW zero (or as it is with accumulate). Results repeat bit for bit on one device.
  */
 size_t elmo_linear_logprobs_backward_workspace_bytes(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx,

@@ -19,6 +19,10 @@
 namespace elmo {
 
 constexpr float L2E = 1.44269502162933349609375f;          // FP32(log2 e)
+// e^(z - m) is formed as 2^(z L2E - b), b = FP32(m L2E), and what b's rounding leaves out as a factor, while |b| is below
+// FAR: the factor then is at most 2^(1/2). From 2^31 on it would leave binary32's range. Rows beyond FAR take z - m first
+// (one more operation a logit, of the waves that have such a row), rows below it keep their bits next to them.
+constexpr float FAR = 16777216.0f;
 constexpr int COEF_THREADS = 1024;
 constexpr int GROUP = 8;                                   // label tiles that are taken together over the rows
 
@@ -108,20 +112,6 @@ struct StatJob : StatArgs {
 #pragma unroll
         for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
       top = fmaxf(top, __shfl_xor(top, 32));
-      // e^(z - top) as 2^(z L2E - b), b = FP32(top L2E): what b's rounding leaves out is a factor of the sum
-      const float ref = top == -__builtin_inff() ? 0.0f : top;
-      const float b = ref * L2E, rest = __builtin_fmaf(ref, L2E, -b);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < S::MF; ++i) {
-        float s = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -b));
-        sum += s;
-      }
-      sum += __shfl_xor(sum, 32);
-      sum *= __builtin_amdgcn_exp2f(-rest);
-      if (half == 0 && n[j] < t.N) part[((int64_t)lt * 2 + wm) * t.N + n[j]] = make_float2(top, sum);
       for (int g = 0; given_here && g < M; ++g) {
         const int id = n[j] < t.N ? ids[n[j] * M + g] : -1;
         const int at = given_place<S::WM_ROWS>(id, l0, t.v1, half);
@@ -136,6 +126,29 @@ struct StatJob : StatArgs {
           if (hit) given[n[j] * M + g] = z;
         }
       }
+      float ref = top == -__builtin_inff() ? 0.0f : top;
+      const bool far = fabsf(ref) * L2E >= FAR && fabsf(ref) < __builtin_inff();
+      if (__any(far)) {
+        const float off = far ? ref : 0.0f;
+        if (far) ref = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S::MF; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] -= off;
+      }
+      // e^(z - top) as 2^(z L2E - b), b = FP32(top L2E): what b's rounding leaves out is a factor of the sum
+      const float b = ref * L2E, rest = __builtin_fmaf(ref, L2E, -b);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::MF; ++i) {
+        float s = 0.0f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], L2E, -b));
+        sum += s;
+      }
+      sum += __shfl_xor(sum, 32);
+      sum *= __builtin_amdgcn_exp2f(-rest);
+      if (half == 0 && n[j] < t.N) part[((int64_t)lt * 2 + wm) * t.N + n[j]] = make_float2(top, sum);
     }
     return n0 + S::WN_ROWS <= t.N;
   }
@@ -204,7 +217,7 @@ struct CoefArgs {
   const int32_t* ids;
   const float *row_max, *log_sum, *dlogp, *dlse;
   float2* most; int parts;                                 // maxima of runs of rows, if taken by themselves
-  float2* coef;                                            // [N]: b, c 2^(what b's rounding left out), scaled
+  float2* coef;                                            // [N]: b, c 2^(what b's rounding left out), scaled; |b| >= FAR: no such factor
   float* up;                                               // [N][M]: the given labels' gradients, scaled
   float* inv;                                              // 1 / scale
   int f16;
@@ -292,7 +305,8 @@ __global__ __launch_bounds__(COEF_THREADS) void k_lin_coef(CoefArgs a) {
   // p = 2^(z L2E - lse L2E): exact for z = lse, where 1 - p needs it
   const double bd = empty ? 0.0 : lse * (double)L2E;
   const float b = (float)bd;
-  a.coef[n] = make_float2(b, empty ? 0.0f : c * scale * __builtin_amdgcn_exp2f(-(float)(bd - (double)b)));
+  const float rest = fabsf(b) >= FAR ? 0.0f : (float)(bd - (double)b);
+  a.coef[n] = make_float2(b, empty ? 0.0f : c * scale * __builtin_amdgcn_exp2f(-rest));
 }
 
 template <class Mul>
@@ -320,6 +334,7 @@ struct GradArgs {
   int planes;                                              // 2: G as two numbers
   const int32_t* ids; int M;
   const float2* coef; const float* up;
+  const float *row_max, *log_sum;                          // of rows beyond FAR
   char* G; int64_t ldg;                                    // [N] rows of the piece's labels; bytes
 };
 
@@ -344,6 +359,15 @@ struct GradJob : GradArgs {
     }
 #pragma unroll
     for (int j = 0; j < S::NF; ++j) {
+      const bool far = fabsf(cf[j].x) >= FAR;
+      if (__any(far)) {                                    // (z - row_max) L2E - log_sum L2E
+        const float off = far ? row_max[n[j]] : 0.0f;
+        if (far) cf[j].x = log_sum[n[j]] * L2E;
+#pragma unroll
+        for (int i = 0; i < S::MF; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) acc[i][j][r] -= off;
+      }
 #pragma unroll
       for (int i = 0; i < S::MF; ++i)
 #pragma unroll
@@ -779,7 +803,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     const int64_t v1 = v0 + s.piece < c.V ? v0 + s.piece : c.V;
     GradArgs g{};
     g.t = tiles_of(s.logits, c.X, c.ldx, c.W, c.ldw, c.N, v0, v1, c.D);
-    g.planes = s.planes; g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.G = ws + s.G; g.ldg = 2 * s.piece;
+    g.planes = s.planes; g.ids = c.ids; g.M = c.M; g.coef = k.coef; g.up = k.up; g.row_max = c.row_max; g.log_sum = c.log_sum; g.G = ws + s.G; g.ldg = 2 * s.piece;
     with_shape(s.logits, [&](auto shape) {
       typedef decltype(shape) S;
       const unsigned grid = blocks_for(s.logits, (int64_t)g.t.row_tiles * g.t.label_tiles, cus);
