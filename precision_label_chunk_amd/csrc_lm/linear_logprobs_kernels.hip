@@ -14,6 +14,8 @@
 // a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows G
 // is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average their roundings, and
 // memory bounds such products. 4,096 x 131,072 x 768: 2.5 ms, 980 TFLOP/s over the three products.
+#include <cfloat>
+
 #include "tile_shapes.hpp"
 
 namespace elmo {
@@ -223,16 +225,21 @@ struct CoefArgs {
   int f16;
 };
 
-// the largest given gradient of a row, and the bound of |G| in it (finite ones only)
+// the largest given gradient of a row (of finite ones), and the bound of |G| in it: FLT_MAX where that is larger (by a factor
+// of at most 1 + 2 ELMO_MAX_GIVEN < 2^8), 0 for a row with a NaN or an infinity
 __device__ __forceinline__ float2 row_bound(const CoefArgs& a, int64_t n) {
   float most = 0.0f, all = a.dlse ? fabsf(a.dlse[n]) : 0.0f;
+  bool finite = all < __builtin_inff();
   for (int g = 0; g < a.M; ++g) {
     const int id = a.ids[n * a.M + g];                     // (both loads are on their way together)
     const float d = fabsf(a.dlogp[n * a.M + g]);
     if (id >= 0 && d < __builtin_inff()) most = fmaxf(most, d);
-    if (id >= 0) all += 2.0f * d;
+    if (id >= 0) {
+      all += 2.0f * d;
+      finite = finite && d < __builtin_inff();
+    }
   }
-  return make_float2(most, all < __builtin_inff() ? all : 0.0f);
+  return make_float2(most, finite ? fminf(all, FLT_MAX) : 0.0f);
 }
 __device__ __forceinline__ float2 block_max(float2 v, float2* s) {
 #pragma unroll
@@ -279,13 +286,13 @@ __global__ __launch_bounds__(COEF_THREADS) void k_lin_coef(CoefArgs a) {
     }
   }
   v = block_max(v, s);
-  // unit: what becomes 1 (the largest given gradient, or else the bound); FP16: times the power of two
-  // that brings the bound into [2^14, 2^15), as far as its inverse is finite
-  float unit = v.x > 0.0f ? v.x : v.y;
+  // unit: what becomes 1 (the largest given gradient, unless the bound is more than 2^60 times that; or else the
+  // bound); FP16: times the power of two that brings the bound into [2^14, 2^15), as far as its inverse is finite
+  float unit = v.x > 0.0f ? fmaxf(v.x, 0x1p-60f * v.y) : v.y;
   unit = fminf(fmaxf(unit, 1e-30f), 1e30f);
   if (a.f16) {
     const float ratio = fmaxf(v.y / unit, 1e-30f);
-    unit = fmaxf(ldexpf(unit, __builtin_amdgcn_frexp_expf(ratio) - 15), 1.17549435e-38f);   // (2^-126)
+    unit = fmaxf(ldexpf(unit, __builtin_amdgcn_frexp_expf(ratio) - (v.y == FLT_MAX ? 15 - 8 : 15)), 1.17549435e-38f);   // (2^-126)
   }
   const float scale = 1.0f / unit;
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.inv = unit;
@@ -293,20 +300,22 @@ __global__ __launch_bounds__(COEF_THREADS) void k_lin_coef(CoefArgs a) {
   if (n >= a.N) return;
   const double lse = (double)a.row_max[n] + (double)a.log_sum[n];
   const bool empty = lse == -__builtin_inf();
-  float c = a.dlse ? a.dlse[n] : 0.0f;
+  float c = a.dlse ? a.dlse[n] : 0.0f, scaled = c * scale;   // (scaled: for a sum beyond binary32's range)
   for (int g = 0; g < a.M; ++g) {
     const int id = a.ids[n * a.M + g];
     float d = 0.0f;
     if (id >= 0) d = a.dlogp[n * a.M + g];
-    if (id >= a.V) c = __builtin_nanf("");
+    if (id >= a.V) c = scaled = __builtin_nanf("");
     c -= d;
+    scaled -= d * scale;
     a.up[n * a.M + g] = empty ? 0.0f : d * scale;
   }
+  if (fabsf(c) < __builtin_inff()) scaled = c * scale;
   // p = 2^(z L2E - lse L2E): exact for z = lse, where 1 - p needs it
   const double bd = empty ? 0.0 : lse * (double)L2E;
   const float b = (float)bd;
   const float rest = fabsf(b) >= FAR ? 0.0f : (float)(bd - (double)b);
-  a.coef[n] = make_float2(b, empty ? 0.0f : c * scale * __builtin_amdgcn_exp2f(-rest));
+  a.coef[n] = make_float2(b, empty ? 0.0f : scaled * __builtin_amdgcn_exp2f(-rest));
 }
 
 template <class Mul>
