@@ -401,7 +401,7 @@ int elmo_i8_matmul(const int8_t* X, const float* x_scales, const int8_t* W, cons
  *   p        0 <= p <= 1 (1: everything is dropped).
  *   step_at  device address of a number added to `step` when the work runs (NULL: none; 8-byte aligned): a
  *            recorded graph that counts it up draws a new mask at each replay.
- *   first    the index of x[0, 0]: parts of a batch draw what the whole would.
+ *   first    the index of x[0, 0]: parts of a batch draw what the whole would. first + T D <= 2^64 - 8.
  * 0 <= T < 2^31 (0: nothing is done), 1 <= D < 2^31. No workspace.
  */
 int elmo_dropout(const void* x, int type, int64_t T, int64_t D, int64_t ldx, const void* residual, int64_t ldr, double p,

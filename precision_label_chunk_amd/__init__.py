@@ -663,6 +663,8 @@ def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
     the counter-based generator keyed by (seed, step) and their index first + t D + d; the mask is not stored. `step` is
     a whole number, or a CUDA int64 tensor of one element that is read when the work runs (for recorded graphs). out = x
     or out = residual writes over it. See elmo_dropout in elmo_xmc.h."""
+    if not 0 <= first < 1 << 64:
+        raise ValueError(f"first must be an index, 0 or more, not {first}")
     e = _etype(x)
     matrix = x.dim() == 2
     if matrix:
@@ -694,7 +696,7 @@ def dropout(x, p, seed, step=0, residual=None, first=0, out=None):
     if D == 0:
         return out
     low = (1 << 64) - 1
-    rc = lib().elmo_dropout(x.data_ptr(), e, T, D, ld, _at(residual), ldr, p, seed & low, step & low, at, first & low,
+    rc = lib().elmo_dropout(x.data_ptr(), e, T, D, ld, _at(residual), ldr, p, seed & low, step & low, at, first,
                             out.data_ptr(), ldy, _stream_of(x.device))
     if rc:
         raise ElmoError("elmo_dropout", rc)

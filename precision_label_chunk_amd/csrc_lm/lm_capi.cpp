@@ -256,7 +256,8 @@ int elmo_dropout(const void* x, int type, int64_t T, int64_t D, int64_t ldx, con
   if (T < 0 || T >= (int64_t(1) << 31) || D < 1 || D >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (ldx < D || ldy < D || (residual && ldr < D) || (y == x && ldy != ldx) || (residual && y == residual && ldy != ldr))
     return ELMO_ESHAPE;
-  if (!(p >= 0.0 && p <= 1.0) || first + (uint64_t)(T * D) < first) return ELMO_EINVAL;
+  // (indices end below 2^64 - 7: blocks of 8 are counted by rounding up)
+  if (!(p >= 0.0 && p <= 1.0) || first > UINT64_MAX - 7 - (uint64_t)(T * D)) return ELMO_EINVAL;
   if (T == 0) return ELMO_OK;
   const size_t e = type_bytes(type);
   if (!x || !y || !aligned_to(x, e) || !aligned_to(y, e) || !aligned_to(residual, e) || !aligned_to(step_at, 8)) return ELMO_EINVAL;
