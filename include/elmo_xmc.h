@@ -350,15 +350,17 @@ int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int6
  * M = 0) and dlse [N] (nullable: of row_max + log_sum):
  *   G[n, v] = p_v (dlse - sum_j dlogp_j) + sum_{j : ids_j = v} dlogp_j;  dX = G W;  dW = G^T X.
  * row_max and log_sum are elmo_linear_logprobs' outputs for the same X and W. The vocabulary goes in pieces
- * of `chunk` labels (rounded up to a multiple of 256; 0: the library's choice, about 2^26 / N): a piece's logits
- * are computed again and G held in the workspace in X's type (for N <= 128 as the sum of two such numbers), the one
- * rounding below 32 bits, relative to each element; sums are binary32. A label given more than once receives the sum of its gradients, a negative
+ * of `chunk` labels (rounded up to a multiple of 256; 0: the library's choice, about 2^27 numbers of G, or 2^28 for N <=
+ * 128): a piece's logits are computed again and G held in the workspace, the one rounding below 32 bits, relative to each
+ * element: in X's type for a result of 16 bits, as the sum of two such numbers for a result in FP32, and for N <= 128; sums
+ * are binary32. A label given more than once receives the sum of its gradients, a negative
  * id none. A row of nothing but -inf logits has G = 0; an id >= V makes G NaN in the whole row.
  *   dX       [N, D] of type `dx_type` (any), dW [V, D] of type `dw_type`, 16-byte aligned rows at pitches lddx,
  *            lddw; either may be NULL. accumulate: dW is added to, in binary32, and rounded once.
  * Neither overlaps another argument (dW is written while W is read). In FP16 an element of G is also off by up to 2^-39
  * of the largest |dlse| + 2 sum |dlogp| of a row. Probabilities below 2^-126 count as 0.
  * N = 0 leaves dW zero (or as it is with accumulate). Results repeat bit for bit on one device.
+ * The workspace's size: need_dx, need_dw are 0 for a result that is not needed, 2 + its element type, or 1: any type.
  */
 size_t elmo_linear_logprobs_backward_workspace_bytes(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx,
                                                      int need_dw);

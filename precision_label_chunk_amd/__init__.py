@@ -579,8 +579,8 @@ def linear_logprobs_backward(X, W, ids, stats: LinearLogProbs, dlogp, dlse=None,
     """(dX [N, D], dW [V, D]) of linear_logprobs(X, W, ids) for the upstream gradients dlogp [N, M] and dlse
     [N] (of the log partition), from the forward's result `stats`; in X's and W's type, or in that of dx and
     dw (float32, bfloat16, float16) where given. accumulate=True adds to dw. One that is not needed is None.
-    `chunk` labels are taken at a time (0: the library's choice). See elmo_linear_logprobs_backward in
-    elmo_xmc.h."""
+    `chunk` labels are taken at a time (0: the library's choice). Above 128 rows the logits' gradient is rounded to 16 bits
+    on the way to a 16-bit result, and held to twice as many for a float32 one. See elmo_linear_logprobs_backward in elmo_xmc.h."""
     e, N, V, D, M, ldx, ldw = _linear(X, W, ids)
     dev = X.device
     if M and dlogp is None:
@@ -604,7 +604,8 @@ def linear_logprobs_backward(X, W, ids, stats: LinearLogProbs, dlogp, dlse=None,
         return t, _etype(t), _rows(name, t)[2]
     dx, xt, lddx = result("dx", dx, need_dx, X)
     dw, wt, lddw = result("dw", dw, need_dw, W)
-    need = lib().elmo_linear_logprobs_backward_workspace_bytes(N, V, D, M, chunk, need_dx, need_dw) if N else 0
+    need = lib().elmo_linear_logprobs_backward_workspace_bytes(N, V, D, M, chunk, 2 + xt if need_dx else 0,
+                                                               2 + wt if need_dw else 0) if N else 0
     workspace = _scratch(workspace, need, X)
     _chk("elmo_linear_logprobs_backward", lib().elmo_linear_logprobs_backward(
         X.data_ptr(), W.data_ptr(), e, N, V, D, ldx, ldw, _at(ids) if M else None, M, stats.row_max.data_ptr(),

@@ -13,7 +13,10 @@
 // keeps the digits of 1 - p). G is scaled by the largest given gradient: the constant gradient 1 / N of
 // a mean then is exactly 1, and in FP16 a power of two more keeps p down to 2^-38. Up to 128 rows G
 // is held as the sum of two 16-bit numbers, in rows n and N + n: few rows do not average their roundings, and
-// memory bounds such products. 4,096 x 131,072 x 768: 2.5 ms, 980 TFLOP/s over the three products.
+// memory bounds such products. Above that it is so where a result is FP32, whose own rounding does not hide that of
+// G; the products of that result take twice the operations. 4,096 x 131,072 x 768: 2.5 ms, 980 TFLOP/s over the three
+// products, with BF16 results (off by 1.9e-3 and 1.7e-3 of their norms, 1.7e-3 and 1.5e-3 with an exact G); 3.4 ms with
+// dW, 3.7 ms with dX in FP32 (2.6 and 2.5 from one number; off by 1.5e-6 for 9.4e-4).
 #include <cfloat>
 
 #include "tile_shapes.hpp"
@@ -440,7 +443,7 @@ struct ProductArgs {
   const char* W; int64_t ldw;
   const char* G; int64_t ldg;
   int64_t N, v0, v1, cols;                                 // cols: the piece's labels, a multiple of 256
-  int planes;
+  int w_planes, x_planes;                                  // 2: with both numbers of G, of which the second starts at row N
   int D, d_tiles, row_tiles;
   const float* inv;
   // dW: the tokens in w_slots runs of w_per; one run goes to the result, several to `wpart`
@@ -518,10 +521,10 @@ struct WeightJob : ProductArgs {
     const int64_t t0 = slot * w_per, left = N - t0, rows = left < w_per ? left : w_per;
     const int d0 = dt * S::M, v = vt * S::N;
     const int dc = D - d0 < S::M ? D - d0 : S::M;
-    // (two planes come with one run: X's rows with the first, then again with the second)
+    // (X's rows with the first number of G, then again with the second)
     const int stages = (int)((rows + 31) / 32);
     const char *x = X + t0 * ldx + 2 * d0, *g = G + t0 * ldg + 2 * (int64_t)v;
-    return {{x, ldx, rows, 2 * dc, stages, x}, {g, ldg, rows, 2 * S::N, stages, g + N * ldg}, planes * stages};
+    return {{x, ldx, rows, 2 * dc, stages, x}, {g, ldg, rows, 2 * S::N, stages, g + N * ldg}, w_planes * stages};
   }
   __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int dt, vt, slot;
@@ -548,12 +551,12 @@ struct FeatureJob : ProductArgs {
     const int64_t c0 = slot * x_per, n = (int64_t)nt * S::N;
     const int64_t left = cols - c0, len = left < x_per ? left : x_per;
     const int d0 = dt * S::M, dc = D - d0 < S::M ? D - d0 : S::M;
-    return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, planes * N - n, 0}, (int)(len / 32)};
+    return {{W + (v0 + c0) * ldw + 2 * d0, ldw, v1 - v0 - c0, 2 * dc}, {G + n * ldg + 2 * c0, ldg, x_planes * N - n, 0}, (int)(len / 32)};
   }
   __device__ __forceinline__ bool finish(int u, f32x16_t (&acc)[S::MF][S::NF], int wm, int wn, int lane, char* lds) const {
     int dt, nt, slot;
     place(u, dt, nt, slot);
-    const int64_t rows = planes * N;
+    const int64_t rows = x_planes * N;
     const OutArgs o = xpart ? OutArgs{xpart + slot * rows * D, D, T_F32_, !first} : dX;
     return store_tile<S>(o, acc, xpart ? 1.0f : *inv, (int64_t)nt * S::N + S::WN_ROWS * wn, rows, dt * S::M + S::WM_ROWS * wm, D, lane, lds);
   }
@@ -724,17 +727,20 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 // first: the gradient codes' pass has just read W (behind dW: 210 and 133 us). One run over all labels in one plane
 // needs no sum of dX and no launch for it (512 x 1,000 x 256, loss and gradient: 43 us against 46.5).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
-constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers
-LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw) {
+constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers for every result
+LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, ResultKind dx, ResultKind dw) {
+  const bool need_dx = dx != NO_RESULT, need_dw = dw != NO_RESULT;
   LinearGradLayout s{};
   const int cus = device_cus();
   const int64_t whole = ceil_div(V, 256);   // pieces are multiples of 256 labels
   if (chunk > V) chunk = V;
-  int64_t most = chunk > 0 ? ceil_div(chunk, 256) : (int64_t(1) << 27) / N / 256;
+  s.x_planes = N <= TWO_PLANES || dx == RESULT_32 ? 2 : 1;
+  s.w_planes = N <= TWO_PLANES || dw == RESULT_32 ? 2 : 1;
+  s.planes = (need_dx && s.x_planes == 2) || (need_dw && s.w_planes == 2) ? 2 : 1;
+  int64_t most = chunk > 0 ? ceil_div(chunk, 256) : (int64_t(1) << 27) / (N <= TWO_PLANES ? N : s.planes * N) / 256;
   most = most < 1 ? 1 : (most > whole ? whole : most);
   if (most > MAX_PIECE / 256) most = MAX_PIECE / 256;
-  s.planes = N <= TWO_PLANES ? 2 : 1;
-  const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most), x_rows = s.planes * N;
+  const int64_t wst = ceil_div(N, 32), fewest = ceil_div(whole, most), x_rows = s.x_planes * N;
   const double rd = (double)x_rows * D * 4e-6 / 5.0;       // us for dX's partial sums to memory
   double least = 0.0;
   const int64_t last = chunk > 0 || fewest == 1 ? fewest : fewest + 4;
@@ -758,16 +764,16 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
       if (k > 0 && N >= 1024 && n >= 16384) break;         // (the large shape's)
       int h, l;
       for (int64_t ws = 1; ws <= 16; ws *= 2) {
-        if (ws > 1 && (!need_dw || s.planes > 1 || ws * 2 > wst || wt * ws > most_units)) break;
+        if (ws > 1 && (!need_dw || N <= TWO_PLANES || ws * 2 > wst || wt * ws > most_units)) break;
         const double sum_w = ws > 1 ? 2.0 + (double)(ws + 1) * n * D * 4e-6 / 5.0 : 0.0;
-        const int64_t w_stages = s.planes * ceil_div(wst, ws);
+        const int64_t w_stages = s.w_planes * ceil_div(wst, ws);
         if (need_dw) {
           const double us = products_time(c, wt * ws, w_stages, 0, 0, false, cus, &h, &l) + sum_w;
           if (bw.us == 0.0 || us < bw.us) bw = Best{us, k, (int)ws};
         }
         for (const int64_t xs : {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 24, 32, 48, 64, 96, 128, 192, 256, 384, 512}) {
           if (xs > 1 && (!need_dx || xs * 4 > xst || xt * xs > most_units)) break;
-          const double sum_x = s.planes == 1 && used == 1 && xs == 1 ? 0.0 : 5.0 + (double)xs * (rd + 0.02) / (double)used;   // (the sum of the runs: a launch more)
+          const double sum_x = s.x_planes == 1 && used == 1 && xs == 1 ? 0.0 : 5.0 + (double)xs * (rd + 0.02) / (double)used;   // (the sum of the runs: a launch more)
           if (need_dx && ws == 1) {
             const double us = products_time(c, 0, 0, xt * xs, ceil_div(xst, xs), used > 1, cus, &h, &l) + sum_x;
             if (bx.us == 0.0 || us < bx.us) bx = Best{us, k, (int)xs};
@@ -782,13 +788,13 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
   s.x_slots = (int)ceil_div(s.piece < V ? s.piece : V, s.x_per);
   s.w_per = ceil_div(wst, s.w_slots) * 32;
   s.w_slots = (int)ceil_div(N, s.w_per);
-  s.sum_x = s.planes > 1 || s.x_slots > 1 || s.piece < V;
+  s.sum_x = s.x_planes > 1 || s.x_slots > 1 || s.piece < V;
   size_t at = 0;
   s.most = at; at += up256(256 * 8);
   s.inv = at; at += 256;
   s.coef = at; at += up256((size_t)N * 8);
   s.up = at; at += up256((size_t)N * (M > 0 ? M : 1) * 4);
-  s.G = at; at += up256((size_t)x_rows * s.piece * 2);
+  s.G = at; at += up256((size_t)s.planes * N * s.piece * 2);
   s.xpart = at; if (need_dx && s.sum_x) at += up256((size_t)s.x_slots * x_rows * D * 4);
   s.wpart = at; if (need_dw && s.w_slots > 1) at += up256((size_t)s.w_slots * s.piece * D * 4);
   s.total = at;
@@ -821,7 +827,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     if (hipGetLastError() != hipSuccess) return ELMO_EHIP_;
     ProductArgs p{};
     p.X = (const char*)c.X; p.ldx = 2 * c.ldx; p.W = (const char*)c.W; p.ldw = 2 * c.ldw; p.G = ws + s.G; p.ldg = 2 * s.piece;
-    p.planes = s.planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.inv = k.inv;
+    p.w_planes = s.w_planes; p.x_planes = s.x_planes; p.N = c.N; p.v0 = v0; p.v1 = v1; p.D = c.D; p.inv = k.inv;
     p.cols = ceil_div(v1 - v0, 32) * 32;                   // (G is zero behind the last label, up to its tile's end)
     p.w_slots = s.w_slots; p.w_per = s.w_per; p.wpart = (float*)(ws + s.wpart);
     p.dW = OutArgs{c.dW, c.lddw, c.dw_type, c.accumulate};
@@ -831,12 +837,12 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
       const ShapeCost& cost = SHAPES[number];
       ProductArgs q = p;
       q.d_tiles = (int)ceil_div(c.D, cost.size);
-      q.row_tiles = (int)ceil_div(s.planes * c.N, cost.size);
+      q.row_tiles = (int)ceil_div(s.x_planes * c.N, cost.size);
       q.w_units = dw ? (int)ceil_div(v1 - v0, cost.size) * q.d_tiles * q.w_slots : 0;
       q.x_units = dx ? q.row_tiles * q.d_tiles * q.x_slots : 0;
       const unsigned grid = blocks_for(number, (int64_t)q.w_units + q.x_units, cus);
       if ((int64_t)q.w_units + q.x_units <= grid) q.x_light = 1;   // a unit for each block
-      else products_time(cost, q.w_units, s.planes * ceil_div(s.w_per, 32), q.x_units, ceil_div(s.x_per, 32), s.piece < c.V, cus, &q.x_heavy, &q.x_light);
+      else products_time(cost, q.w_units, s.w_planes * ceil_div(s.w_per, 32), q.x_units, ceil_div(s.x_per, 32), s.piece < c.V, cus, &q.x_heavy, &q.x_light);
       with_shape(number, [&](auto shape) {
         typedef decltype(shape) S;
         hipLaunchKernelGGL((k_lin_products<Mul, S>), dim3(grid), dim3(S::THREADS), 0, st, q);
@@ -851,7 +857,7 @@ static int grad_as(const LinearGradCall& c, const LinearGradLayout& s, char* ws,
     // the runs of dW summed, and those of dX behind the last piece
     SumArgs w{}, x{};
     if (c.dW && p.w_slots > 1) w = SumArgs{p.wpart, p.cols * c.D, v0, v1 - v0, p.w_slots, c.D, p.dW};
-    if (c.dX && s.sum_x && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.planes * s.x_slots, c.D, p.dX};
+    if (c.dX && s.sum_x && v1 == c.V) x = SumArgs{p.xpart, c.N * c.D, 0, c.N, s.x_planes * s.x_slots, c.D, p.dX};
     const unsigned wb = w.rows ? sum_grid(w.rows, c.D) : 0, xb = x.rows ? sum_grid(x.rows, c.D) : 0;
     if (wb + xb == 0) continue;
     if (w.slots > 32 || x.slots > 32) hipLaunchKernelGGL(k_lin_sum<16>, dim3(wb + xb), dim3(1024), 0, st, w, x, (int)wb, (const float*)k.inv);

@@ -43,6 +43,14 @@ int check_linear(int type, int64_t N, int64_t V, int D, int64_t ldx, int64_t ldw
   return ELMO_OK;
 }
 
+elmo::ResultKind result_kind(const void* p, int type) { return !p ? elmo::NO_RESULT : type == ELMO_T_F32 ? elmo::RESULT_32 : elmo::RESULT_16; }
+// whether a result that is needed as the workspace's query says (0: not, 2 + its type, else in any type) may be
+// of a kind (one that is not needed: the first)
+bool may_be(int need, elmo::ResultKind kind) {
+  if (need == 0 || need == 2 + ELMO_T_BF16 || need == 2 + ELMO_T_F16) return kind == elmo::RESULT_16;
+  return need != 2 + ELMO_T_F32 || kind == elmo::RESULT_32;
+}
+
 int check_i8(int64_t N, int64_t L, int D) {
   if (N < 0 || N >= (int64_t(1) << 31) || L < 1 || L >= (int64_t(1) << 31)) return ELMO_ESHAPE;
   if (D < 64 || D % 64 != 0 || D > ELMO_MAX_I8_D) return ELMO_ESHAPE;
@@ -190,7 +198,15 @@ int elmo_linear_logprobs(const void* X, const void* W, int type, int64_t N, int6
 size_t elmo_linear_logprobs_backward_workspace_bytes(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx,
                                                      int need_dw) {
   if (N < 1 || chunk < 0 || check_linear(ELMO_T_BF16, N, V, D, D, D, M) != ELMO_OK) return 0;
-  return elmo::linear_grad_layout(N, V, D, M, chunk, need_dx, need_dw).total;
+  // a type that is not told: the largest workspace of any
+  size_t most = 0;
+  for (const elmo::ResultKind dx : {elmo::RESULT_16, elmo::RESULT_32})
+    for (const elmo::ResultKind dw : {elmo::RESULT_16, elmo::RESULT_32}) {
+      if (!may_be(need_dx, dx) || !may_be(need_dw, dw)) continue;
+      const size_t total = elmo::linear_grad_layout(N, V, D, M, chunk, need_dx ? dx : elmo::NO_RESULT, need_dw ? dw : elmo::NO_RESULT).total;
+      most = total > most ? total : most;
+    }
+  return most;
 }
 
 int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_t N, int64_t V, int D, int64_t ldx,
@@ -211,7 +227,7 @@ int elmo_linear_logprobs_backward(const void* X, const void* W, int type, int64_
   for (const void* p : {(const void*)ids, (const void*)dlogp, (const void*)row_max, (const void*)log_sum, (const void*)dlse})
     if (!aligned_to(p, 4)) return ELMO_EINVAL;
   if (!workspace || !aligned16(workspace)) return ELMO_EWORKSPACE;
-  const elmo::LinearGradLayout s = elmo::linear_grad_layout(N, V, D, M, chunk, dX != nullptr, dW != nullptr);
+  const elmo::LinearGradLayout s = elmo::linear_grad_layout(N, V, D, M, chunk, result_kind(dX, dx_type), result_kind(dW, dw_type));
   if (workspace_bytes < s.total) return ELMO_EWORKSPACE;
   elmo::LinearGradCall c{};
   c.X = X; c.W = W; c.type = type; c.N = N; c.V = V; c.D = D; c.ldx = ldx; c.ldw = ldw; c.ids = ids; c.M = M;

@@ -49,7 +49,7 @@ struct LinearGradLayout {
   int64_t piece, x_per, w_per;                             // labels per piece; labels / tokens per run
   int x_slots, w_slots;                                    // runs
   int logits, w_shape, x_shape;                            // tile shapes of the logits, of dW and of dX
-  int planes;                                              // 16-bit numbers whose sum holds an element of G
+  int planes, w_planes, x_planes;                          // 16-bit numbers whose sum holds an element of G; those that dW and dX take
   bool sum_x;                                              // dX is the sum of several runs, pieces or planes
   size_t most, inv, coef, up, G, xpart, wpart, total;
 };
@@ -60,7 +60,8 @@ struct LinearGradCall {
   void* dX; int dx_type; int64_t lddx;
   void* dW; int dw_type; int64_t lddw; int accumulate;
 };
-LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, int need_dx, int need_dw);
+enum ResultKind { NO_RESULT, RESULT_16, RESULT_32 };       // by its element type's bits
+LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, ResultKind dx, ResultKind dw);
 int run_zero_rows(void* out, int type, int64_t rows, int D, int64_t ld, hipStream_t st);
 int run_linear_logprobs_grad(const LinearGradCall& c, const LinearGradLayout& s, void* workspace, hipStream_t st);
 
