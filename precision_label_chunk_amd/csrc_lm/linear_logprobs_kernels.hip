@@ -725,7 +725,10 @@ static double products_time(const ShapeCost& c, int64_t w_units, int64_t w_stage
 // products share a launch, or each has its own with its own shape (few rows, where memory bounds them: dW in the large
 // shape, dX in the medium one take 156 us at 2 x 365,721 x 576, one launch 217; 93 and 139 at 64 x 131,072 x 768). dX goes
 // first: the gradient codes' pass has just read W (behind dW: 210 and 133 us). One run over all labels in one plane
-// needs no sum of dX and no launch for it (512 x 1,000 x 256, loss and gradient: 43 us against 46.5).
+// needs no sum of dX and no launch for it (512 x 1,000 x 256, loss and gradient: 43 us against 46.5). The small shapes
+// are tried at every size: with the large one alone from 1,024 rows and 16,384 labels on, gradients of few features take
+// longer (4,096 x 32,003 x 64 191 us against 162, 2,698 x 120,686 x 128 551 against 507; of 114 sizes two were shorter so, by 5 and 8%
+// at 320 features, and those of 768 and more did not change).
 constexpr int64_t MAX_PIECE = (1 << 22) - 256;             // labels: 256 rows of G stay within 2^31 bytes
 constexpr int64_t TWO_PLANES = 128;                        // rows up to which G is held as two numbers for every result
 LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t chunk, ResultKind dx, ResultKind dw) {
@@ -761,7 +764,6 @@ LinearGradLayout linear_grad_layout(int64_t N, int64_t V, int D, int M, int64_t 
       const ShapeCost& c = SHAPES[k];
       const int64_t dt = ceil_div(D, c.size), wt = need_dw ? ceil_div(n, c.size) * dt : 0, xt = need_dx ? ceil_div(x_rows, c.size) * dt : 0;
       const int64_t most_units = 2 * (int64_t)cus * c.blocks;
-      if (k > 0 && N >= 1024 && n >= 16384) break;         // (the large shape's)
       int h, l;
       for (int64_t ws = 1; ws <= 16; ws *= 2) {
         if (ws > 1 && (!need_dw || N <= TWO_PLANES || ws * 2 > wst || wt * ws > most_units)) break;
