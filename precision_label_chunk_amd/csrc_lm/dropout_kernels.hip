@@ -29,12 +29,6 @@ __device__ __forceinline__ void drop8(const DropArgs& a, uint64_t step, const fl
   }
 }
 
-template <typename E>
-__device__ __forceinline__ void get8(const typename E::raw* p, float* f) {
-#pragma unroll
-  for (int h = 0; h < 8 / E::VEC; ++h) E::widen(*(const i32x4_t*)(p + h * E::VEC), f + h * E::VEC);
-}
-
 // Rows whose 8-element vectors are blocks of the generator and 16-byte aligned (one long row where the
 // tensors have no gaps). D8 = whole vectors of a row; what is left of the last row (below 8) goes to the
 // first thread behind them.
@@ -46,8 +40,8 @@ __global__ __launch_bounds__(256) void k_dropout_rows(DropArgs a) {
   for (int64_t i = blockIdx.x * (int64_t)256 + threadIdx.x; i < n8; i += (int64_t)gridDim.x * 256) {
     const int64_t t = a.T == 1 ? 0 : i / d8, d = (i - t * d8) * 8;
     float x[8], r[8], y[8];
-    get8<E>((const raw*)a.x + t * a.ldx + d, x);
-    if constexpr (RES) get8<E>((const raw*)a.r + t * a.ldr + d, r);
+    load_vec8<E>((const raw*)a.x + t * a.ldx + d, x);
+    if constexpr (RES) load_vec8<E>((const raw*)a.r + t * a.ldr + d, r);
     drop8<E, RES>(a, step, x, r, (a.first + (uint64_t)(t * a.D + d)) >> 3, y);
     raw* p = (raw*)a.y + t * a.ldy + d;
 #pragma unroll

@@ -66,4 +66,11 @@ struct ElemF16 {
   }
 };
 
+// eight elements, 16-byte aligned
+template <typename E>
+__device__ __forceinline__ void load_vec8(const typename E::raw* p, float* f) {
+#pragma unroll
+  for (int h = 0; h < 8 / E::VEC; ++h) E::widen(*(const i32x4_t*)(p + h * E::VEC), f + h * E::VEC);
+}
+
 }  // namespace elmo

@@ -28,11 +28,6 @@ __device__ __forceinline__ int quantise(float x, float inv, float top) {
 
 // A row per group of G threads (a wave, or the block); a thread's first VECS vectors of 8 elements stay in
 // registers between the maximum and the codes, the rest is read again. 16,384 x 4,096 BF16: 43 us, 4.7 TB/s.
-template <typename E>
-__device__ __forceinline__ void load8(const typename E::raw* p, float* f) {
-#pragma unroll
-  for (int h = 0; h < 8 / E::VEC; ++h) E::widen(*(const i32x4_t*)(p + h * E::VEC), f + h * E::VEC);
-}
 template <typename E, int G>
 __global__ __launch_bounds__(256) void k_i8_quantize(const typename E::raw* x, int64_t N, int D, int64_t ldx, int8_t* codes, float* scales) {
   constexpr int VECS = 4;
@@ -56,13 +51,13 @@ __global__ __launch_bounds__(256) void k_i8_quantize(const typename E::raw* x, i
   for (int v = 0; v < VECS; ++v) {
     const int d = (v * G + lane) * 8;
     if (d < D) {
-      load8<E>(row + d, f[v]);
+      load_vec8<E>(row + d, f[v]);
       see(f[v]);
     }
   }
   for (int d = (VECS * G + lane) * 8; d < D; d += G * 8) {
     float g[8];
-    load8<E>(row + d, g);
+    load_vec8<E>(row + d, g);
     see(g);
   }
   if (bad) top = __builtin_inff();
@@ -95,7 +90,7 @@ __global__ __launch_bounds__(256) void k_i8_quantize(const typename E::raw* x, i
   }
   for (int d = (VECS * G + lane) * 8; d < D; d += G * 8) {
     float g[8];
-    load8<E>(row + d, g);
+    load_vec8<E>(row + d, g);
     put(d, g);
   }
   if (lane == 0) scales[n] = none ? __builtin_nanf("") : top / 127.0f;
