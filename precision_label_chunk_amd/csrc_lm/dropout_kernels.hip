@@ -30,8 +30,8 @@ __device__ __forceinline__ void drop8(const DropArgs& a, uint64_t step, const fl
 }
 
 // Rows whose 8-element vectors are blocks of the generator and 16-byte aligned (one long row where the
-// tensors have no gaps). D8 = whole vectors of a row; what is left of the last row (below 8) goes to the
-// first thread behind them.
+// tensors have no gaps). d8 = whole vectors of a row; what is left of the last row (below 8) is taken by the grid's
+// first thread beside its own vectors.
 template <typename E, bool RES>
 __global__ __launch_bounds__(256) void k_dropout_rows(DropArgs a) {
   typedef typename E::raw raw;
